@@ -19,7 +19,9 @@ import numpy as np
 __all__ = ["Varlen", "GDNShape", "FlareError", "lib", "gdn_dual_fwd", "gdn_dual_fwd_pool", "gdn_dual_fwd_route1", "gdn_dual_bwd",
            "gdn_dual_fwd_conv", "block_step", "block_step_conv", "conv_cache_fill", "gdn_verify", "gdn_scatter", "gdn_verify_outputs", "gdn_commit_prefix", "shortconv_dual", "shortconv_dual_bwd", "shortconv_dual_bwd_workspace_bytes", "qkv_prologue",
            "qkv_prologue_bwd", "qkv_prologue_bwd_workspace_bytes", "chunk_size", "ckpt_slots", "EVAL", "COMMIT",
-           "QK_L2NORM", "F32", "BF16"]
+           "QK_L2NORM", "F32", "BF16",
+           "gated_norm", "gated_norm_bwd", "residual_norm", "residual_norm_bwd", "rotary_frequencies", "rotary",
+           "rotary_cache", "step_tables", "block_attention", "LINEAR", "SILU", "SIGMOID"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflare_gdn.so")
@@ -129,6 +131,7 @@ def lib():
     L.flare_timing_avg_ms.restype = ctypes.c_double
     L.flare_timing_reset.argtypes = []
     L.flare_timing_reset.restype = None
+    _layer_declare(L)
     _lib = L
     return L
 
@@ -909,3 +912,12 @@ def timing_avg_ms(kernel: str):
 
 def timing_reset() -> None:
     lib().flare_timing_reset()
+
+
+# the operators around the GDN step
+from .layer import (LINEAR, SIGMOID, SILU, TABLES_BAD_LENGTH, TABLES_NO_PAGES, TABLES_OK,  # noqa: E402
+                    TABLES_TOO_LONG, TABLES_TOO_MANY_TOKENS, AttentionShape, RotaryShape, block_attention,
+                    block_attention_workspace_bytes, gated_norm, gated_norm_bwd, gated_norm_bwd_workspace_bytes,
+                    residual_norm, residual_norm_bwd, residual_norm_bwd_workspace_bytes, rotary, rotary_cache,
+                    rotary_frequencies, step_tables)
+from .layer import declare as _layer_declare  # noqa: E402

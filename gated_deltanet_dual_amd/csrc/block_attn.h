@@ -1,0 +1,32 @@
+// block_attn.h -- how a block attention is cut into parts (host and device;
+// no HIP types, so that the workspace size can be told and tested without a GPU).
+#pragma once
+
+#include "layer_ops.h"
+
+#ifdef __HIPCC__
+#define FLARE_HD __host__ __device__ inline
+#else
+#define FLARE_HD inline
+#endif
+
+namespace flare {
+
+struct AttnPlan {
+  int tiles;       // 16-row query tiles of a workgroup
+  int page_shift;
+  int prefix_parts, prefix_chunk, prefix_groups;  // parts of the prefix, keys a part, row groups
+  int own_parts, own_chunk, own_groups;
+  int64_t prefix_blocks, own_blocks;
+};
+
+// A request's own keys: never more than its table or the caller's bound holds.
+FLARE_HD int attn_own_len(const BlockAttnArgs &a, int32_t len) {
+  const int most = a.max_seq_len;
+  return len < 0 ? 0 : len > most ? most : len;
+}
+
+// a.max_seq_len <= max_pages * page
+AttnPlan attn_plan(const BlockAttnArgs &a);
+
+}  // namespace flare

@@ -1,0 +1,192 @@
+// host_layer.cpp -- validation of the operators around the GDN step before any
+// launch, how they are cut into work, and the workspace sizes that follow.
+// Pure C++.
+#include "block_attn.h"
+#include "host_plan.h"
+
+namespace flare {
+
+namespace {
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+}  // namespace
+
+AttnPlan attn_plan(const BlockAttnArgs &a) {
+  AttnPlan p{};
+  while ((1 << p.page_shift) < a.page) ++p.page_shift;
+  const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
+  const int64_t all_rows = rows * a.num_req;
+  p.tiles = rows <= 16 && (a.prefix_len == 0 || all_rows <= 16) ? 1 : 2;
+  const int per = 16 * p.tiles;
+  p.own_groups = (int)ceil_div(rows, per);
+  p.prefix_groups = (int)ceil_div(all_rows, per);
+  // parts short enough that the launch fills the chip, of 128 to 4096 keys
+  // (a wave keeps the pages of its subtiles in its lanes: 64 of 16 keys)
+  auto cut = [](int64_t len, int64_t units, int *chunk, int *parts) {
+    int64_t c = 4096;
+    while (c > 128 && units * ceil_div(len, c) < 1024) c /= 2;
+    *chunk = (int)c;
+    *parts = (int)ceil_div(len, c);
+  };
+  cut(a.prefix_len, (int64_t)p.prefix_groups * a.kv_heads, &p.prefix_chunk, &p.prefix_parts);
+  cut(a.max_seq_len, (int64_t)p.own_groups * a.kv_heads * a.num_req, &p.own_chunk, &p.own_parts);
+  if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
+  p.prefix_blocks = (int64_t)p.prefix_parts * p.prefix_groups * a.kv_heads;
+  p.own_blocks = (int64_t)p.own_parts * p.own_groups * a.kv_heads * a.num_req;
+  return p;
+}
+
+
+int norm_bwd_blocks(int64_t rows) { return (int)(rows < kNormBwdBlocks ? rows : kNormBwdBlocks); }
+
+size_t norm_bwd_workspace_bytes(int64_t rows, int32_t dim, int weights) {
+  return (size_t)norm_bwd_blocks(rows) * dim * weights * sizeof(float) + 256;
+}
+
+flare_status check_io(int32_t io_dtype) {
+  if (io_dtype != FLARE_F32 && io_dtype != FLARE_BF16)
+    return fail(FLARE_ERR_UNSUPPORTED, "io_dtype %d unknown", io_dtype);
+  return FLARE_OK;
+}
+
+flare_status check_gate(const void *gate, int32_t activation, int64_t stride, int64_t row) {
+  if (!gate) return FLARE_OK;
+  if (activation != FLARE_GATE_LINEAR && activation != FLARE_GATE_SILU && activation != FLARE_GATE_SIGMOID)
+    return fail(FLARE_ERR_UNSUPPORTED, "gate activation %d unknown", activation);
+  if (stride < row) return fail(FLARE_ERR_SHAPE, "gate_stride %lld below a row of %lld", (long long)stride, (long long)row);
+  return FLARE_OK;
+}
+
+static flare_status check_norm_rows(int64_t rows, int32_t dim, int64_t x_stride, int64_t row) {
+  if (dim < 1) return fail(FLARE_ERR_SHAPE, "dim must be positive");
+  if (dim > 16384) return fail(FLARE_ERR_UNSUPPORTED, "dim %d, at most 16384", dim);
+  if (rows > INT32_MAX) return fail(FLARE_ERR_UNSUPPORTED, "%lld rows, at most 2^31 - 1", (long long)rows);
+  if (x_stride < row) return fail(FLARE_ERR_SHAPE, "x_stride %lld below a row of %lld", (long long)x_stride, (long long)row);
+  return FLARE_OK;
+}
+
+flare_status check_gated_norm(int64_t tokens, int32_t heads, int32_t dim, int32_t io_dtype, const void *x,
+                              int64_t x_stride, const void *gate, int64_t gate_stride, const float *weight,
+                              int32_t activation) {
+  if (tokens < 0 || heads < 1) return fail(FLARE_ERR_SHAPE, "tokens must not be negative, heads positive");
+  if (tokens > INT32_MAX) return fail(FLARE_ERR_UNSUPPORTED, "too many tokens");
+  const int64_t row = (int64_t)heads * (dim > 0 ? dim : 0);
+  flare_status st = check_io(io_dtype);
+  if (st != FLARE_OK) return st;
+  st = check_norm_rows(tokens * heads, dim, x_stride, row);
+  if (st != FLARE_OK) return st;
+  st = check_gate(gate, activation, gate_stride, row);
+  if (st != FLARE_OK) return st;
+  if (tokens > 0 && (!x || !weight)) return fail(FLARE_ERR_NULL, "gated_norm: a required pointer is NULL");
+  return FLARE_OK;
+}
+
+flare_status check_residual_norm(int64_t tokens, int32_t dim, int32_t io_dtype, int32_t res_dtype, const void *x,
+                                 int64_t x_stride, const void *residual, const void *gate, int64_t gate_stride,
+                                 const float *w_pre, int32_t activation) {
+  if (tokens < 0) return fail(FLARE_ERR_SHAPE, "tokens must not be negative");
+  flare_status st = check_io(io_dtype);
+  if (st == FLARE_OK) st = check_io(res_dtype);
+  if (st != FLARE_OK) return st;
+  if (res_dtype == FLARE_BF16 && io_dtype != FLARE_BF16)
+    return fail(FLARE_ERR_UNSUPPORTED, "a bf16 residual goes with bf16 io");
+  st = check_norm_rows(tokens, dim, x_stride, dim);
+  if (st != FLARE_OK) return st;
+  st = check_gate(gate, activation, gate_stride, dim);
+  if (st != FLARE_OK) return st;
+  if (tokens > 0 && (!x || !residual || !w_pre))
+    return fail(FLARE_ERR_NULL, "residual_norm: a required pointer is NULL");
+  return FLARE_OK;
+}
+
+flare_status check_workspace(const void *workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need)
+    return fail(FLARE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? bytes : (size_t)0, need);
+  if (((uintptr_t)workspace & 255u) != 0) return fail(FLARE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  return FLARE_OK;
+}
+
+flare_status check_rotary(int64_t tokens, const flare_rotary_shape *s, const int32_t *positions, const double *freqs,
+                          const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_out) {
+  if (!s) return fail(FLARE_ERR_NULL, "rotary: shape is NULL");
+  if (tokens < 0 || s->q_heads < 1 || s->k_heads < 0 || s->dim < 1 || s->half < 0)
+    return fail(FLARE_ERR_SHAPE, "rotary: negative sizes, or no q heads or channels");
+  if (tokens > INT32_MAX) return fail(FLARE_ERR_UNSUPPORTED, "rotary: too many tokens");
+  if (s->dim > 1024) return fail(FLARE_ERR_UNSUPPORTED, "rotary: dim %d, at most 1024", s->dim);
+  if (s->q_heads > 65536 || s->k_heads > 65536) return fail(FLARE_ERR_UNSUPPORTED, "rotary: at most 65536 heads");
+  if (2 * s->half > s->dim)
+    return fail(FLARE_ERR_SHAPE, "rotary: 2 * half = %d beyond the head's %d channels", 2 * s->half, s->dim);
+  if (s->interleaved != 0 && s->interleaved != 1)
+    return fail(FLARE_ERR_UNSUPPORTED, "rotary: interleaved %d unknown", s->interleaved);
+  flare_status st = check_io(s->io_dtype);
+  if (st != FLARE_OK) return st;
+  if (q_stride < (int64_t)s->q_heads * s->dim || (s->k_heads > 0 && k_stride < (int64_t)s->k_heads * s->dim))
+    return fail(FLARE_ERR_SHAPE, "rotary: a token stride is below a row");
+  if (tokens > 0 && (!positions || (s->half > 0 && !freqs) || !q || !q_out || (s->k_heads > 0 && !k)))
+    return fail(FLARE_ERR_NULL, "rotary: a required pointer is NULL");
+  return FLARE_OK;
+}
+
+flare_status check_step_tables(const StepTablesArgs &a) {
+  if (a.num_req < 0 || a.max_pages < 0 || a.num_free < 0 || a.max_tokens < 0 || a.position_offset < 0)
+    return fail(FLARE_ERR_SHAPE, "step_tables: a negative size");
+  if (a.page < 1) return fail(FLARE_ERR_SHAPE, "step_tables: page must be positive");
+  if (a.num_req > kTablesMaxReq)
+    return fail(FLARE_ERR_UNSUPPORTED, "step_tables: %d requests, at most %d", a.num_req, kTablesMaxReq);
+  if (a.num_free > INT32_MAX || a.max_tokens > INT32_MAX)
+    return fail(FLARE_ERR_UNSUPPORTED, "step_tables: at most 2^31 - 1 free pages and tokens");
+  if (!a.pages_used || !a.pages_used_out || !a.status || !a.cu_new ||
+      (a.num_req > 0 && (!a.seq_lens || !a.new_lens || !a.seq_lens_out)) || (a.num_req > 0 && a.max_pages > 0 && !a.block_table) ||
+      (a.num_free > 0 && !a.free_pages) || (a.max_tokens > 0 && (!a.positions || !a.slots)))
+    return fail(FLARE_ERR_NULL, "step_tables: a required pointer is NULL");
+  if (a.pages_used == a.pages_used_out || (a.num_req > 0 && a.seq_lens == a.seq_lens_out))
+    return fail(FLARE_ERR_SHAPE, "step_tables: an output is the memory of its input");
+  return FLARE_OK;
+}
+
+flare_status check_attention_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
+                                   int32_t prefix_len) {
+  if (!s) return fail(FLARE_ERR_NULL, "block_attention: shape is NULL");
+  if (num_req < 0 || max_seq_len < 0 || prefix_len < 0) return fail(FLARE_ERR_SHAPE, "block_attention: a negative size");
+  if (s->block < 1 || s->q_heads < 1 || s->kv_heads < 1)
+    return fail(FLARE_ERR_SHAPE, "block_attention: block and heads must be positive");
+  if (s->q_heads % s->kv_heads != 0)
+    return fail(FLARE_ERR_SHAPE, "block_attention: %d q heads are no multiple of %d kv heads", s->q_heads, s->kv_heads);
+  if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: head dim %d not instantiated (64, 128, 256)", s->head_dim);
+  if (s->page < 16 || (s->page & (s->page - 1)) != 0)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: page %d is no power of two of at least 16", s->page);
+  if (s->io_dtype != FLARE_BF16) return fail(FLARE_ERR_UNSUPPORTED, "block_attention: bf16 only");
+  if (s->causal != 0 && s->causal != 1) return fail(FLARE_ERR_UNSUPPORTED, "block_attention: causal %d unknown", s->causal);
+  // keys are counted in 32 bits, with room for a tile past the end
+  if (max_seq_len > INT32_MAX - 8192 || prefix_len > INT32_MAX - 8192)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: at most 2^31 - 8193 keys");
+  if ((int64_t)num_req * s->block > INT32_MAX / 64 / s->q_heads)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: num_req * block * q_heads beyond 2^25");
+  return FLARE_OK;
+}
+
+BlockAttnArgs attention_args(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
+                             int32_t prefix_len) {
+  BlockAttnArgs a{};
+  a.num_req = num_req;
+  a.block = s->block;
+  a.q_heads = s->q_heads;
+  a.kv_heads = s->kv_heads;
+  a.dim = s->head_dim;
+  a.page = s->page;
+  a.causal = s->causal;
+  a.prefix_len = prefix_len;
+  a.max_seq_len = max_seq_len;
+  a.scale = s->scale > 0.0f ? s->scale : 1.0f / __builtin_sqrtf((float)s->head_dim);
+  return a;
+}
+
+size_t block_attention_workspace_bytes(const BlockAttnArgs &a) {
+  if (a.num_req == 0) return 0;
+  const AttnPlan p = attn_plan(a);
+  const int64_t parts = (int64_t)p.prefix_parts + p.own_parts;
+  if (parts <= 1) return 0;
+  return (size_t)parts * a.num_req * a.block * a.q_heads * (a.dim + 2) * sizeof(float) + 256;
+}
+
+}  // namespace flare

@@ -560,6 +560,203 @@ flare_status flare_qkv_prologue_bwd_noalloc(const flare_varlen *varlen,
                                             float *const dweight[3],
                                             void *stream);
 
+/* ---- the operators around the GDN step -----------------------------------
+ * A hybrid layer (Overall framework: GDN layers beside softmax layers, whose
+ * serving keeps a causal cache that denoising forwards only read) needs these
+ * next to the entry points above.  io: FLARE_F32 or FLARE_BF16; weights, gates'
+ * arithmetic, statistics and sums are fp32.  Token strides count elements; the
+ * last dimensions are contiguous.  Rows of any width and alignment are taken;
+ * 16-byte aligned rows whose width is a multiple of 16 bytes are moved 16 bytes
+ * at a time. */
+
+/* What a gate g is turned into before it multiplies. */
+enum { FLARE_GATE_LINEAR = 0, FLARE_GATE_SILU = 1, FLARE_GATE_SIGMOID = 2 };
+
+/* The norm behind a block with its gate, per (token, head) row of `dim`:
+ *   y = x / sqrt(mean x^2 + eps) * weight * act(gate)
+ * (the output norm of a GDN layer; with heads = 1 and no gate a plain RMS norm).
+ *   x, gate   io [tokens, heads, dim], x_stride / gate_stride elements between
+ *             tokens (heads * dim when packed; a slice of a fused projection
+ *             has more).  gate NULL: no gate, activation is ignored
+ *   weight    fp32 [dim]
+ *   y         io [tokens, heads, dim], packed
+ *   rstd      fp32 [tokens, heads] 1 / sqrt(mean x^2 + eps) for the reverse
+ *             mode, or NULL
+ * 1 <= dim <= 16384; tokens * heads < 2^31. */
+flare_status flare_gated_norm(int64_t tokens, int32_t heads, int32_t dim,
+                              int32_t io_dtype, const void *x, int64_t x_stride,
+                              const void *gate, int64_t gate_stride,
+                              const float *weight, int32_t activation,
+                              float eps, void *y, float *rstd, void *stream);
+
+/* Reverse mode: the forward's inputs and its rstd, dy io [tokens, heads, dim]
+ * with dy_stride elements between tokens; writes dx, dgate (packed; dgate NULL
+ * without a gate) and dweight fp32 [dim].  workspace: 256-byte aligned,
+ * flare_gated_norm_bwd_workspace_size bytes (partial weight sums, added in a
+ * fixed order: results are run-to-run identical). */
+size_t flare_gated_norm_bwd_workspace_size(int64_t tokens, int32_t heads,
+                                           int32_t dim);
+flare_status flare_gated_norm_bwd(int64_t tokens, int32_t heads, int32_t dim,
+                                  int32_t io_dtype, const void *x,
+                                  int64_t x_stride, const void *gate,
+                                  int64_t gate_stride, const float *weight,
+                                  int32_t activation, const float *rstd,
+                                  const void *dy, int64_t dy_stride, void *dx,
+                                  void *dgate, float *dweight, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Everything between two blocks in one pass: the norm behind the block, its
+ * gate, the residual with its scale, and the norm before the next block:
+ *   n = x / sqrt(mean x^2 + eps) * w_post        (n = x when w_post is NULL)
+ *   h = residual + scale * act(gate) * n
+ *   y = h / sqrt(mean h^2 + eps) * w_pre
+ * y is of h before h is rounded to its own type.
+ *   x, gate    io [tokens, dim] with token strides; gate NULL: no gate
+ *   residual   res_dtype [tokens, dim] packed: fp32, or bf16 with bf16 io
+ *   w_pre, w_post, scale  fp32 [dim]; w_post and scale may be NULL
+ *   h          res_dtype [tokens, dim];  y  io [tokens, dim]
+ *   rstd       fp32 [tokens, 2]: 1 / sqrt of the post and the pre norm, or NULL
+ * 1 <= dim <= 16384; tokens < 2^31. */
+flare_status flare_residual_norm(int64_t tokens, int32_t dim, int32_t io_dtype,
+                                 int32_t res_dtype, const void *x,
+                                 int64_t x_stride, const void *residual,
+                                 const void *gate, int64_t gate_stride,
+                                 const float *w_pre, const float *w_post,
+                                 const float *scale, int32_t activation,
+                                 float eps, void *h, void *y, float *rstd,
+                                 void *stream);
+
+/* Reverse mode: the forward's inputs and rstd, dy io and dh res_dtype
+ * [tokens, dim] packed (the gradients of y and h; dh NULL = 0); writes dx io,
+ * dresidual res_dtype, dgate io (NULL without a gate), dw_pre, and dw_post and
+ * dscale where the forward had them (else NULL), all fp32 [dim].  workspace as
+ * for flare_gated_norm_bwd. */
+size_t flare_residual_norm_bwd_workspace_size(int64_t tokens, int32_t dim);
+flare_status flare_residual_norm_bwd(
+    int64_t tokens, int32_t dim, int32_t io_dtype, int32_t res_dtype,
+    const void *x, int64_t x_stride, const void *residual, const void *gate,
+    int64_t gate_stride, const float *w_pre, const float *w_post,
+    const float *scale, int32_t activation, const float *rstd, const void *dy,
+    const void *dh, void *dx, void *dresidual, void *dgate, float *dw_pre,
+    float *dw_post, float *dscale, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/* Rotary positions on the first 2 * half channels of every head:
+ *   (a, b) -> mscale * (a cos - b sin, a sin + b cos),  angle = position * freq
+ * over the pairs (i, half + i), or (2i, 2i + 1) when interleaved; the channels
+ * behind pass through unchanged (not scaled).  Angles are reduced in 64 bits.
+ * inverse = 1 turns by the negative angle: the reverse mode, applied to the
+ * outputs' gradients.
+ *   positions  int32 [tokens]
+ *   freqs      fp64 [half], radians a position (a scaled context scales these
+ *              and mscale)
+ *   q, k       io [tokens, q_heads / k_heads, dim] with token strides;
+ *              k_heads = 0: q alone
+ *   q_out, k_out  packed
+ * Requirements: 0 <= 2 * half <= dim <= 1024. */
+typedef struct {
+  int32_t q_heads, k_heads, dim, half;
+  int32_t io_dtype;
+  int32_t interleaved;
+  float mscale;
+} flare_rotary_shape;
+flare_status flare_rotary(int64_t tokens, const flare_rotary_shape *shape,
+                          const int32_t *positions, const double *freqs,
+                          const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, int32_t inverse, void *q_out,
+                          void *k_out, void *stream);
+
+/* The serving form: q turned to q_out, k turned and v copied into the pages of
+ * the cache, row t at slots[t] = page id * page + offset in the page.
+ *   slots      int64 [tokens]; a slot outside [0, num_pages * page) (a padded
+ *              row's -1) writes nothing; live slots are distinct
+ *   k_cache, v_cache  io [num_pages, k_heads, page, dim] */
+flare_status flare_rotary_cache(int64_t tokens, const flare_rotary_shape *shape,
+                                const int32_t *positions, const double *freqs,
+                                const void *q, int64_t q_stride, const void *k,
+                                int64_t k_stride, const void *v,
+                                int64_t v_stride, const int64_t *slots,
+                                void *q_out, void *k_cache, void *v_cache,
+                                int64_t num_pages, int32_t page, void *stream);
+
+/* The tables of a serving step, from lengths that stay on the device.  Request
+ * r holds seq_lens[r] tokens in the cache and adds new_lens[r]; its pages are
+ * block_table[r][0 .. ceil(seq_lens[r] / page)).  The pages it opens are taken,
+ * in request order, from free_pages[*pages_used] on and entered into its row.
+ *   cu_new     int32 [num_req + 1]  offsets of the requests' new tokens
+ *   positions  int32 [max_tokens]   position_offset (a shared prefix) + the
+ *              token's position in its request
+ *   slots      int64 [max_tokens]   page id * page + offset, for
+ *              flare_rotary_cache
+ *   seq_lens_out int32 [num_req]    seq_lens + new_lens
+ *   pages_used_out int32 [1]
+ *   status     int32 [1] device: FLARE_TABLES_OK, or why nothing was allocated:
+ *              then cu_new is all zero, every slot is -1, and the table, the
+ *              lengths and pages_used are unchanged
+ * Rows behind the last new token get position 0 and slot -1.  pages_used,
+ * seq_lens and their _out buffers must not be the same memory.
+ * num_req <= 8192; any page >= 1. */
+enum {
+  FLARE_TABLES_OK = 0,
+  FLARE_TABLES_NO_PAGES = 1,        /* fewer free pages than are opened        */
+  FLARE_TABLES_TOO_MANY_TOKENS = 2, /* more new tokens than max_tokens         */
+  FLARE_TABLES_TOO_LONG = 3,        /* a request outgrows max_pages or int32   */
+  FLARE_TABLES_BAD_LENGTH = 4       /* a negative length or pages_used         */
+};
+flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens,
+                               const int32_t *new_lens, int32_t *block_table,
+                               int32_t max_pages, const int32_t *free_pages,
+                               int64_t num_free, const int32_t *pages_used,
+                               int32_t page, int32_t position_offset,
+                               int64_t max_tokens, int32_t *cu_new,
+                               int32_t *positions, int64_t *slots,
+                               int32_t *seq_lens_out, int32_t *pages_used_out,
+                               int32_t *status, void *stream);
+
+/* The block step of a softmax layer: the B = block queries of each request over
+ * a prefix of prefix_len keys that every request shares, computed once for all
+ * of them, and over the request's own seq_lens[r] keys, the block's included.
+ *   causal = 0  every query sees all of them (a denoising read: the block is
+ *               seen whole by each of its positions)
+ *   causal = 1  query b sees the prefix and its request's first
+ *               seq_lens[r] - (B - 1 - b) own keys (replay, verification)
+ *   o = softmax(scale q k^T) v over the seen keys;  a query that sees none: 0
+ *   q          bf16 [num_req, B, q_heads, head_dim]
+ *   k_cache, v_cache  bf16 [num_pages, kv_heads, page, head_dim]; query head h
+ *              reads kv head h / (q_heads / kv_heads)
+ *   block_table int32 [num_req, max_pages], prefix_table int32
+ *              [ceil(prefix_len / page)] (may be NULL for prefix_len = 0): page
+ *              ids.  Only entries that the lengths reach are read; an id outside
+ *              [0, num_pages) reads another page of the cache, never beyond it
+ *   seq_lens   int32 [num_req] device, taken as within [0, max_seq_len]
+ *   max_seq_len  host bound of seq_lens, at most max_pages * page; the work is
+ *              cut by it, not by the lengths
+ *   o          bf16 [num_req, B, q_heads, head_dim]
+ *   lse        fp32 [num_req, B, q_heads] natural log of the sum of
+ *              exp(scale q k) (-inf where nothing is seen), or NULL
+ *   workspace  flare_block_attention_workspace_size bytes, 256-byte aligned
+ *              (the parts' outputs and statistics); NULL when that is 0
+ * Rows of a page that no length reaches may hold anything, NaN included.
+ * Requirements: io_dtype FLARE_BF16; head_dim in {64, 128, 256}; page a power of
+ * two of at least 16; q_heads a multiple of kv_heads; 16-byte aligned q,
+ * caches and o.  scale <= 0 selects 1 / sqrt(head_dim). */
+typedef struct {
+  int32_t block, q_heads, kv_heads, head_dim, page;
+  int32_t io_dtype;
+  int32_t causal;
+  float scale;
+} flare_attention_shape;
+size_t flare_block_attention_workspace_size(int32_t num_req,
+                                            const flare_attention_shape *shape,
+                                            int32_t max_seq_len,
+                                            int32_t prefix_len);
+flare_status flare_block_attention(
+    int32_t num_req, const flare_attention_shape *shape, const void *q,
+    const void *k_cache, const void *v_cache, int64_t num_pages,
+    const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens,
+    int32_t max_seq_len, const int32_t *prefix_table, int32_t prefix_len,
+    void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Thread-local message for the last non-OK status; "" if none. */
 const char *flare_last_error(void);
 
@@ -585,7 +782,9 @@ int32_t flare_version(void);
  * parts of the reverse chunk step),
  * "gdn_fwd_scan_kernel" (the forward state recurrence; "gdn_dual_fwd_kernel"
  * then names the forward's output pass) and "gdn_bwd_scan_kernel" (the
- * reverse recurrence).
+ * reverse recurrence); "norm_kernel", "norm_bwd_kernel" (both launches),
+ * "rotary_kernel", "step_tables_kernel", "block_attention_kernel" (all launches
+ * of a call).
  * flare_timing_enable(1) turns it on (events are created lazily, host side
  * only; no device memory is allocated), (0) off.  Returns the previous state.
  * flare_timing_avg_ms() blocks until the recorded launches of that kernel
