@@ -13,11 +13,11 @@
 namespace flare {
 
 struct AttnPlan {
-  int tiles;       // 16-row query tiles of a workgroup
+  int tiles;       // 16-row query tiles of a wave (4 waves a workgroup)
   int page_shift;
   int prefix_parts, prefix_chunk, prefix_groups;  // parts of the prefix, keys a part, row groups
   int own_parts, own_chunk, own_groups;
-  int64_t prefix_blocks, own_blocks;
+  int64_t prefix_blocks, own_blocks;              // prefix: a multiple of 8, some of them empty
 };
 
 // A request's own keys: never more than its table or the caller's bound holds.

@@ -29,6 +29,34 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
+// 16 bytes of memory a lane, at base + offset bytes, straight into LDS: lane i's at
+// lds + 16 i.  Written as
+// an instruction because the compiler, which cannot tell the tile in flight from
+// the tile being read, waits for the one before reading the other; whoever reads
+// waits for the load counter, then meets the others at a barrier.  No register is
+// written but M0, which nothing else in these kernels uses.
+__device__ __forceinline__ void load_lds16(const u16 *base, uint32_t offset, const u16 *lds) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u16 *)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base)
+               : "memory");
+}
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const u16 *uniform(const u16 *p) {
+  const uint64_t v = (uint64_t)p;
+  return (const u16 *)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
+                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32);
+}
+// Every load and LDS access of this wave done (vmcnt 0, lgkmcnt 0), then the others'.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <bool V> struct Const { static constexpr bool value = V; };
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // max with lane ^ 16 and lane ^ 32
@@ -49,99 +77,150 @@ __device__ __forceinline__ int v_piece(int row, int c) {
   return c ^ (2 * ((D == 64 ? row >> 1 : row) & (pairs - 1)));
 }
 
-// One workgroup: NQ * 16 rows of one kv head over one part.  Its four waves
-// take the part's 32-key tiles in turn, each with its own m, l and O, and are
-// joined through LDS at the end.  K goes from memory straight to MFMA operand
-// registers; V through a wave's own LDS tile (in-order LDS accesses of one
-// wave: no barrier in the loop).  The loads of the next tile are issued as soon
-// as the registers of this one are consumed.
-template <int D, int NQ>
-__global__ __launch_bounds__(256) void attn_rows_kernel(BlockAttnArgs a, AttnPlan p) {
-  constexpr int KS = D / 32;       // MFMA steps over the head
-  constexpr int DT = D / 16;       // 16-channel tiles of O
-  constexpr int VL = D / 16;       // 16-byte V pieces a lane loads per tile
-  constexpr int PIECES = D / 8;    // 16-byte pieces of a row
-  __shared__ __align__(16) u16 lds[4][32 * D];
-  __shared__ float stat[4][NQ][2][16];
-  const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
+// Where the 16-byte piece c of row `row` of a K tile [rows][D] bf16 sits: the 16
+// rows whose same piece one operand read takes fall on all banks.
+template <int D>
+__device__ __forceinline__ int k_piece(int row, int c) {
+  constexpr int pieces = D / 8 < 16 ? D / 8 : 16;
+  return c ^ ((D == 64 ? row >> 1 : row) & (pieces - 1));
+}
 
-  // which rows and keys
-  int64_t id = blockIdx.x;
-  const bool shared = id < p.prefix_blocks;
-  const int groups = shared ? p.prefix_groups : p.own_groups;
-  const int parts = shared ? p.prefix_parts : p.own_parts;
-  if (!shared) id -= p.prefix_blocks;
-  const int head = (int)(id % a.kv_heads);
-  id /= a.kv_heads;
-  const int rg = (int)(id % groups);
-  id /= groups;
-  const int part = (int)(id % parts);
-  const int req = (int)(id / parts);  // 0 for the prefix
-  const int G = a.q_heads / a.kv_heads, BG = a.block * G;
-  int64_t row0, row_end;  // rows (token * G + query of the group) of this workgroup
-  int len, chunk;
+// What a workgroup works on: rows [row0, row_end) (token * G + query of the
+// group) of one kv head against keys [k0, k1) of the prefix or of one request.
+struct Part {
+  uint32_t row0, row_end;
+  int head, k0, k1, out;  // out: the part's place in the workspace
+  int len, req;           // own keys of the request; req < 0: the prefix
   const int32_t *table;
-  if (shared) {
-    row0 = 0;
-    row_end = (int64_t)a.num_req * BG;
-    len = a.prefix_len;
-    chunk = p.prefix_chunk;
-    table = a.prefix_table;
-  } else {
-    row0 = (int64_t)req * BG;
-    row_end = row0 + BG;
-    len = attn_own_len(a, a.seq_lens[req]);
-    chunk = p.own_chunk;
-    table = a.block_table + (int64_t)req * a.max_pages;
-  }
-  row0 += (int64_t)rg * NQ * 16;
-  const int k0 = part * chunk;
-  const int k1 = len - k0 < chunk ? len : k0 + chunk;
-  const bool only = p.prefix_parts + p.own_parts == 1;
-  // a part behind the request's length: the joining launch does not read it
-  if (k0 >= k1 && !only) return;
-  const int tiles = (k1 - k0 + 31) >> 5;
+};
 
-  // the pages of this wave's subtiles: lane i holds that of tile wave + 4 (i / 2), subtile i & 1
+// Workgroups of the prefix and of the requests' own keys alternate in octets
+// (one for each XCD), in proportion: the prefix is bound by its products, the
+// own keys by memory, so a CU holds both kinds at a time.  The units (head, part)
+// of the prefix go round the XCDs and a unit's row groups stay on one: they read
+// the same keys from its L2.
+template <int ROWS>
+__device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan &p, Part &w) {
+  const uint32_t G = a.q_heads / a.kv_heads, BG = a.block * G;
+  const uint64_t po = p.prefix_blocks / 8, all = po + (p.own_blocks + 7) / 8, oct = blockIdx.x / 8;
+  const uint32_t pi = (uint32_t)(oct * po / all);
+  if ((oct + 1) * po / all > pi) {
+    const uint32_t unit = pi / p.prefix_groups * 8 + blockIdx.x % 8, rg = pi % p.prefix_groups;
+    if (unit >= (uint32_t)(a.kv_heads * p.prefix_parts)) return false;
+    const int part = (int)(unit / a.kv_heads);
+    w.head = (int)(unit % a.kv_heads);
+    w.row0 = rg * ROWS;
+    w.row_end = a.num_req * BG;
+    w.len = a.prefix_len;
+    w.k0 = part * p.prefix_chunk;
+    w.k1 = w.len - w.k0 < p.prefix_chunk ? w.len : w.k0 + p.prefix_chunk;
+    w.out = part;
+    w.req = -1;
+    w.table = a.prefix_table;
+    return true;
+  }
+  uint32_t id = (uint32_t)(oct - pi) * 8 + blockIdx.x % 8;
+  if (id >= p.own_blocks) return false;
+  w.head = (int)(id % (uint32_t)a.kv_heads);
+  id /= (uint32_t)a.kv_heads;
+  const uint32_t rg = id % (uint32_t)p.own_groups;
+  id /= (uint32_t)p.own_groups;
+  // all requests' first parts before their second: the longest requests' last ones start last
+  w.req = (int)(id % (uint32_t)a.num_req);
+  const int part = (int)(id / (uint32_t)a.num_req);
+  w.len = attn_own_len(a, a.seq_lens[w.req]);
+  w.row0 = w.req * BG + rg * ROWS;
+  w.row_end = (w.req + 1) * BG;
+  w.k0 = part * p.own_chunk;
+  w.k1 = w.len - w.k0 < p.own_chunk ? w.len : w.k0 + p.own_chunk;
+  w.out = p.prefix_parts + part;
+  w.table = a.block_table + (int64_t)w.req * a.max_pages;
+  // a part behind the request's length is not read by the joining launch; the
+  // only part is written in any case
+  return w.k0 < w.k1 || p.prefix_parts + p.own_parts == 1;
+}
+
+// One part.  The four waves hold NQ * 16 rows each and share the part's K and V
+// tiles of TK keys, which memory fills straight into LDS, a tile ahead: the
+// barrier that ends a tile is also the one that the next one's data waits at.
+// Waves without rows (a request's few) only help to load.
+template <int D, int NQ, int TK, int WPS>
+__global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPlan p) {
+  constexpr int KS = D / 32;                    // MFMA steps over the head
+  constexpr int DT = D / 16;                    // 16-channel tiles of O
+  constexpr int SUBS = TK / 16;                 // 16-key subtiles of a tile
+  constexpr int PIECES = D / 8;                 // 16-byte pieces of a row
+  constexpr int LOADS = 16 * PIECES / 64;       // 1 KiB loads of a subtile
+  __shared__ __align__(16) u16 kt_lds[2][TK * D];
+  __shared__ __align__(16) u16 vt_lds[2][TK * D];
+  const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
+  Part w;
+  if (!find_part<64 * NQ>(a, p, w)) return;
+  const int k0 = w.k0, k1 = w.k1, head = w.head;
+  const uint32_t G = a.q_heads / a.kv_heads;
+  const uint32_t row0 = w.row0 + wave * (NQ * 16);
+  const bool live = row0 < w.row_end;
+  const int tiles = k1 > k0 ? (k1 - k0 + TK - 1) / TK : 0;
+  // keys below `all` are seen by every row: the tiles below it need no mask
+  const bool causal = a.causal && w.req >= 0;
+  int all = causal ? w.len - (a.block - 1) : w.len;
+  if (all > k1) all = k1;
+  const int full = all > k0 ? (all - k0) / TK : 0;
+
+  // lane i holds the page of the subtile of tile i that this wave loads
+  const int last = (k1 - 1) & ~15;
+  const int sub = wave % SUBS;
   int page_id = 0;
-  if (k1 > k0) {
-    int j = k0 + 32 * (wave + 4 * (lane >> 1)) + 16 * (lane & 1);
-    const int last = (k1 - 1) & ~15;
+  if (tiles > 0) {
+    int j = k0 + TK * lane + 16 * sub;
     if (j > last) j = last;
-    page_id = table[j >> p.page_shift];
+    page_id = w.table[j >> p.page_shift];
     if (page_id < 0) page_id = 0;
     if (page_id >= a.num_pages) page_id = (int)a.num_pages - 1;
   }
+  // TK = 64: a wave fills one subtile of K and of V; TK = 32: waves 0, 1 fill K, 2, 3 V.
+  // A lane fetches the piece of its row that k_piece / v_piece put where it lands.
+  auto stage = [&](int t, int buf) {
+    int j = k0 + TK * t + 16 * sub;
+    if (j > last) j = last;
+    const int pg = __builtin_amdgcn_readlane(page_id, t);
+    const int64_t at = ((((int64_t)pg * a.kv_heads + head) << p.page_shift) + (j & (a.page - 1))) * D;
+    const u16 *kp = uniform((const u16 *)a.k_cache + at), *vp = uniform((const u16 *)a.v_cache + at);
+    int l = lane;
+    asm volatile("" : "+v"(l));  // offsets formed per tile: held over the loop they cost 2 LOADS registers
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int row = (i * 64 + l) / PIECES, slot = (i * 64 + l) % PIECES;
+      if (SUBS == 4 || wave < 2)
+        load_lds16(kp, 2 * (row * D + k_piece<D>(row, slot) * 8), &kt_lds[buf][sub * 16 * D + i * 512]);
+      if (SUBS == 4 || wave >= 2)
+        load_lds16(vp, 2 * (row * D + v_piece<D>(row, slot) * 8), &vt_lds[buf][sub * 16 * D + i * 512]);
+    }
+  };
+  if (tiles > 0) stage(0, 0);
 
-  // the queries, and how many keys each sees
+  // the queries, and in the last tiles of a request how many keys each sees
   bf16x8 q[NQ][KS];
   int lim[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int64_t m = row0 + n * 16 + col;
-    lim[n] = 0;
-    const bool ok = m < row_end;
-    const int64_t tok = ok ? m / G : 0;
-    const int g = ok ? (int)(m - tok * G) : 0;
-    const u16 *src = (const u16 *)a.q + (tok * a.q_heads + head * G + g) * D;
+    const uint32_t m = row0 + n * 16 + col;
+    const uint32_t tok = m / G;
+    const u16 *src = (const u16 *)a.q + ((int64_t)tok * a.q_heads + head * G + (m - tok * G)) * D + grp * 8;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      u16x8 z = {};
-      if (ok) z = *reinterpret_cast<const u16x8 *>(src + s * 32 + grp * 8);
-      q[n][s] = as_bf16x8(z);
+      u32x4v z = {0, 0, 0, 0};
+      if (m < w.row_end) z = *reinterpret_cast<const u32x4v *>(src + s * 32);
+      q[n][s] = __builtin_bit_cast(bf16x8, z);
     }
-    if (ok) {
-      lim[n] = len;
-      if (!shared && a.causal) {
-        const int b = (int)(tok - (int64_t)req * a.block);
-        const int seen = len - (a.block - 1 - b);
-        lim[n] = seen > 0 ? seen : 0;
-      }
+    lim[n] = k1;
+    if (causal) {
+      const int seen = w.len - (a.block - 1 - ((int)tok - w.req * a.block));
+      lim[n] = seen < k1 ? seen : k1;
     }
   }
-  // keys below this are seen by every row
-  const int all = shared || !a.causal ? len : len - (a.block - 1);
   const float sc = a.scale * kLog2e;
+  const float room = 8.0f / sc;  // how far a score may pass the kept maximum: weights up to 2^8
 
   floatx4 o[NQ][DT];
   float m[NQ], l[NQ];
@@ -152,195 +231,178 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(BlockAttnArgs a, AttnPla
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[n][d] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
-
-  bf16x8 kf[2][KS];
-  u16x8 vr[VL];
-  u16 *const vt = lds[wave];
-  auto rows_of = [&](int t, int sub) -> int64_t {
-    int j = k0 + 32 * t + 16 * sub;
-    const int last = (k1 - 1) & ~15;
-    if (j > last) j = last;
-    const int pg = __builtin_amdgcn_readlane(page_id, 2 * ((t - wave) >> 2) + sub);
-    return ((((int64_t)pg * a.kv_heads + head) << p.page_shift) + (j & (a.page - 1))) * D;
-  };
-  auto load_k = [&](int t) {
+  // this lane's places in a tile: K operand step e, V channel tile d; rows
+  // further down by multiples of 16 are constant offsets from them
+  int ka[KS], va[DT];
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const u16 *src = (const u16 *)a.k_cache + rows_of(t, sub) + col * D + grp * 8;
+  for (int e = 0; e < KS; ++e) ka[e] = col * D + k_piece<D>(col, 4 * e + grp) * 8;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) kf[sub][s] = as_bf16x8(*reinterpret_cast<const u16x8 *>(src + s * 32));
-    }
-  };
-  auto load_v = [&](int t) {
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const u16 *src = (const u16 *)a.v_cache + rows_of(t, sub);
-#pragma unroll
-      for (int i = 0; i < VL / 2; ++i) {
-        const int idx = i * 64 + lane;
-        vr[sub * (VL / 2) + i] = *reinterpret_cast<const u16x8 *>(src + idx * 8);
-      }
-    }
-  };
-  if (wave < tiles) {
-    load_k(wave);
-    load_v(wave);
+  for (int d = 0; d < DT; ++d) {
+    const int r = 4 * grp + (col >> 2);
+    va[d] = r * D + v_piece<D>(r, 2 * d + ((col & 3) >> 1)) * 8 + (col & 1) * 4;
   }
-  for (int t = wave; t < tiles; t += 4) {
-    const int kt = k0 + 32 * t;
-    floatx4 s[NQ][2];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        s[n][sub] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < KS; ++e) mma_bf16(s[n][sub], kf[sub][e], q[n][e]);
-      }
-    if (t + 4 < tiles) load_k(t + 4);
-    // V rows behind the length hold anything: 0 * NaN must not reach O
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int idx = (i % (VL / 2)) * 64 + lane;
-      const int row = (i / (VL / 2)) * 16 + idx / PIECES, c = idx % PIECES;
-      u16x8 z = {};
-      if (kt + row < k1) z = vr[i];
-      *reinterpret_cast<u16x8 *>(vt + row * D + v_piece<D>(row, c) * 8) = z;
+  auto tile = [&](int t, const u16 *kb, u16 *vb, auto ragged) {
+    const int kt = k0 + TK * t;
+    if constexpr (ragged.value) {
+      // V rows behind the length hold anything: 0 * NaN must not reach O
+      for (int i = threadIdx.x; i < TK * PIECES; i += 256)
+        if (kt + i / PIECES >= k1) *reinterpret_cast<u32x4v *>(vb + 8 * i) = u32x4v{0, 0, 0, 0};
+      __syncthreads();
     }
-    if (t + 4 < tiles) load_v(t + 4);
-
-    bf16x8 pb[NQ];
+    if (!live) return;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int hi = lim[n] < k1 ? lim[n] : k1;
-      float x[8], top = -INFINITY;
+    for (int h = 0; h < TK / 32; ++h) {
+      floatx4 s[NQ][2];
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
+      for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = kt + 16 * sub + 4 * grp + r;
-          float v = s[n][sub][r] * sc;
-          if (kt + 32 > all || kt + 32 > k1) v = key < hi ? v : -INFINITY;
-          x[4 * sub + r] = v;
-          top = fmaxf(top, v);
-        }
-      top = xmax32(xmax16(top));
-      const float mn = fmaxf(m[n], top);
-      const float base = mn == -INFINITY ? 0.0f : mn;  // a row that sees nothing yet
-      const float al = __builtin_amdgcn_exp2f(m[n] - base);
-      float sum = 0.0f;
-      uint32_t w[4];
+        for (int e = 0; e < KS; ++e) {
+          const bf16x8 kf =
+              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4v *>(kb + ka[e] + (32 * h + 16 * sb) * D));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(x[e] - base);
-        sum += x[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-      pb[n] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
-      l[n] = l[n] * al + sum;
-      if (__any(m[n] != mn)) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[n][d] *= al;
-      }
-      m[n] = mn;
-    }
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const int r0 = 4 * grp + (col >> 2), c = 2 * d + ((col & 3) >> 1), half = (col & 1) * 4;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vt + r0 * D + v_piece<D>(r0, c) * 8 + half));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4 *)(vt + (16 + r0) * D + v_piece<D>(16 + r0, c) * 8 + half));
-      const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf, pb[n]);
-    }
-  }
-
-  // join the four waves: their maxima and sums, then the outputs, one query
-  // tile at a time (a wave's O of 16 rows is the size of its V tile)
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    l[n] = xsum32(xsum16(l[n]));
-    if (grp == 0) {
-      stat[wave][n][0][col] = m[n];
-      stat[wave][n][1][col] = l[n];
-    }
-  }
-  __syncthreads();
-  const int64_t rows_all = (int64_t)a.num_req * a.block * a.q_heads;
-  const int out_part = shared ? part : p.prefix_parts + part;
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w][n][0][col]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    const float f = __builtin_amdgcn_exp2f(m[n] - base);
-    float *of = reinterpret_cast<float *>(lds[wave]);
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const int c = (4 * d + grp) ^ (col & 7);  // 16-byte pieces of a row of D floats
-      *reinterpret_cast<floatx4 *>(of + col * D + c * 4) = o[n][d] * f;
-    }
-    __syncthreads();
-    // 16 rows of D floats: thread i sums piece i % (D / 4) of row i / (D / 4)
-    for (int i = threadIdx.x; i < 16 * (D / 4); i += 256) {
-      const int r = i / (D / 4), c = i % (D / 4);
-      const int64_t mrow = row0 + n * 16 + r;
-      if (mrow < row_end) {
-        floatx4 sum = {0.f, 0.f, 0.f, 0.f};
-        float mr = -INFINITY, lr = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          sum += *reinterpret_cast<const floatx4 *>(reinterpret_cast<const float *>(lds[w]) + r * D + (c ^ (r & 7)) * 4);
-          mr = fmaxf(mr, stat[w][n][0][r]);
-        }
-        const float br = mr == -INFINITY ? 0.0f : mr;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) lr += stat[w][n][1][r] * __builtin_amdgcn_exp2f(stat[w][n][0][r] - br);
-        const int64_t tok = mrow / G;
-        const int64_t row = tok * a.q_heads + head * G + (mrow - tok * G);
-        if (only) {
-          const float inv = lr > 0.0f || lr != lr ? 1.0f / lr : 0.0f;
-          const uint2 w2 = make_uint2(pack_bf16x2(sum[0] * inv, sum[1] * inv), pack_bf16x2(sum[2] * inv, sum[3] * inv));
-          *reinterpret_cast<uint2 *>((u16 *)a.o + row * D + c * 4) = w2;
-          if (a.lse && c == 0) a.lse[row] = lr > 0.0f || lr != lr ? (mr + log2f(lr)) * 0.69314718055994530942f : -INFINITY;
-        } else {
-          *reinterpret_cast<floatx4 *>(a.part + ((int64_t)out_part * rows_all + row) * D + c * 4) = sum;
-          if (c == 0) {
-            float *ml = a.part + (int64_t)(p.prefix_parts + p.own_parts) * rows_all * D + ((int64_t)out_part * rows_all + row) * 2;
-            ml[0] = mr;
-            ml[1] = lr;
+          for (int n = 0; n < NQ; ++n) {
+            if (e == 0) s[n][sb] = floatx4{0.f, 0.f, 0.f, 0.f};
+            mma_bf16(s[n][sb], kf, q[n][e]);
           }
         }
+      float top[NQ];
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        if constexpr (ragged.value) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (kt + 32 * h + 16 * (e >> 2) + 4 * grp + (e & 3) >= lim[n]) s[n][e >> 2][e & 3] = -INFINITY;
+        }
+        top[n] = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), s[n][0][2]), s[n][0][3]);
+        top[n] = fmaxf(fmaxf(fmaxf(fmaxf(top[n], s[n][1][0]), s[n][1][1]), s[n][1][2]), s[n][1][3]);
+        over |= top[n] > m[n] + room;
+      }
+      if (__any(over)) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const float mn = fmaxf(m[n], xmax32(xmax16(top[n])));
+          const float al = __builtin_amdgcn_exp2f((m[n] - (mn == -INFINITY ? 0.0f : mn)) * sc);
+          m[n] = mn;
+          l[n] *= al;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[n][d] *= al;
+        }
+      }
+      bf16x8 pb[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float base = m[n] == -INFINITY ? 0.0f : m[n] * sc;  // a row that sees nothing yet
+        float x[8], sum = 0.0f;
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e >> 2][e & 3], sc, -base));
+          sum += x[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        pb[n] = __builtin_bit_cast(bf16x8, make_uint4(v[0], v[1], v[2], v[3]));
+        l[n] += sum;
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + 32 * h * D));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + (32 * h + 16) * D));
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf, pb[n]);
       }
     }
-    __syncthreads();
+  };
+  meet();
+  int t = 0;
+  for (; t < full; t += 2) {
+    if (t + 1 < tiles) stage(t + 1, 1);
+    tile(t, kt_lds[0], vt_lds[0], Const<false>{});
+    meet();
+    if (t + 1 >= full) break;
+    if (t + 2 < tiles) stage(t + 2, 0);
+    tile(t + 1, kt_lds[1], vt_lds[1], Const<false>{});
+    meet();
+  }
+  for (t = full; t < tiles; ++t) {
+    if (t + 1 < tiles) stage(t + 1, (t + 1) & 1);
+    tile(t, kt_lds[t & 1], vt_lds[t & 1], Const<true>{});
+    meet();
+  }
+
+  const int64_t rows_all = (int64_t)a.num_req * a.block * a.q_heads;
+  float *stat = a.part + (int64_t)(p.prefix_parts + p.own_parts) * rows_all * D;
+  const bool only = p.prefix_parts + p.own_parts == 1;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const uint32_t mrow = row0 + n * 16 + col;
+    l[n] = xsum32(xsum16(l[n]));
+    if (mrow < w.row_end) {
+      const uint32_t tok = mrow / G;
+      const int64_t row = (int64_t)tok * a.q_heads + head * G + (mrow - tok * G);
+      const float mx = m[n] == -INFINITY ? m[n] : m[n] * sc;
+      if (only) {
+        const bool any = l[n] > 0.0f || l[n] != l[n];
+        const float inv = any ? 1.0f / l[n] : 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          *reinterpret_cast<uint2 *>((u16 *)a.o + row * D + 16 * d + 4 * grp) =
+              make_uint2(pack_bf16x2(o[n][d][0] * inv, o[n][d][1] * inv), pack_bf16x2(o[n][d][2] * inv, o[n][d][3] * inv));
+        if (a.lse && grp == 0) a.lse[row] = any ? (mx + log2f(l[n])) * 0.69314718055994530942f : -INFINITY;
+      } else {
+        const int64_t at = (int64_t)w.out * rows_all + row;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) *reinterpret_cast<floatx4 *>(a.part + at * D + 16 * d + 4 * grp) = o[n][d];
+        if (grp == 0) *reinterpret_cast<float2 *>(stat + at * 2) = make_float2(mx, l[n]);
+      }
+    }
   }
 }
 
-// Joins the parts of a row: D / 4 lanes a row, 16 bytes each.
+// Joins the parts of a row: D / 4 lanes hold 16 bytes of it each.  With `split`
+// above 1 that many lane groups share a row's parts and add up through LDS.
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPlan p) {
-  constexpr int L = D / 4;
+__global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPlan p, int split) {
+  constexpr int L = D / 4;   // lanes a row
+  constexpr int S = 256 / L; // lane groups of a workgroup
+  __shared__ __align__(16) float acc[S][D];
   const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;
-  const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int c = threadIdx.x % L;
-  if (row >= rows) return;
-  const int req = (int)(row / ((int64_t)a.block * a.q_heads));
+  const int c = threadIdx.x % L, sg = threadIdx.x / L, mine = sg % split;
+  const int64_t row = (int64_t)blockIdx.x * (S / split) + sg / split;
+  const bool live = row < rows;
+  const int req = live ? (int)((uint32_t)row / (uint32_t)(a.block * a.q_heads)) : 0;
   const int len = attn_own_len(a, a.seq_lens[req]);
-  const int parts = p.prefix_parts + (len + p.own_chunk - 1) / p.own_chunk;
-  const float *ml = a.part + (int64_t)(p.prefix_parts + p.own_parts) * rows * D;
+  const int parts = live ? p.prefix_parts + (len + p.own_chunk - 1) / p.own_chunk : 0;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)(p.prefix_parts + p.own_parts) * rows * D) + row;
   float m = -INFINITY, l = 0.0f;
-  floatx4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, ml[((int64_t)i * rows + row) * 2]);
-  const float base = m == -INFINITY ? 0.0f : m;
-  for (int i = 0; i < parts; ++i) {
-    const float f = __builtin_amdgcn_exp2f(ml[((int64_t)i * rows + row) * 2] - base);
-    l += ml[((int64_t)i * rows + row) * 2 + 1] * f;
-    o += *reinterpret_cast<const floatx4 *>(a.part + ((int64_t)i * rows + row) * D + c * 4) * f;
+  for (int i = c; i < parts; i += L) {
+    const float2 v = ml[i * rows];
+    const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
+    l = l * __builtin_amdgcn_exp2f(m - base) + v.y * __builtin_amdgcn_exp2f(v.x - base);
+    m = mn;
   }
+#pragma unroll
+  for (int x = 1; x < L; x <<= 1) {
+    const float mo = __shfl_xor(m, x), lo = __shfl_xor(l, x);
+    const float mn = fmaxf(m, mo), base = mn == -INFINITY ? 0.0f : mn;
+    l = l * __builtin_amdgcn_exp2f(m - base) + lo * __builtin_amdgcn_exp2f(mo - base);
+    m = mn;
+  }
+  const float base = m == -INFINITY ? 0.0f : m;
+  floatx4 o = {0.f, 0.f, 0.f, 0.f};
+  const float *src = a.part + row * D + c * 4;
+#pragma unroll 4
+  for (int i = mine; i < parts; i += split)
+    o += *reinterpret_cast<const floatx4 *>(src + i * rows * D) * __builtin_amdgcn_exp2f(ml[i * rows].x - base);
+  if (split > 1) {
+    *reinterpret_cast<floatx4 *>(&acc[sg][c * 4]) = o;
+    __syncthreads();
+    if (mine != 0) return;
+    for (int i = 1; i < split; ++i) o += *reinterpret_cast<const floatx4 *>(&acc[sg + i][c * 4]);
+  }
+  if (!live) return;
   const bool any = l > 0.0f || l != l;
   const float inv = any ? 1.0f / l : 0.0f;
   *reinterpret_cast<uint2 *>((u16 *)a.o + row * D + c * 4) =
@@ -348,15 +410,17 @@ __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPla
   if (a.lse && c == 0) a.lse[row] = any ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <int D>
+template <int D, int NQ, int TK, int WPS>
 hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
-  const int64_t blocks = p.prefix_blocks + p.own_blocks;
-  if (p.tiles == 1) attn_rows_kernel<D, 1><<<(unsigned)blocks, 256, 0, st>>>(a, p);
-  else attn_rows_kernel<D, 2><<<(unsigned)blocks, 256, 0, st>>>(a, p);
+  const int64_t blocks = p.prefix_blocks + (p.own_blocks + 7) / 8 * 8;
+  attn_kernel<D, NQ, TK, WPS><<<(unsigned)blocks, 256, 0, st>>>(a, p);
   if (p.prefix_parts + p.own_parts > 1) {
     const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;
-    const int per = 256 / (D / 4);
-    attn_join_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a, p);
+    // few rows: every lane group of a workgroup on one
+    constexpr int groups = 256 / (D / 4);
+    const int split = rows < 512 * groups ? groups : 1;
+    const int per = groups / split;
+    attn_join_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a, p, split);
   }
   return hipGetLastError();
 }
@@ -367,9 +431,9 @@ hipError_t launch_block_attention(const BlockAttnArgs &a, hipStream_t st) {
   if (a.num_req == 0) return hipSuccess;
   const AttnPlan p = attn_plan(a);
   TimedLaunch tl(K_BLOCK_ATTN, st);
-  if (a.dim == 64) return launch_d<64>(a, p, st);
-  if (a.dim == 128) return launch_d<128>(a, p, st);
-  return launch_d<256>(a, p, st);
+  if (a.dim == 64) return p.tiles == 1 ? launch_d<64, 1, 64, 3>(a, p, st) : launch_d<64, 2, 64, 3>(a, p, st);
+  if (a.dim == 128) return p.tiles == 1 ? launch_d<128, 1, 64, 2>(a, p, st) : launch_d<128, 2, 64, 2>(a, p, st);
+  return launch_d<256, 1, 32, 2>(a, p, st);
 }
 
 }  // namespace flare

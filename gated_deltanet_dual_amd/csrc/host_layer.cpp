@@ -15,23 +15,39 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
   const int64_t all_rows = rows * a.num_req;
-  p.tiles = rows <= 16 && (a.prefix_len == 0 || all_rows <= 16) ? 1 : 2;
-  const int per = 16 * p.tiles;
+  p.tiles = a.dim <= 128 && (rows > 64 || (a.prefix_len > 0 && all_rows > 64)) ? 2 : 1;
+  const int per = 64 * p.tiles;
   p.own_groups = (int)ceil_div(rows, per);
   p.prefix_groups = (int)ceil_div(all_rows, per);
-  // parts short enough that the launch fills the chip, of 128 to 4096 keys
-  // (a wave keeps the pages of its subtiles in its lanes: 64 of 16 keys)
-  auto cut = [](int64_t len, int64_t units, int *chunk, int *parts) {
-    int64_t c = 4096;
-    while (c > 128 && units * ceil_div(len, c) < 1024) c /= 2;
-    *chunk = (int)c;
-    *parts = (int)ceil_div(len, c);
-  };
-  cut(a.prefix_len, (int64_t)p.prefix_groups * a.kv_heads, &p.prefix_chunk, &p.prefix_parts);
-  cut(a.max_seq_len, (int64_t)p.own_groups * a.kv_heads * a.num_req, &p.own_chunk, &p.own_parts);
+  // a wave keeps the pages of its part's tiles in its 64 lanes
+  const int64_t longest = a.dim == 256 ? 2048 : 4096, slots = 512;
+
+  // The prefix: a unit (kv head, part) stays on one XCD, which holds slots / 8
+  // workgroups at a time; the parts that finish first, counting a workgroup as
+  // its keys and 128 more for its start and end.
+  p.prefix_chunk = (int)longest;
+  if (a.prefix_len > 0) {
+    int64_t best = INT64_MAX;
+    const int64_t least = ceil_div(a.prefix_len, longest);
+    for (int64_t n = least; n <= least + 128; ++n) {
+      const int64_t chunk = ceil_div(ceil_div(a.prefix_len, n), 64) * 64, parts = ceil_div(a.prefix_len, chunk);
+      const int64_t rounds = ceil_div(ceil_div(parts * a.kv_heads, 8) * p.prefix_groups, slots / 8);
+      if (rounds * (chunk + 128) < best) {
+        best = rounds * (chunk + 128);
+        p.prefix_chunk = (int)chunk;
+        p.prefix_parts = (int)parts;
+      }
+    }
+  }
+  // The own keys: parts of 128 keys and more, short enough that the launch fills the chip.
+  int64_t c = longest;
+  const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
+  while (c > 128 && units * ceil_div(a.max_seq_len, c) < slots) c /= 2;
+  p.own_chunk = (int)c;
+  p.own_parts = (int)ceil_div(a.max_seq_len, c);
   if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
-  p.prefix_blocks = (int64_t)p.prefix_parts * p.prefix_groups * a.kv_heads;
-  p.own_blocks = (int64_t)p.own_parts * p.own_groups * a.kv_heads * a.num_req;
+  p.prefix_blocks = ceil_div((int64_t)p.prefix_parts * a.kv_heads, 8) * 8 * p.prefix_groups;
+  p.own_blocks = units * p.own_parts;
   return p;
 }
 

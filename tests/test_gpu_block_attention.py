@@ -82,6 +82,14 @@ CASES = [
     (2, 2, 1, 3, 128, 16, [0, 0], 30),
     (1, 1, 1, 2, 64, 16, [4500], 0),
     (40, 2, 1, 2, 64, 32, [(i * 37) % 90 for i in range(40)], 300),
+    # prefixes long and wide enough for shared tiles, in one part and in several, ending inside a tile and a page
+    (40, 2, 2, 2, 128, 16, [(i * 11) % 50 for i in range(40)], 333),
+    (9, 8, 1, 3, 128, 64, [8 + i for i in range(9)], 64),
+    (9, 8, 1, 3, 128, 64, [8 + i for i in range(9)], 1),
+    (30, 4, 1, 2, 128, 32, [4] * 30, 1500),
+    (33, 2, 1, 2, 256, 16, [(i * 7) % 40 for i in range(33)], 700),
+    (64, 1, 1, 1, 64, 16, [0] * 64, 1000),
+    (13, 1, 1, 8, 128, 128, [0] * 13, 200),
 ]
 
 
