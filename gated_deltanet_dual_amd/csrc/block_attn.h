@@ -13,7 +13,7 @@
 namespace flare {
 
 struct AttnPlan {
-  int tiles;       // 16-row query tiles of a wave (4 waves a workgroup)
+  int prefix_tiles, own_tiles;  // 16-row query tiles of a wave (4 waves a workgroup)
   int page_shift;
   int prefix_parts, prefix_chunk, prefix_groups;  // parts of the prefix, keys a part, row groups
   int own_parts, own_chunk, own_groups;

@@ -35,11 +35,18 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // the tile being read, waits for the one before reading the other; whoever reads
 // waits for the load counter, then meets the others at a barrier.  No register is
 // written but M0, which nothing else in these kernels uses.
-__device__ __forceinline__ void load_lds16(const u16 *base, uint32_t offset, const u16 *lds) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(
-      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u16 *)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base)
-               : "memory");
+template <bool NT>
+__device__ __forceinline__ void load_lds16(const u16 *base, uint32_t offset, uint32_t lds) {
+  if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+// The LDS address of p, the same in all lanes.
+__device__ __forceinline__ uint32_t lds_at(const u16 *p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u16 *)p);
 }
 // A pointer that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ const u16 *uniform(const u16 *p) {
@@ -99,17 +106,17 @@ struct Part {
 // own keys by memory, so a CU holds both kinds at a time.  The units (head, part)
 // of the prefix go round the XCDs and a unit's row groups stay on one: they read
 // the same keys from its L2.
-template <int ROWS>
+template <int PREFIX_ROWS, int OWN_ROWS>
 __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan &p, Part &w) {
   const uint32_t G = a.q_heads / a.kv_heads, BG = a.block * G;
   const uint64_t po = p.prefix_blocks / 8, all = po + (p.own_blocks + 7) / 8, oct = blockIdx.x / 8;
-  const uint32_t pi = (uint32_t)(oct * po / all);
+  const uint32_t pi = (uint32_t)(oct * po / all);  // octets of the prefix before this one
   if ((oct + 1) * po / all > pi) {
     const uint32_t unit = pi / p.prefix_groups * 8 + blockIdx.x % 8, rg = pi % p.prefix_groups;
     if (unit >= (uint32_t)(a.kv_heads * p.prefix_parts)) return false;
     const int part = (int)(unit / a.kv_heads);
     w.head = (int)(unit % a.kv_heads);
-    w.row0 = rg * ROWS;
+    w.row0 = rg * PREFIX_ROWS;
     w.row_end = a.num_req * BG;
     w.len = a.prefix_len;
     w.k0 = part * p.prefix_chunk;
@@ -129,7 +136,7 @@ __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan
   w.req = (int)(id % (uint32_t)a.num_req);
   const int part = (int)(id / (uint32_t)a.num_req);
   w.len = attn_own_len(a, a.seq_lens[w.req]);
-  w.row0 = w.req * BG + rg * ROWS;
+  w.row0 = w.req * BG + rg * OWN_ROWS;
   w.row_end = (w.req + 1) * BG;
   w.k0 = part * p.own_chunk;
   w.k1 = w.len - w.k0 < p.own_chunk ? w.len : w.k0 + p.own_chunk;
@@ -143,22 +150,21 @@ __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan
 // One part.  The four waves hold NQ * 16 rows each and share the part's K and V
 // tiles of TK keys, which memory fills straight into LDS, a tile ahead: the
 // barrier that ends a tile is also the one that the next one's data waits at.
-// Waves without rows (a request's few) only help to load.
-template <int D, int NQ, int TK, int WPS>
-__global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPlan p) {
+// Waves without rows (a request's few) only help to load; `turn` moves the waves
+// with rows on from workgroup to workgroup, so that all SIMDs of a CU get some.
+template <int D, int NQ, int TK, bool NT>
+__device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan &p, const Part &w, int turn,
+                                          u16 (&kt_lds)[2][TK * D], u16 (&vt_lds)[2][TK * D]) {
   constexpr int KS = D / 32;                    // MFMA steps over the head
   constexpr int DT = D / 16;                    // 16-channel tiles of O
   constexpr int SUBS = TK / 16;                 // 16-key subtiles of a tile
   constexpr int PIECES = D / 8;                 // 16-byte pieces of a row
   constexpr int LOADS = 16 * PIECES / 64;       // 1 KiB loads of a subtile
-  __shared__ __align__(16) u16 kt_lds[2][TK * D];
-  __shared__ __align__(16) u16 vt_lds[2][TK * D];
-  const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
-  Part w;
-  if (!find_part<64 * NQ>(a, p, w)) return;
+  const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int k0 = w.k0, k1 = w.k1, head = w.head;
   const uint32_t G = a.q_heads / a.kv_heads;
-  const uint32_t row0 = w.row0 + wave * (NQ * 16);
+  const uint32_t row0 = w.row0 + ((wave + turn) & 3) * (NQ * 16);
   const bool live = row0 < w.row_end;
   const int tiles = k1 > k0 ? (k1 - k0 + TK - 1) / TK : 0;
   // keys below `all` are seen by every row: the tiles below it need no mask
@@ -180,21 +186,24 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
   }
   // TK = 64: a wave fills one subtile of K and of V; TK = 32: waves 0, 1 fill K, 2, 3 V.
   // A lane fetches the piece of its row that k_piece / v_piece put where it lands.
+  // Row and piece of load i differ from those of load 0 by bits of i alone, so the
+  // byte offset is that of load 0 with a constant's bits turned over.
+  const uint32_t ky = 2 * (lane / PIECES * D + k_piece<D>(lane / PIECES, lane % PIECES) * 8);
+  const uint32_t vy = 2 * (lane / PIECES * D + v_piece<D>(lane / PIECES, lane % PIECES) * 8);
+  const uint32_t k_at = lds_at(&kt_lds[0][sub * 16 * D]), v_at = lds_at(&vt_lds[0][sub * 16 * D]);
   auto stage = [&](int t, int buf) {
     int j = k0 + TK * t + 16 * sub;
     if (j > last) j = last;
     const int pg = __builtin_amdgcn_readlane(page_id, t);
     const int64_t at = ((((int64_t)pg * a.kv_heads + head) << p.page_shift) + (j & (a.page - 1))) * D;
     const u16 *kp = uniform((const u16 *)a.k_cache + at), *vp = uniform((const u16 *)a.v_cache + at);
-    int l = lane;
-    asm volatile("" : "+v"(l));  // offsets formed per tile: held over the loop they cost 2 LOADS registers
+    const uint32_t to = buf * (TK * D * 2);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int row = (i * 64 + l) / PIECES, slot = (i * 64 + l) % PIECES;
-      if (SUBS == 4 || wave < 2)
-        load_lds16(kp, 2 * (row * D + k_piece<D>(row, slot) * 8), &kt_lds[buf][sub * 16 * D + i * 512]);
-      if (SUBS == 4 || wave >= 2)
-        load_lds16(vp, 2 * (row * D + v_piece<D>(row, slot) * 8), &vt_lds[buf][sub * 16 * D + i * 512]);
+      constexpr int RPI = 64 / PIECES;
+      const uint32_t kx = 2 * (i * RPI * D + k_piece<D>(i * RPI, 0) * 8), vx = 2 * (i * RPI * D + v_piece<D>(i * RPI, 0) * 8);
+      if (SUBS == 4 || wave < 2) load_lds16<NT>(kp, ky ^ kx, k_at + to + i * 1024);
+      if (SUBS == 4 || wave >= 2) load_lds16<NT>(vp, vy ^ vx, v_at + to + i * 1024);
     }
   };
   if (tiles > 0) stage(0, 0);
@@ -253,10 +262,11 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
 #pragma unroll
     for (int h = 0; h < TK / 32; ++h) {
       floatx4 s[NQ][2];
+      // two subtiles in turn: 2 NQ accumulators, each product a step behind its last
 #pragma unroll
-      for (int sb = 0; sb < 2; ++sb)
+      for (int e = 0; e < KS; ++e)
 #pragma unroll
-        for (int e = 0; e < KS; ++e) {
+        for (int sb = 0; sb < 2; ++sb) {
           const bf16x8 kf =
               __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4v *>(kb + ka[e] + (32 * h + 16 * sb) * D));
 #pragma unroll
@@ -265,6 +275,14 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
             mma_bf16(s[n][sb], kf, q[n][e]);
           }
         }
+      // V's operands while the scores become weights
+      bf16x8 vf[DT];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + 32 * h * D));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + (32 * h + 16) * D));
+        vf[d] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
       float top[NQ];
       bool over = false;
 #pragma unroll
@@ -306,13 +324,9 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
         l[n] += sum;
       }
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + 32 * h * D));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + (32 * h + 16) * D));
-        const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf, pb[n]);
-      }
+        for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf[d], pb[n]);
     }
   };
   meet();
@@ -358,6 +372,22 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
         if (grp == 0) *reinterpret_cast<float2 *>(stat + at * 2) = make_float2(mx, l[n]);
       }
     }
+  }
+}
+
+// NQP, NQO: row tiles of a wave for the prefix (rows of all requests) and for a
+// request's own keys.
+template <int D, int NQP, int NQO, int TK, int WPS>
+__global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPlan p) {
+  __shared__ __align__(16) u16 kt_lds[2][TK * D];
+  __shared__ __align__(16) u16 vt_lds[2][TK * D];
+  Part w;
+  if (!find_part<64 * NQP, 64 * NQO>(a, p, w)) return;
+  if (w.req < 0) {
+    attn_part<D, NQP, TK, false>(a, p, w, 0, kt_lds, vt_lds);
+  } else {
+    const uint32_t oct = blockIdx.x / 8;
+    attn_part<D, NQO, TK, NQO == 1>(a, p, w, (oct + oct / 32) & 3, kt_lds, vt_lds);
   }
 }
 
@@ -410,10 +440,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPla
   if (a.lse && c == 0) a.lse[row] = any ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <int D, int NQ, int TK, int WPS>
+template <int D, int NQP, int NQO, int TK, int WPS>
 hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   const int64_t blocks = p.prefix_blocks + (p.own_blocks + 7) / 8 * 8;
-  attn_kernel<D, NQ, TK, WPS><<<(unsigned)blocks, 256, 0, st>>>(a, p);
+  attn_kernel<D, NQP, NQO, TK, WPS><<<(unsigned)blocks, 256, 0, st>>>(a, p);
   if (p.prefix_parts + p.own_parts > 1) {
     const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;
     // few rows: every lane group of a workgroup on one
@@ -431,9 +461,15 @@ hipError_t launch_block_attention(const BlockAttnArgs &a, hipStream_t st) {
   if (a.num_req == 0) return hipSuccess;
   const AttnPlan p = attn_plan(a);
   TimedLaunch tl(K_BLOCK_ATTN, st);
-  if (a.dim == 64) return p.tiles == 1 ? launch_d<64, 1, 64, 3>(a, p, st) : launch_d<64, 2, 64, 3>(a, p, st);
-  if (a.dim == 128) return p.tiles == 1 ? launch_d<128, 1, 64, 2>(a, p, st) : launch_d<128, 2, 64, 2>(a, p, st);
-  return launch_d<256, 1, 32, 2>(a, p, st);
+  if (a.dim == 64) {
+    if (p.own_tiles == 2) return launch_d<64, 2, 2, 64, 3>(a, p, st);
+    return p.prefix_tiles == 2 ? launch_d<64, 2, 1, 64, 3>(a, p, st) : launch_d<64, 1, 1, 64, 3>(a, p, st);
+  }
+  if (a.dim == 128) {
+    if (p.own_tiles == 2) return launch_d<128, 2, 2, 64, 2>(a, p, st);
+    return p.prefix_tiles == 2 ? launch_d<128, 2, 1, 64, 2>(a, p, st) : launch_d<128, 1, 1, 64, 2>(a, p, st);
+  }
+  return launch_d<256, 1, 1, 32, 2>(a, p, st);
 }
 
 }  // namespace flare

@@ -15,10 +15,10 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
   const int64_t all_rows = rows * a.num_req;
-  p.tiles = a.dim <= 128 && (rows > 64 || (a.prefix_len > 0 && all_rows > 64)) ? 2 : 1;
-  const int per = 64 * p.tiles;
-  p.own_groups = (int)ceil_div(rows, per);
-  p.prefix_groups = (int)ceil_div(all_rows, per);
+  p.own_tiles = a.dim <= 128 && rows > 64 ? 2 : 1;
+  p.prefix_tiles = a.dim <= 128 && (all_rows > 64 || p.own_tiles == 2) ? 2 : 1;
+  p.own_groups = (int)ceil_div(rows, 64 * p.own_tiles);
+  p.prefix_groups = (int)ceil_div(all_rows, 64 * p.prefix_tiles);
   // a wave keeps the pages of its part's tiles in its 64 lanes
   const int64_t longest = a.dim == 256 ? 2048 : 4096, slots = 512;
 
