@@ -20,33 +20,48 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   p.own_groups = (int)ceil_div(rows, 64 * p.own_tiles);
   p.prefix_groups = (int)ceil_div(all_rows, 64 * p.prefix_tiles);
   // a wave keeps the pages of its part's tiles in its 64 lanes
-  const int64_t longest = a.dim == 256 ? 2048 : 4096, slots = 512;
+  const int64_t longest = a.dim == 256 ? 2048 : 4096;
 
-  // The prefix: a unit (kv head, part) stays on one XCD, which holds slots / 8
-  // workgroups at a time; the parts that finish first, counting a workgroup as
-  // its keys and 128 more for its start and end.
+  // How long the parts are: the shortest time, counted in keys that a workgroup
+  // passes (64 in about 1.3 us).  512 workgroups run at a time (two a CU); a
+  // round of them costs its keys and 384 more for its start and end, and every
+  // part is written and read again by the joining launch, rows * dim * 8 bytes at
+  // 5 TB/s and a little.  Measured against parts twice as long and as short:
+  // 16 requests x 4 over 4096 own keys (16 q, 4 kv heads, d = 128) 24.9 us at the
+  // chosen 512 keys, 29.2 at 256, 28.5 at 1024; 16 x 4 over a prefix of 4096:
+  // 21.6 us at 256, 23.8 at 128 and at 512; 37 x 7 at d = 256 over own 777 keys
+  // 41.6 us at 512, 45.1 at 256, 53.5 at 1024.
+  constexpr int64_t kSlots = 512, kStart = 384;
+  const int64_t join = all_rows * a.kv_heads * a.dim / 12500 + 2;
+
+  // A unit (kv head, part) of the prefix stays on one of 8 XCDs.
   p.prefix_chunk = (int)longest;
-  if (a.prefix_len > 0) {
-    int64_t best = INT64_MAX;
-    const int64_t least = ceil_div(a.prefix_len, longest);
-    for (int64_t n = least; n <= least + 128; ++n) {
-      const int64_t chunk = ceil_div(ceil_div(a.prefix_len, n), 64) * 64, parts = ceil_div(a.prefix_len, chunk);
-      const int64_t rounds = ceil_div(ceil_div(parts * a.kv_heads, 8) * p.prefix_groups, slots / 8);
-      if (rounds * (chunk + 128) < best) {
-        best = rounds * (chunk + 128);
-        p.prefix_chunk = (int)chunk;
-        p.prefix_parts = (int)parts;
-      }
+  int64_t best = INT64_MAX;
+  for (int64_t n = ceil_div(a.prefix_len, longest), most = n + 128; a.prefix_len > 0 && n <= most; ++n) {
+    const int64_t chunk = ceil_div(ceil_div(a.prefix_len, n), 64) * 64, parts = ceil_div(a.prefix_len, chunk);
+    const int64_t rounds = ceil_div(ceil_div(parts * a.kv_heads, 8) * p.prefix_groups, kSlots / 8);
+    const int64_t cost = rounds * (chunk + kStart) + parts * join;
+    if (cost < best) {
+      best = cost;
+      p.prefix_chunk = (int)chunk;
+      p.prefix_parts = (int)parts;
     }
   }
-  // The own keys: parts of 128 keys and more, short enough that the launch fills the chip.
-  int64_t c = longest;
-  const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
-  while (c > 128 && units * ceil_div(a.max_seq_len, c) < slots) c /= 2;
-  p.own_chunk = (int)c;
-  p.own_parts = (int)ceil_div(a.max_seq_len, c);
-  if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
   p.prefix_blocks = ceil_div((int64_t)p.prefix_parts * a.kv_heads, 8) * 8 * p.prefix_groups;
+  // The own keys share the rounds with the prefix.
+  const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
+  best = INT64_MAX;
+  p.own_chunk = (int)longest;
+  for (int64_t c = longest; a.max_seq_len > 0 && c >= 128; c /= 2) {
+    const int64_t parts = ceil_div(a.max_seq_len, c), rounds = ceil_div(p.prefix_blocks + units * parts, kSlots);
+    const int64_t cost = rounds * ((c < a.max_seq_len ? c : a.max_seq_len) + kStart) + parts * join;
+    if (cost < best) {
+      best = cost;
+      p.own_chunk = (int)c;
+      p.own_parts = (int)parts;
+    }
+  }
+  if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
   p.own_blocks = units * p.own_parts;
   return p;
 }
