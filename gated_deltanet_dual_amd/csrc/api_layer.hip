@@ -124,7 +124,7 @@ flare_status flare_residual_norm_bwd(int64_t tokens, int32_t dim, int32_t io_dty
   a.rstd = const_cast<float *>(rstd);
   a.dx = dx; a.dres = dresidual; a.dgate = dgate;
   a.dw_pre = dw_pre; a.dw_post = dw_post; a.dscale = dscale;
-  a.part = reinterpret_cast<float *>(workspace);
+  a.part[0] = reinterpret_cast<float *>(workspace);
   return hip_status(launch_residual_norm_bwd(a, (hipStream_t)stream), "residual_norm_bwd launch");
 }
 
@@ -209,7 +209,8 @@ flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens, const i
 size_t flare_block_attention_workspace_size(int32_t num_req, const flare_attention_shape *shape, int32_t max_seq_len,
                                             int32_t prefix_len) {
   if (check_attention_shape(num_req, shape, max_seq_len, prefix_len) != FLARE_OK) return 0;
-  return block_attention_workspace_bytes(attention_args(num_req, shape, max_seq_len, prefix_len));
+  const BlockAttnArgs a = attention_args(num_req, shape, max_seq_len, prefix_len);
+  return block_attention_workspace_bytes(a, attn_plan(a));
 }
 
 flare_status flare_block_attention(int32_t num_req, const flare_attention_shape *shape, const void *q,
@@ -234,12 +235,12 @@ flare_status flare_block_attention(int32_t num_req, const flare_attention_shape 
   if ((((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)o) & 15u) != 0)
     return fail(FLARE_ERR_ALIGN, "block_attention: q, the caches and o must be 16-byte aligned");
   BlockAttnArgs a = attention_args(num_req, shape, max_seq_len, prefix_len);
-  const size_t need = block_attention_workspace_bytes(a);
+  const AttnPlan p = attn_plan(a);
+  const size_t need = block_attention_workspace_bytes(a, p);
   if (need > 0) {
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != FLARE_OK) return st;
   }
-  const AttnPlan p = attn_plan(a);
   if (p.prefix_blocks + p.own_blocks > INT32_MAX)
     return fail(FLARE_ERR_UNSUPPORTED, "block_attention: too many workgroups");
   a.num_pages = num_pages;
@@ -248,7 +249,7 @@ flare_status flare_block_attention(int32_t num_req, const flare_attention_shape 
   a.block_table = block_table; a.seq_lens = seq_lens; a.prefix_table = prefix_table;
   a.o = o; a.lse = lse;
   a.part = reinterpret_cast<float *>(workspace);
-  return hip_status(launch_block_attention(a, (hipStream_t)stream), "block_attention launch");
+  return hip_status(launch_block_attention(a, p, (hipStream_t)stream), "block_attention launch");
 }
 
 }  // extern "C"

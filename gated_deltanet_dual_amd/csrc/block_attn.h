@@ -28,5 +28,6 @@ FLARE_HD int attn_own_len(const BlockAttnArgs &a, int32_t len) {
 
 // a.max_seq_len <= max_pages * page
 AttnPlan attn_plan(const BlockAttnArgs &a);
+size_t block_attention_workspace_bytes(const BlockAttnArgs &a, const AttnPlan &p);
 
 }  // namespace flare

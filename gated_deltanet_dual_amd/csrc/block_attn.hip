@@ -457,9 +457,7 @@ hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_block_attention(const BlockAttnArgs &a, hipStream_t st) {
-  if (a.num_req == 0) return hipSuccess;
-  const AttnPlan p = attn_plan(a);
+hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   TimedLaunch tl(K_BLOCK_ATTN, st);
   if (a.dim == 64) {
     if (p.own_tiles == 2) return launch_d<64, 2, 2, 64, 3>(a, p, st);

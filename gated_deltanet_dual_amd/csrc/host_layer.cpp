@@ -37,7 +37,7 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   // A unit (kv head, part) of the prefix stays on one of 8 XCDs.
   p.prefix_chunk = (int)longest;
   int64_t best = INT64_MAX;
-  for (int64_t n = ceil_div(a.prefix_len, longest), most = n + 128; a.prefix_len > 0 && n <= most; ++n) {
+  for (int64_t n = ceil_div(a.prefix_len, longest), most = n + 128; a.prefix_len > 0 && n <= most; n += 1 + n / 8) {
     const int64_t chunk = ceil_div(ceil_div(a.prefix_len, n), 64) * 64, parts = ceil_div(a.prefix_len, chunk);
     const int64_t rounds = ceil_div(ceil_div(parts * a.kv_heads, 8) * p.prefix_groups, kSlots / 8);
     const int64_t cost = rounds * (chunk + kStart) + parts * join;
@@ -67,10 +67,15 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
 }
 
 
-int norm_bwd_blocks(int64_t rows) { return (int)(rows < kNormBwdBlocks ? rows : kNormBwdBlocks); }
+int norm_bwd_blocks(int64_t rows, int32_t dim) {
+  // what the chip holds at a time: six workgroups of 256 threads a CU where a wave
+  // holds rows, three where the row is a workgroup's
+  const int64_t most = dim <= 512 ? 1536 : 768;
+  return (int)(rows < most ? rows : most);
+}
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t dim, int weights) {
-  return (size_t)norm_bwd_blocks(rows) * dim * weights * sizeof(float) + 256;
+  return (size_t)norm_bwd_blocks(rows, dim) * dim * weights * sizeof(float) + 256;
 }
 
 flare_status check_io(int32_t io_dtype) {
@@ -212,11 +217,9 @@ BlockAttnArgs attention_args(int32_t num_req, const flare_attention_shape *s, in
   return a;
 }
 
-size_t block_attention_workspace_bytes(const BlockAttnArgs &a) {
-  if (a.num_req == 0) return 0;
-  const AttnPlan p = attn_plan(a);
+size_t block_attention_workspace_bytes(const BlockAttnArgs &a, const AttnPlan &p) {
   const int64_t parts = (int64_t)p.prefix_parts + p.own_parts;
-  if (parts <= 1) return 0;
+  if (a.num_req == 0 || parts <= 1) return 0;
   return (size_t)parts * a.num_req * a.block * a.q_heads * (a.dim + 2) * sizeof(float) + 256;
 }
 

@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "block_attn.h"
 #include "layer_ops.h"
 #include "timing.h"
 
@@ -14,6 +15,6 @@ hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t st);
 hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t st);
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st);
 hipError_t launch_step_tables(const StepTablesArgs &a, hipStream_t st);
-hipError_t launch_block_attention(const BlockAttnArgs &a, hipStream_t st);
+hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st);
 
 }  // namespace flare

@@ -11,9 +11,6 @@
 namespace flare {
 
 // ---------------------------------------------------------------- norms
-// Row blocks of the reverse modes: each sums the weight gradients of its rows
-// and writes one partial row, which a second launch adds in a fixed order.
-constexpr int kNormBwdBlocks = 512;
 
 struct GatedNormArgs {
   int64_t tokens;
@@ -37,7 +34,7 @@ struct ResidualNormArgs {
   float *rstd;                          // [tokens][2]: post, pre
   void *h, *y, *dx, *dres, *dgate;
   float *dw_pre, *dw_post, *dscale;
-  float *part;  // [3][blocks][dim]: w_pre, then w_post and scale where present
+  float *part[3];  // [blocks][dim] of w_pre, w_post, scale; the workspace in part[0] at the launcher
 };
 
 // ---------------------------------------------------------------- rotary
@@ -59,7 +56,7 @@ struct RotaryArgs {
 };
 
 // ---------------------------------------------------------------- step tables
-constexpr int kTablesMaxReq = 8192;  // two int32 per request in LDS
+constexpr int kTablesMaxReq = 8192;  // three int32 per request in LDS
 
 struct StepTablesArgs {
   int num_req, max_pages, page;
@@ -84,9 +81,10 @@ struct BlockAttnArgs {
 };
 
 // ---------------------------------------------------------------- host checks
-// Rows of partial weight sums of a norm's reverse mode over this many rows, and
-// the bytes of its workspace with `weights` weights.
-int norm_bwd_blocks(int64_t rows);
+// Workgroups of a norm's reverse mode over this many rows at most: each sums the
+// weight gradients of its rows and writes one partial row, which a second launch
+// adds in a fixed order.  And the bytes of its workspace with `weights` weights.
+int norm_bwd_blocks(int64_t rows, int32_t dim);
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t dim, int weights);
 
 flare_status check_io(int32_t io_dtype);
@@ -104,7 +102,6 @@ flare_status check_step_tables(const StepTablesArgs &a);
 // shape alone (for the size query), then everything
 flare_status check_attention_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
                                    int32_t prefix_len);
-size_t block_attention_workspace_bytes(const BlockAttnArgs &a);
 BlockAttnArgs attention_args(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
                              int32_t prefix_len);
 

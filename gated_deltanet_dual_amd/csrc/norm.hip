@@ -57,25 +57,52 @@ template <typename IO> struct Vec<IO, 1> {
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-// act(g); act < 0: no gate
-__device__ __forceinline__ float gate_value(float g, int act) {
-  if (act == FLARE_GATE_LINEAR) return g;
-  const float p = sigmoid(g);
-  return act == FLARE_GATE_SIGMOID ? p : g * p;
+// f = act(g) of a vector's elements (1 without a gate, act < 0).  The choice is
+// made once for the vector: inside the element loop it would cut the code at
+// every element.
+template <int VEC> __device__ __forceinline__ void gate_values(const float *g, int act, float *f) {
+  if (act == FLARE_GATE_SILU) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = g[e] * sigmoid(g[e]);
+  } else if (act == FLARE_GATE_SIGMOID) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = sigmoid(g[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = act == FLARE_GATE_LINEAR ? g[e] : 1.0f;
+  }
 }
-// act(g) and its derivative
-__device__ __forceinline__ float gate_value_d(float g, int act, float &d) {
-  if (act == FLARE_GATE_LINEAR) {
-    d = 1.0f;
-    return g;
+// and the derivative d (0 without a gate)
+template <int VEC> __device__ __forceinline__ void gate_values_d(const float *g, int act, float *f, float *d) {
+  if (act == FLARE_GATE_SILU) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float x = g[e], p = sigmoid(x);  // f may be g
+      f[e] = x * p;
+      d[e] = p * (1.0f + x * (1.0f - p));
+    }
+  } else if (act == FLARE_GATE_SIGMOID) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      f[e] = sigmoid(g[e]);
+      d[e] = f[e] * (1.0f - f[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      f[e] = act == FLARE_GATE_LINEAR ? g[e] : 1.0f;
+      d[e] = act == FLARE_GATE_LINEAR ? 1.0f : 0.0f;
+    }
   }
-  const float p = sigmoid(g);
-  if (act == FLARE_GATE_SIGMOID) {
-    d = p * (1.0f - p);
-    return p;
+}
+// The vector c of an fp32 weight, or ones where it is absent.
+template <int VEC> __device__ __forceinline__ void load_or_one(const float *w, int c, float *f) {
+  if (w) {
+    Vec<float, VEC>::load(w + c * VEC, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = 1.0f;
   }
-  d = p * (1.0f + g * (1.0f - p));
-  return g * p;
 }
 
 // A row is held by a team of `team` threads, a power of two: up to a wave
@@ -103,8 +130,8 @@ template <bool BLOCK> struct Team {
 };
 
 // ---------------------------------------------------------------- gated norm
-template <typename IO, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : 256) void gated_norm_kernel(GatedNormArgs a, int team) {
+template <typename IO, int VEC, int NV, bool BLOCK, int THREADS>
+__global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a, int team) {
   __shared__ float red[16];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
@@ -135,11 +162,9 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void gated_norm_kernel(GatedNor
       if (c < nv) {
         float w[VEC], o[VEC];
         Vec<float, VEC>::load(a.weight + c * VEC, w);
+        gate_values<VEC>(gv[i], a.act, o);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          o[e] = xv[i][e] * r * w[e];
-          if (a.act >= 0) o[e] *= gate_value(gv[i][e], a.act);
-        }
+        for (int e = 0; e < VEC; ++e) o[e] *= xv[i][e] * r * w[e];
         Vec<IO, VEC>::store(y + c * VEC, o);
       }
     }
@@ -180,8 +205,8 @@ __device__ __forceinline__ void write_partial(const float (&acc)[NV][VEC], const
   }
 }
 
-template <typename IO, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : 256) void gated_norm_bwd_kernel(GatedNormArgs a, int team) {
+template <typename IO, int VEC, int NV, bool BLOCK, int THREADS>
+__global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a, int team) {
   __shared__ float red[16];
   __shared__ float cols[BLOCK ? 1 : 256 * VEC];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
@@ -208,15 +233,15 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void gated_norm_bwd_kernel(Gate
         Vec<IO, VEC>::load(x + c * VEC, u[i]);
         Vec<IO, VEC>::load(dy + c * VEC, du[i]);
         if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, gv[i]);
+        float f[VEC], d[VEC];
+        gate_values_d<VEC>(gv[i], a.act, f, d);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           u[i][e] *= r;
-          float d = 0.0f, act = 1.0f;
-          if (a.act >= 0) act = gate_value_d(gv[i][e], a.act, d);
-          const float dn = du[i][e];
-          dw[i][e] += dn * u[i][e] * act;
-          gv[i][e] = dn * u[i][e] * w[i][e] * d;
-          du[i][e] = dn * w[i][e] * act;
+          const float du_u = du[i][e] * u[i][e];
+          dw[i][e] += du_u * f[e];
+          gv[i][e] = du_u * w[i][e] * d[e];
+          du[i][e] *= w[i][e] * f[e];
           dot += du[i][e] * u[i][e];
         }
       }
@@ -238,8 +263,8 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void gated_norm_bwd_kernel(Gate
 }
 
 // ---------------------------------------------------------------- residual norm
-template <typename IO, typename RES, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_kernel(ResidualNormArgs a, int team) {
+template <typename IO, typename RES, int VEC, int NV, bool BLOCK, int THREADS>
+__global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs a, int team) {
   __shared__ float red[16];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
@@ -268,16 +293,13 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_kernel(Resid
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        float w1[VEC], sc[VEC];
-        if (a.w_post) Vec<float, VEC>::load(a.w_post + c * VEC, w1);
-        if (a.scale) Vec<float, VEC>::load(a.scale + c * VEC, sc);
+        float w1[VEC], sc[VEC], f[VEC];
+        load_or_one<VEC>(a.w_post, c, w1);
+        load_or_one<VEC>(a.scale, c, sc);
+        gate_values<VEC>(gv[i], a.act, f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float z = xv[i][e];
-          if (a.w_post) z *= r1 * w1[e];
-          if (a.act >= 0) z *= gate_value(gv[i][e], a.act);
-          if (a.scale) z *= sc[e];
-          hv[i][e] += z;
+          hv[i][e] += xv[i][e] * r1 * w1[e] * f[e] * sc[e];
           ss += hv[i][e] * hv[i][e];
         }
         Vec<RES, VEC>::store((RES *)a.h + row * a.dim + c * VEC, hv[i]);
@@ -303,14 +325,22 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_kernel(Resid
   }
 }
 
-template <typename IO, typename RES, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_bwd_kernel(ResidualNormArgs a, int team) {
+template <typename IO, typename RES, int VEC, int NV, bool BLOCK, int THREADS>
+__global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNormArgs a, int team) {
   __shared__ float red[16];
   __shared__ float cols[BLOCK ? 1 : 256 * VEC];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
   const int nv = a.dim / VEC;
   float dw2[NV][VEC] = {}, dw1[NV][VEC] = {}, ds[NV][VEC] = {};
+  // the weights of a thread's one vector stay in registers over its rows
+  constexpr bool KEEP = NV == 1;
+  float w2[VEC] = {}, w1[VEC] = {}, sc[VEC] = {};
+  if (KEEP && tm.lane < nv) {
+    Vec<float, VEC>::load(a.w_pre + tm.lane * VEC, w2);
+    load_or_one<VEC>(a.w_post, tm.lane, w1);
+    load_or_one<VEC>(a.scale, tm.lane, sc);
+  }
   for (int64_t row = (int64_t)blockIdx.x * per + (BLOCK ? 0 : threadIdx.x / team); row < a.tokens;
        row += (int64_t)gridDim.x * per) {
     const IO *x = (const IO *)a.x + row * a.x_stride;
@@ -318,7 +348,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_bwd_kernel(R
     const RES *res = (const RES *)a.residual + row * a.dim;
     const float r1 = a.rstd[2 * row], r2 = a.rstd[2 * row + 1];
     // h again, in fp32 as the forward formed it
-    float n[NV][VEC], gv[NV][VEC], u[NV][VEC], dy[NV][VEC], dot = 0.0f;
+    float n[NV][VEC], f[NV][VEC], df[NV][VEC], u[NV][VEC], dy[NV][VEC], dh[NV][VEC], dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
@@ -326,22 +356,32 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_bwd_kernel(R
         Vec<IO, VEC>::load(x + c * VEC, n[i]);
         Vec<RES, VEC>::load(res + c * VEC, u[i]);
         Vec<IO, VEC>::load((const IO *)a.dy + row * a.dim + c * VEC, dy[i]);
-        if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, gv[i]);
-        float w1[VEC], w2[VEC], sc[VEC];
-        Vec<float, VEC>::load(a.w_pre + c * VEC, w2);
-        if (a.w_post) Vec<float, VEC>::load(a.w_post + c * VEC, w1);
-        if (a.scale) Vec<float, VEC>::load(a.scale + c * VEC, sc);
+        if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, f[i]);
+        if (a.dh) {
+          Vec<RES, VEC>::load((const RES *)a.dh + row * a.dim + c * VEC, dh[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) dh[i][e] = 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = tm.lane + i * team;
+      if (c < nv) {
+        if constexpr (!KEEP) {
+          Vec<float, VEC>::load(a.w_pre + c * VEC, w2);
+          load_or_one<VEC>(a.w_post, c, w1);
+          load_or_one<VEC>(a.scale, c, sc);
+        }
+        gate_values_d<VEC>(f[i], a.act, f[i], df[i]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float z = n[i][e];
-          if (a.w_post) z *= r1 * w1[e];
-          if (a.act >= 0) z *= gate_value(gv[i][e], a.act);
-          if (a.scale) z *= sc[e];
-          u[i][e] = (u[i][e] + z) * r2;
+          n[i][e] *= r1;  // the normalised x (x itself without a post-norm: r1 is 1)
+          u[i][e] = (u[i][e] + n[i][e] * w1[e] * f[i][e] * sc[e]) * r2;
           dw2[i][e] += dy[i][e] * u[i][e];
           dy[i][e] *= w2[e];
           dot += dy[i][e] * u[i][e];
-          n[i][e] *= r1;  // the normalised x (x itself without a post-norm)
         }
       }
     }
@@ -351,69 +391,66 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void residual_norm_bwd_kernel(R
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        float dh[VEC], w1[VEC], sc[VEC], dg[VEC];
-        if (a.dh) Vec<RES, VEC>::load((const RES *)a.dh + row * a.dim + c * VEC, dh);
-        if (a.w_post) Vec<float, VEC>::load(a.w_post + c * VEC, w1);
-        if (a.scale) Vec<float, VEC>::load(a.scale + c * VEC, sc);
+        if constexpr (!KEEP) {
+          load_or_one<VEC>(a.w_post, c, w1);
+          load_or_one<VEC>(a.scale, c, sc);
+        }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float d = r2 * (dy[i][e] - u[i][e] * dot);
-          if (a.dh) d += dh[e];
-          dh[e] = d;
-          float act = 1.0f, dact = 0.0f;
-          if (a.act >= 0) act = gate_value_d(gv[i][e], a.act, dact);
-          const float z = a.w_post ? n[i][e] * w1[e] : n[i][e];
-          const float s = a.scale ? sc[e] : 1.0f;
-          dg[e] = d * s * z * dact;
-          if (a.scale) ds[i][e] += d * act * z;
-          d *= s * act;  // the gradient of z
-          if (a.w_post) {
-            dw1[i][e] += d * n[i][e];
-            d *= w1[e];
-            dot1 += d * n[i][e];
-          }
-          u[i][e] = d;
+          const float d = dh[i][e] + r2 * (dy[i][e] - u[i][e] * dot);
+          dh[i][e] = d;
+          const float dz = d * n[i][e] * w1[e];  // z dh: what the gate and the scale see
+          df[i][e] *= dz * sc[e];
+          ds[i][e] += dz * f[i][e];
+          const float t = d * sc[e] * f[i][e];  // the gradient of z
+          dw1[i][e] += t * n[i][e];
+          u[i][e] = t * w1[e];
+          dot1 += u[i][e] * n[i][e];
         }
-        Vec<RES, VEC>::store((RES *)a.dres + row * a.dim + c * VEC, dh);
-        if (a.act >= 0) Vec<IO, VEC>::store((IO *)a.dgate + row * a.dim + c * VEC, dg);
+        Vec<RES, VEC>::store((RES *)a.dres + row * a.dim + c * VEC, dh[i]);
+        if (a.act >= 0) Vec<IO, VEC>::store((IO *)a.dgate + row * a.dim + c * VEC, df[i]);
       }
     }
-    if (a.w_post) dot1 = tm.sum(dot1, red) / (float)a.dim;
+    // without a post-norm x's gradient is z's
+    dot1 = a.w_post ? tm.sum(dot1, red) / (float)a.dim : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        if (a.w_post) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) u[i][e] = r1 * (u[i][e] - n[i][e] * dot1);
-        }
+        for (int e = 0; e < VEC; ++e) u[i][e] = r1 * (u[i][e] - n[i][e] * dot1);
         Vec<IO, VEC>::store((IO *)a.dx + row * a.dim + c * VEC, u[i]);
       }
     }
   }
-  const int64_t plane = (int64_t)gridDim.x * a.dim;
-  write_partial<VEC, NV, BLOCK>(dw2, tm, a.dim, a.part, cols);
-  if (a.w_post) write_partial<VEC, NV, BLOCK>(dw1, tm, a.dim, a.part + plane, cols);
-  if (a.scale) write_partial<VEC, NV, BLOCK>(ds, tm, a.dim, a.part + 2 * plane, cols);
+  write_partial<VEC, NV, BLOCK>(dw2, tm, a.dim, a.part[0], cols);
+  if (a.w_post) write_partial<VEC, NV, BLOCK>(dw1, tm, a.dim, a.part[1], cols);
+  if (a.scale) write_partial<VEC, NV, BLOCK>(ds, tm, a.dim, a.part[2], cols);
 }
 
-// out[c] = sum over the blocks' partial rows, in a fixed order: 16 groups of
-// rows side by side, then the groups' sums.  blockIdx.y picks the weight.
-__global__ void norm_partials_kernel(const float *part, int blocks, int dim, float *o0, float *o1, float *o2) {
-  __shared__ float lds[16][64];
+// out[c] = sum over the workgroups' partial rows, in a fixed order: 64 groups of
+// rows side by side for 16 columns, then the groups' sums.  blockIdx.y picks the
+// weight.  512 rows of 128 columns: 9.6 us with 16 groups for 64 columns, PARTIALS_US
+// so.
+__global__ __launch_bounds__(1024) void norm_partials_kernel(const float *part, int blocks, int dim, float *o0, float *o1,
+                                                            float *o2) {
+  __shared__ float lds[16][16];
   float *out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 16 + (threadIdx.x & 15);
   float s = 0.0f;
   if (c < dim) {
     const float *p = part + (int64_t)blockIdx.y * blocks * dim + c;
-    for (int b = w; b < blocks; b += 16) s += p[(int64_t)b * dim];
+#pragma unroll 8
+    for (int b = threadIdx.x >> 4; b < blocks; b += 64) s += p[(int64_t)b * dim];
   }
-  lds[w][threadIdx.x & 63] = s;
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if ((threadIdx.x & 63) < 16) lds[threadIdx.x >> 6][threadIdx.x & 15] = s;
   __syncthreads();
-  if (w == 0 && c < dim) {
+  if (threadIdx.x < 16 && c < dim) {
     s = 0.0f;
-    for (int i = 0; i < 16; ++i) s += lds[i][threadIdx.x & 63];
+    for (int i = 0; i < 16; ++i) s += lds[i][threadIdx.x];
     out[c] = s;
   }
 }
@@ -429,39 +466,55 @@ bool aligned(const void *p, int64_t stride, int elem) {
   return ((uintptr_t)p & 15) == 0 && (stride * elem) % 16 == 0;
 }
 
-// The shape of a team for rows of nv vectors: `max_nv` vectors a thread at
-// most, a wave if that holds the row.
+// The shape of a team for rows of nv vectors.
 struct TeamPlan {
   int team, nv, block;
 };
-TeamPlan plan_team(int nv, int max_nv) {
-  const int wave = pow2_at_least((nv + max_nv - 1) / max_nv);
-  if (wave <= 64) {
-    // as many lanes as there are vectors, up to a wave; then more vectors a lane
+// Forward: a wave holds a row of up to 256 vectors (4 a lane), for the fewest
+// exchanges; longer rows take a workgroup.
+TeamPlan plan_forward(int nv) {
+  if (nv <= 256) {
     const int team = nv >= 64 ? 64 : pow2_at_least(nv);
     return {team, (nv + team - 1) / team, 0};
   }
-  return {wave, (nv + wave - 1) / wave, 1};
+  const int most = nv > 4096 ? 16 : 4;
+  const int team = pow2_at_least((nv + most - 1) / most);
+  return {team, (nv + team - 1) / team, 1};
+}
+// Reverse: the weights' sums stay in registers beside five inputs, so that a
+// thread holds one vector where 1024 threads can hold the row.
+TeamPlan plan_reverse(int nv) {
+  int team = pow2_at_least(nv);
+  if (team > 1024) team = 1024;
+  return {team, (nv + team - 1) / team, team > 64};
 }
 
 }  // namespace
 
-#define NORM_LAUNCH(NV, BLK, KERNEL, ...)                                                          \
-  KERNEL<__VA_ARGS__, NV, BLK><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
-#define NORM_PICK(KERNEL, ...)                                                                     \
+#define NORM_LAUNCH(NV, BLK, THREADS, KERNEL, ...)                                                 \
+  KERNEL<__VA_ARGS__, NV, BLK, THREADS><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
+// The last type argument is the vector's width: rows of more than 4 vectors a
+// thread are those of single elements.
+#define NORM_PICK_BLOCK(KERNEL, VEC, ...)                                                          \
   do {                                                                                             \
-    if (grid == 0) break; /* no rows: the reverse modes still write their weights' sums */         \
-    if (p.block) {                                                                                 \
-      if (p.nv <= 4) NORM_LAUNCH(4, true, KERNEL, __VA_ARGS__);                                    \
-      else NORM_LAUNCH(16, true, KERNEL, __VA_ARGS__);                                             \
-    } else if (p.nv == 1) NORM_LAUNCH(1, false, KERNEL, __VA_ARGS__);                              \
-    else if (p.nv == 2) NORM_LAUNCH(2, false, KERNEL, __VA_ARGS__);                                \
-    else NORM_LAUNCH(4, false, KERNEL, __VA_ARGS__);                                               \
+    if (p.nv <= 4) NORM_LAUNCH(4, true, 1024, KERNEL, __VA_ARGS__, VEC);                           \
+    else if constexpr (VEC == 1) NORM_LAUNCH(16, true, 1024, KERNEL, __VA_ARGS__, VEC);            \
   } while (0)
-
-// vectors a thread holds at most: 4, or 16 single elements where the row
-// needs more than 1024 threads of 4
-static TeamPlan plan_rows(int nv) { return plan_team(nv, nv > 4096 ? 16 : 4); }
+#define NORM_PICK_FORWARD(KERNEL, VEC, ...)                                                        \
+  do {                                                                                             \
+    if (p.block) NORM_PICK_BLOCK(KERNEL, VEC, __VA_ARGS__);                                        \
+    else if (p.nv == 1) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);                      \
+    else if (p.nv == 2) NORM_LAUNCH(2, false, 256, KERNEL, __VA_ARGS__, VEC);                      \
+    else NORM_LAUNCH(4, false, 256, KERNEL, __VA_ARGS__, VEC);                                     \
+  } while (0)
+#define NORM_PICK_REVERSE(KERNEL, VEC, ...)                                                        \
+  do {                                                                                             \
+    if (grid == 0) break; /* no rows: the weights' sums are still written */                       \
+    if (!p.block) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);                            \
+    else if (p.nv > 1) NORM_PICK_BLOCK(KERNEL, VEC, __VA_ARGS__);                                  \
+    else if (p.team <= 256) NORM_LAUNCH(1, true, 256, KERNEL, __VA_ARGS__, VEC);                   \
+    else NORM_LAUNCH(1, true, 1024, KERNEL, __VA_ARGS__, VEC);                                     \
+  } while (0)
 
 static int row_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
   const int64_t per = p.block ? 1 : 256 / p.team;
@@ -469,41 +522,54 @@ static int row_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
   return (int)(n < most ? n : most);
 }
 
+// Workgroups of a reverse mode: one alone where it passes the rows in four steps
+// (its sums are the weights' gradients: no second launch), else up to `most`.
+static int reverse_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
+  const int64_t per = p.block ? 1 : 256 / p.team;
+  if (rows > 0 && rows <= 4 * per) return 1;
+  if (p.team >= 512) most = most < 256 * (1024 / p.team) ? most : 256 * (1024 / p.team);
+  return row_blocks(rows, p, most);
+}
+
 hipError_t launch_gated_norm(const GatedNormArgs &a, hipStream_t st) {
   const int64_t rows = a.tokens * a.heads;
   const int e = a.bf16 ? 2 : 4, vec = 16 / e;
   const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.y, a.dim, e) &&
                     aligned(a.weight, 4, 4) && (a.act < 0 || aligned(a.gate, a.gate_stride, e));
-  const TeamPlan p = plan_rows(wide ? a.dim / vec : a.dim);
+  const TeamPlan p = plan_forward(wide ? a.dim / vec : a.dim);
   const int grid = row_blocks(rows, p, 1 << 20);
   TimedLaunch tl(K_NORM, st);
   if (a.bf16) {
-    if (wide) NORM_PICK(gated_norm_kernel, u16, 8);
-    else NORM_PICK(gated_norm_kernel, u16, 1);
+    if (wide) NORM_PICK_FORWARD(gated_norm_kernel, 8, u16);
+    else NORM_PICK_FORWARD(gated_norm_kernel, 1, u16);
   } else {
-    if (wide) NORM_PICK(gated_norm_kernel, float, 4);
-    else NORM_PICK(gated_norm_kernel, float, 1);
+    if (wide) NORM_PICK_FORWARD(gated_norm_kernel, 4, float);
+    else NORM_PICK_FORWARD(gated_norm_kernel, 1, float);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_gated_norm_bwd(const GatedNormArgs &a, hipStream_t st) {
+hipError_t launch_gated_norm_bwd(const GatedNormArgs &args, hipStream_t st) {
+  GatedNormArgs a = args;
   const int64_t rows = a.tokens * a.heads;
   const int e = a.bf16 ? 2 : 4, vec = 16 / e;
   const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.dy, a.dy_stride, e) &&
-                    aligned(a.dx, a.dim, e) && aligned(a.weight, 4, 4) && aligned(a.part, a.dim, 4) &&
+                    aligned(a.dx, a.dim, e) && aligned(a.weight, 4, 4) && aligned(a.dweight, a.dim, 4) &&
                     (a.act < 0 || (aligned(a.gate, a.gate_stride, e) && aligned(a.dgate, a.dim, e)));
-  const TeamPlan p = plan_rows(wide ? a.dim / vec : a.dim);
-  const int grid = row_blocks(rows, p, norm_bwd_blocks(rows));
+  const TeamPlan p = plan_reverse(wide ? a.dim / vec : a.dim);
+  const int grid = reverse_blocks(rows, p, norm_bwd_blocks(rows, a.dim));
+  float *const part = a.part;
+  if (grid == 1) a.part = a.dweight;
   TimedLaunch tl(K_NORM_BWD, st);
   if (a.bf16) {
-    if (wide) NORM_PICK(gated_norm_bwd_kernel, u16, 8);
-    else NORM_PICK(gated_norm_bwd_kernel, u16, 1);
+    if (wide) NORM_PICK_REVERSE(gated_norm_bwd_kernel, 8, u16);
+    else NORM_PICK_REVERSE(gated_norm_bwd_kernel, 1, u16);
   } else {
-    if (wide) NORM_PICK(gated_norm_bwd_kernel, float, 4);
-    else NORM_PICK(gated_norm_bwd_kernel, float, 1);
+    if (wide) NORM_PICK_REVERSE(gated_norm_bwd_kernel, 4, float);
+    else NORM_PICK_REVERSE(gated_norm_bwd_kernel, 1, float);
   }
-  norm_partials_kernel<<<dim3((a.dim + 63) / 64, 1), 1024, 0, st>>>(a.part, grid, a.dim, a.dweight, nullptr, nullptr);
+  if (grid != 1)
+    norm_partials_kernel<<<dim3((a.dim + 15) / 16, 1), 1024, 0, st>>>(part, grid, a.dim, a.dweight, nullptr, nullptr);
   return hipGetLastError();
 }
 
@@ -513,48 +579,59 @@ hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t st) {
                     aligned(a.h, a.dim, re) && aligned(a.y, a.dim, e) && aligned(a.w_pre, 4, 4) &&
                     (!a.w_post || aligned(a.w_post, 4, 4)) && (!a.scale || aligned(a.scale, 4, 4)) &&
                     (a.act < 0 || aligned(a.gate, a.gate_stride, e));
-  const TeamPlan p = plan_rows(wide ? a.dim / vec : a.dim);
+  const TeamPlan p = plan_forward(wide ? a.dim / vec : a.dim);
   const int grid = row_blocks(a.tokens, p, 1 << 20);
   TimedLaunch tl(K_NORM, st);
   if (a.bf16) {
     if (a.res_bf16) {
-      if (wide) NORM_PICK(residual_norm_kernel, u16, u16, 8);
-      else NORM_PICK(residual_norm_kernel, u16, u16, 1);
+      if (wide) NORM_PICK_FORWARD(residual_norm_kernel, 8, u16, u16);
+      else NORM_PICK_FORWARD(residual_norm_kernel, 1, u16, u16);
     } else {
-      if (wide) NORM_PICK(residual_norm_kernel, u16, float, 8);
-      else NORM_PICK(residual_norm_kernel, u16, float, 1);
+      if (wide) NORM_PICK_FORWARD(residual_norm_kernel, 8, u16, float);
+      else NORM_PICK_FORWARD(residual_norm_kernel, 1, u16, float);
     }
   } else {
-    if (wide) NORM_PICK(residual_norm_kernel, float, float, 4);
-    else NORM_PICK(residual_norm_kernel, float, float, 1);
+    if (wide) NORM_PICK_FORWARD(residual_norm_kernel, 4, float, float);
+    else NORM_PICK_FORWARD(residual_norm_kernel, 1, float, float);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t st) {
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs &args, hipStream_t st) {
+  ResidualNormArgs a = args;
   const int e = a.bf16 ? 2 : 4, re = a.res_bf16 ? 2 : 4, vec = 16 / e;
   const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.residual, a.dim, re) &&
                     aligned(a.dy, a.dim, e) && aligned(a.dx, a.dim, e) && aligned(a.dres, a.dim, re) &&
-                    (!a.dh || aligned(a.dh, a.dim, re)) && aligned(a.part, a.dim, 4) && aligned(a.w_pre, 4, 4) &&
+                    (!a.dh || aligned(a.dh, a.dim, re)) && aligned(a.dw_pre, a.dim, 4) &&
+                    (!a.w_post || aligned(a.dw_post, a.dim, 4)) && (!a.scale || aligned(a.dscale, a.dim, 4)) && aligned(a.w_pre, 4, 4) &&
                     (!a.w_post || aligned(a.w_post, 4, 4)) && (!a.scale || aligned(a.scale, 4, 4)) &&
                     (a.act < 0 || (aligned(a.gate, a.gate_stride, e) && aligned(a.dgate, a.dim, e)));
-  const TeamPlan p = plan_rows(wide ? a.dim / vec : a.dim);
-  const int grid = row_blocks(a.tokens, p, norm_bwd_blocks(a.tokens));
+  const TeamPlan p = plan_reverse(wide ? a.dim / vec : a.dim);
+  const int grid = reverse_blocks(a.tokens, p, norm_bwd_blocks(a.tokens, a.dim));
+  float *const part = a.part[0];
+  a.part[1] = part + (int64_t)grid * a.dim;
+  a.part[2] = part + 2 * (int64_t)grid * a.dim;
+  if (grid == 1) {
+    a.part[0] = a.dw_pre;
+    a.part[1] = a.dw_post;
+    a.part[2] = a.dscale;
+  }
   TimedLaunch tl(K_NORM_BWD, st);
   if (a.bf16) {
     if (a.res_bf16) {
-      if (wide) NORM_PICK(residual_norm_bwd_kernel, u16, u16, 8);
-      else NORM_PICK(residual_norm_bwd_kernel, u16, u16, 1);
+      if (wide) NORM_PICK_REVERSE(residual_norm_bwd_kernel, 8, u16, u16);
+      else NORM_PICK_REVERSE(residual_norm_bwd_kernel, 1, u16, u16);
     } else {
-      if (wide) NORM_PICK(residual_norm_bwd_kernel, u16, float, 8);
-      else NORM_PICK(residual_norm_bwd_kernel, u16, float, 1);
+      if (wide) NORM_PICK_REVERSE(residual_norm_bwd_kernel, 8, u16, float);
+      else NORM_PICK_REVERSE(residual_norm_bwd_kernel, 1, u16, float);
     }
   } else {
-    if (wide) NORM_PICK(residual_norm_bwd_kernel, float, float, 4);
-    else NORM_PICK(residual_norm_bwd_kernel, float, float, 1);
+    if (wide) NORM_PICK_REVERSE(residual_norm_bwd_kernel, 4, float, float);
+    else NORM_PICK_REVERSE(residual_norm_bwd_kernel, 1, float, float);
   }
-  norm_partials_kernel<<<dim3((a.dim + 63) / 64, 3), 1024, 0, st>>>(
-      a.part, grid, a.dim, a.dw_pre, a.w_post ? a.dw_post : nullptr, a.scale ? a.dscale : nullptr);
+  if (grid != 1)
+    norm_partials_kernel<<<dim3((a.dim + 15) / 16, 3), 1024, 0, st>>>(
+        part, grid, a.dim, a.dw_pre, a.w_post ? a.dw_post : nullptr, a.scale ? a.dscale : nullptr);
   return hipGetLastError();
 }
 

@@ -13,70 +13,88 @@ namespace {
 
 constexpr int kThreads = 512;
 
+// n / page for n < 2^31 as a product: with s = ceil(log2 page) and m =
+// floor(2^(31 + s) / page) + 1 (below 2^32), m page = 2^(31 + s) + e with
+// 0 < e <= page <= 2^s, so that n m / 2^(31 + s) lies above n / page by less than
+// n / 2^31 / page < 1 / page: never at or beyond the next whole number.
+struct PageDiv {
+  uint32_t m;
+  int shift;
+};
+__device__ __forceinline__ int32_t div_page(uint32_t n, const PageDiv &d) {
+  return (int32_t)(((uint64_t)n * d.m) >> d.shift);
+}
+// Pages that n tokens take.
+__device__ __forceinline__ int32_t pages_of(uint32_t n, const PageDiv &d) { return n ? div_page(n - 1, d) + 1 : 0; }
+
 // Every workgroup scans all lengths (8 bytes a request, from the L2) and keeps
 // the two offsets of each request in LDS; then it fills its own share of the
 // rows.  One launch instead of a scan and a fill.
-__global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a, int rows_per_block) {
+__global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a, PageDiv pd, int rows_per_block) {
   extern __shared__ int32_t lds[];
-  int32_t *cu = lds, *first = lds + a.num_req;  // tokens and new pages before each request
+  // of each request: tokens and new pages before it, and the tokens it holds
+  int32_t *cu = lds, *first = lds + a.num_req, *have = lds + 2 * a.num_req;
   __shared__ int64_t wave_tok[kThreads / 64], wave_pg[kThreads / 64];
   __shared__ int bad;
   const int R = a.num_req, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (tid == 0) bad = 0;
-  __syncthreads();
-  const int64_t limit = (int64_t)a.max_pages * a.page;
-  int64_t tok0 = 0, pg0 = 0;
-  int why = 0;  // the largest of the thread's reasons
-  for (int base = 0; base < R; base += kThreads) {
-    const int r = base + tid;
-    int64_t held = 0, fresh = 0;
-    int64_t tokens = 0;
-    if (r < R) {
-      held = a.seq_lens[r];
-      tokens = a.new_lens[r];
-      if (held < 0 || tokens < 0) {
-        why = FLARE_TABLES_BAD_LENGTH;
-        held = tokens = 0;
-      }
-      if (held + tokens > limit || held + tokens + a.position_offset > INT32_MAX) {
-        why = why > FLARE_TABLES_TOO_LONG ? why : FLARE_TABLES_TOO_LONG;
-      }
-      fresh = (held + tokens + a.page - 1) / a.page - (held + a.page - 1) / a.page;
-    }
-    int64_t st = tokens, sp = fresh;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t ut = __shfl_up(st, o), up = __shfl_up(sp, o);
-      if (lane >= o) {
-        st += ut;
-        sp += up;
-      }
-    }
-    if (lane == 63) {
-      wave_tok[wave] = st;
-      wave_pg[wave] = sp;
-    }
-    __syncthreads();
-    int64_t bt = tok0, bp = pg0;
-    for (int w = 0; w < kThreads / 64; ++w) {
-      if (w < wave) {
-        bt += wave_tok[w];
-        bp += wave_pg[w];
-      }
-      tok0 += wave_tok[w];
-      pg0 += wave_pg[w];
-    }
-    if (r < R) {
-      // beyond 32 bits only where the call is refused below
-      cu[r] = (int32_t)(bt + st - tokens);
-      first[r] = (int32_t)(bp + sp - fresh);
-    }
-    __syncthreads();
-  }
   const int32_t used = *a.pages_used;
-  if (used < 0) why = FLARE_TABLES_BAD_LENGTH;
+  if (tid == 0) bad = 0;
+  for (int r = tid; r < R; r += kThreads) {
+    have[r] = a.seq_lens[r];
+    cu[r] = a.new_lens[r];
+  }
+  __syncthreads();
+  // a thread sums a run of requests, the workgroup scans the threads' sums once
+  const int64_t limit = (int64_t)a.max_pages * a.page;
+  const int run = (R + kThreads - 1) / kThreads, r0 = tid * run, r1 = r0 + run < R ? r0 + run : R;
+  int64_t tokens = 0, pages = 0;
+  int why = 0;  // the largest of the thread's reasons
+  for (int r = r0; r < r1; ++r) {
+    const int64_t held = have[r], add = cu[r];
+    if (held < 0 || add < 0) {
+      why = FLARE_TABLES_BAD_LENGTH;
+    } else {
+      if ((held + add > limit || held + add + a.position_offset > INT32_MAX) && why < FLARE_TABLES_TOO_LONG)
+        why = FLARE_TABLES_TOO_LONG;
+      tokens += add;
+      if (held + add <= INT32_MAX) pages += pages_of((uint32_t)(held + add), pd) - pages_of((uint32_t)held, pd);
+    }
+  }
+  int64_t st = tokens, sp = pages;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t ut = __shfl_up(st, o), up = __shfl_up(sp, o);
+    if (lane >= o) {
+      st += ut;
+      sp += up;
+    }
+  }
+  if (lane == 63) {
+    wave_tok[wave] = st;
+    wave_pg[wave] = sp;
+  }
   if (why) atomicMax(&bad, why);
   __syncthreads();
-  int status = bad;
+  int64_t tok0 = 0, pg0 = 0;  // totals
+  st -= tokens;
+  sp -= pages;
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w < wave) {
+      st += wave_tok[w];
+      sp += wave_pg[w];
+    }
+    tok0 += wave_tok[w];
+    pg0 += wave_pg[w];
+  }
+  // beyond 32 bits only where the call is refused below
+  for (int r = r0; r < r1; ++r) {
+    const uint32_t held = (uint32_t)have[r], add = (uint32_t)cu[r];
+    cu[r] = (int32_t)st;
+    first[r] = (int32_t)sp;
+    st += add;
+    sp += pages_of(held + add, pd) - pages_of(held, pd);
+  }
+  __syncthreads();
+  int status = used < 0 ? FLARE_TABLES_BAD_LENGTH : bad;
   if (status == 0 && tok0 > a.max_tokens) status = FLARE_TABLES_TOO_MANY_TOKENS;
   if (status == 0 && used + pg0 > a.num_free) status = FLARE_TABLES_NO_PAGES;
   const int64_t total = status ? 0 : tok0;
@@ -84,54 +102,77 @@ __global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a,
   // the per-request outputs, spread over the workgroups
   for (int r = blockIdx.x * kThreads + tid; r < R; r += gridDim.x * kThreads) {
     a.cu_new[r] = status ? 0 : cu[r];
-    a.seq_lens_out[r] = a.seq_lens[r] + (status ? 0 : a.new_lens[r]);
+    a.seq_lens_out[r] = have[r] + (status ? 0 : a.new_lens[r]);
   }
   if (blockIdx.x == 0 && tid == 0) {
     a.cu_new[R] = (int32_t)total;
     *a.pages_used_out = used + (status ? 0 : (int32_t)pg0);
     *a.status = status;
   }
+  // four rows of a thread side by side: their searches and page loads overlap
   const int64_t row0 = (int64_t)blockIdx.x * rows_per_block;
-  for (int i = tid; i < rows_per_block; i += kThreads) {
-    const int64_t row = row0 + i;
-    if (row >= a.max_tokens) break;
-    if (row >= total) {
-      a.positions[row] = 0;
-      a.slots[row] = -1;
-      continue;
+  int top = 1;
+  while (2 * top < R) top *= 2;
+  for (int i = tid; i < rows_per_block; i += 4 * kThreads) {
+    int req[4];
+    int32_t id[4], pos[4];
+    bool live[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      req[k] = 0;
+      live[k] = i + k * kThreads < rows_per_block && row0 + i + k * kThreads < total;
     }
-    // the request of this row: the last one that starts at or before it
-    int lo = 0, hi = R - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu[mid] <= (int32_t)row) lo = mid;
-      else hi = mid - 1;
+    // the request of a row: the last one that starts at or before it (no branches:
+    // the four rows' LDS reads and page loads are then in flight together)
+    for (int step = top; step > 0; step >>= 1) {
+      int32_t at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at[k] = cu[req[k] + step < R ? req[k] + step : req[k]];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        req[k] += req[k] + step < R && at[k] <= (int32_t)(row0 + i + k * kThreads) ? step : 0;
     }
-    const int32_t held = a.seq_lens[lo];
-    const int32_t pos = held + ((int32_t)row - cu[lo]);
-    const int32_t pg = pos / a.page, have = (held + a.page - 1) / a.page;
-    int32_t *entry = a.block_table + (int64_t)lo * a.max_pages + pg;
-    int32_t id;
-    if (pg >= have) {
-      id = a.free_pages[used + first[lo] + pg - have];
+    const int32_t *from[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = req[k];
+      const int32_t held = have[r];
+      pos[k] = held + ((int32_t)(row0 + i + k * kThreads) - cu[r]);
+      const int32_t pg = div_page(pos[k], pd), old = pages_of(held, pd);
+      from[k] = pg >= old ? a.free_pages + (used + first[r] + pg - old) : a.block_table + ((int64_t)r * a.max_pages + pg);
+      if (!live[k]) from[k] = a.pages_used;  // padding: any readable place
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) id[k] = *from[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t row = row0 + i + k * kThreads;
+      if (i + k * kThreads >= rows_per_block || row >= a.max_tokens) continue;
+      const int32_t pg = div_page(pos[k], pd), off = pos[k] - pg * a.page;
       // the row that opens a page enters it into the table
-      if (pos == pg * a.page) *entry = id;
-    } else {
-      id = *entry;
+      if (live[k] && off == 0 && pg >= pages_of(have[req[k]], pd))
+        a.block_table[(int64_t)req[k] * a.max_pages + pg] = id[k];
+      a.positions[row] = live[k] ? pos[k] + a.position_offset : 0;
+      a.slots[row] = live[k] ? (int64_t)id[k] * a.page + off : -1;
     }
-    a.positions[row] = pos + a.position_offset;
-    a.slots[row] = (int64_t)id * a.page + (pos - pg * a.page);
   }
 }
 
 }  // namespace
 
 hipError_t launch_step_tables(const StepTablesArgs &a, hipStream_t st) {
-  int rows = 1024;
+  // few workgroups where there are many rows: each of them scans all lengths
+  int64_t rows = (a.max_tokens + 511) / 512;
+  rows = rows < 1024 ? 1024 : (rows + kThreads - 1) / kThreads * kThreads;
   int64_t grid = (a.max_tokens + rows - 1) / rows;
   if (grid < 1) grid = 1;
+  PageDiv pd;
+  int log = 0;
+  while (((int64_t)1 << log) < a.page) ++log;
+  pd.m = (uint32_t)((((uint64_t)1 << (31 + log)) / a.page) + 1);
+  pd.shift = 31 + log;
   TimedLaunch tl(K_STEP_TABLES, st);
-  step_tables_kernel<<<(int)grid, kThreads, (size_t)2 * (a.num_req > 0 ? a.num_req : 1) * sizeof(int32_t), st>>>(a, rows);
+  step_tables_kernel<<<(int)grid, kThreads, (size_t)3 * (a.num_req > 0 ? a.num_req : 1) * sizeof(int32_t), st>>>(a, pd, (int)rows);
   return hipGetLastError();
 }
 

@@ -14,7 +14,18 @@ import math
 
 import numpy as np
 
-from . import (BF16, F32, _chk, _chk_buf, _fail, _gpu_device, _io_dtype_of, _ptr, _torch, _check, lib)
+from . import BF16, F32, _check, _chk, _chk_buf, _fail, _gpu_device, _io_dtype_of, lib
+
+_module = None
+
+
+def _torch():
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
+
 
 LINEAR, SILU, SIGMOID = 0, 1, 2
 TABLES_OK, TABLES_NO_PAGES, TABLES_TOO_MANY_TOKENS, TABLES_TOO_LONG, TABLES_BAD_LENGTH = 0, 1, 2, 3, 4
@@ -57,12 +68,19 @@ def declare(L):
 
 def _run(dev, fn, *args):
     """fn(*args, stream) with the tensors' device current, on its current stream."""
-    torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    C = _torch()._C
+    index = dev.index
+    if C._cuda_getDevice() == index:
+        status = fn(*args, C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with _torch().cuda.device(dev):
+            status = fn(*args, C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _token_rows(t, name, shape, dtype, dev):
@@ -72,10 +90,12 @@ def _token_rows(t, name, shape, dtype, dev):
         _fail("%s is required" % name, 1)
     if t.dtype != dtype:
         _fail("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _fail("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.device != dev:
         _fail("%s is on %s, expected %s" % (name, t.device, dev))
+    if shape[0] > 1 and t.is_contiguous():
+        return t.numel() // shape[0]
     row, strides = 1, t.stride()
     for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
         if size != 1 and stride != row:
