@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include "device_common.h"
+#include "fast_div.h"
 #include "layer_launch.h"
 
 namespace flare {
@@ -56,38 +57,49 @@ __device__ __forceinline__ float2 turn(int32_t position, double freq, float m, f
   return make_float2(m * c, m * sign * s);
 }
 
+struct RotaryPlan {
+  int tb;                            // tokens a workgroup
+  FastDiv half, items, per, v_per;   // by half, a token's, a head's and a value head's work items
+};
+
 // One workgroup: `tb` tokens.  Their coefficients first, to LDS, so that a
 // token's angles are formed once for all its heads; then the heads' vectors.
+// A head's work items hold two vectors each, so that a thread has two loads in
+// flight.  First those that turn: a vector of each half (of a pair's two elements
+// where vec is 1), or in the interleaved layout two whole vectors; then copies.  A
+// count that is odd leaves the last item one vector.
+__host__ __device__ inline int turned_items(const RotaryArgs &a, int vec) {
+  return a.interleaved && vec > 1 ? (2 * a.half / vec + 1) / 2 : a.half / vec;
+}
+__host__ __device__ inline int copy_items(int channels, int vec) { return (channels / vec + 1) / 2; }
+
 template <typename IO, int VEC>
-__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int tb) {
+__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, RotaryPlan p) {
   extern __shared__ float2 coef[];  // [tb][half]
-  const int64_t t0 = (int64_t)blockIdx.x * tb;
-  const int n = (int)(a.tokens - t0 < tb ? a.tokens - t0 : tb);
+  const int64_t t0 = (int64_t)blockIdx.x * p.tb;
+  const int n = (int)(a.tokens - t0 < p.tb ? a.tokens - t0 : p.tb);
   for (int i = threadIdx.x; i < n * a.half; i += blockDim.x) {
-    const int t = i / a.half, j = i - t * a.half;
+    const int t = fast_div(i, p.half), j = i - t * a.half;
     coef[i] = turn(a.positions[t0 + t], a.freqs[j], a.mscale, a.sign);
   }
   __syncthreads();
-  // a head's work items: those that turn (a vector of each half; in the
-  // interleaved layout one vector, or one pair where VEC is 1), then copies
-  const int turned = a.interleaved && VEC > 1 ? 2 * a.half / VEC : a.half / VEC;
-  const int per = turned + (a.dim - 2 * a.half) / VEC;
+  const int turned = turned_items(a, VEC), per = turned + copy_items(a.dim - 2 * a.half, VEC);
   const int heads = a.q_heads + a.k_heads;
-  const int v_per = a.slots ? a.dim / VEC : 0;
+  const int v_per = a.slots ? copy_items(a.dim, VEC) : 0;
   const int items = heads * per + a.k_heads * v_per;
   const int64_t cache_tokens = a.num_pages * a.page;
   for (int i = threadIdx.x; i < n * items; i += blockDim.x) {
-    const int t = i / items, r = i - t * items;
+    const int t = fast_div(i, p.items), r = i - t * items;
     const int64_t tok = t0 + t;
     int head, j, kind;  // kind 0 q, 1 k, 2 v
     if (r < heads * per) {
-      head = r / per;
+      head = fast_div(r, p.per);
       j = r - head * per;
       kind = head >= a.q_heads;
       if (kind) head -= a.q_heads;
     } else {
       const int rv = r - heads * per;
-      head = rv / v_per;
+      head = fast_div(rv, p.v_per);
       j = rv - head * v_per;
       kind = 2;
     }
@@ -110,36 +122,50 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int tb) {
       }
     }
     const float2 *cf = coef + t * a.half;
-    Pack<IO, VEC> x, y;
-    if (kind == 2 || j >= turned) {
-      const int c = kind == 2 ? j * VEC : 2 * a.half + (j - turned) * VEC;
-      x.load(src + c);
-      x.store(dst + c);
-    } else if (!a.interleaved || VEC == 1) {
-      // VEC == 1: a single pair of either layout
-      const int c0 = a.interleaved ? 2 * j : j * VEC, c1 = a.interleaved ? 2 * j + 1 : a.half + j * VEC;
-      x.load(src + c0);
-      y.load(src + c1);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float2 w = cf[j * VEC + e];
-        const float u = x.f[e], v = y.f[e];
-        x.f[e] = u * w.x - v * w.y;
-        y.f[e] = u * w.y + v * w.x;
-      }
-      x.store(dst + c0);
-      y.store(dst + c1);
+    // the item's two places in the row; c1 < 0: it has one
+    const bool copy = kind == 2 || j >= turned;
+    int c0, c1;
+    if (copy) {
+      const int first = kind == 2 ? 0 : 2 * a.half, vecs = (a.dim - first) / VEC;
+      c0 = first + 2 * (kind == 2 ? j : j - turned) * VEC;
+      c1 = c0 + VEC < first + vecs * VEC ? c0 + VEC : -1;
+    } else if (!a.interleaved) {
+      c0 = j * VEC;
+      c1 = a.half + c0;
+    } else if (VEC == 1) {
+      c0 = 2 * j;
+      c1 = c0 + 1;
     } else {
-      x.load(src + j * VEC);
-#pragma unroll
-      for (int e = 0; e + 1 < VEC; e += 2) {
-        const float2 w = cf[(j * VEC + e) / 2];
-        const float u = x.f[e], v = x.f[e + 1];
-        x.f[e] = u * w.x - v * w.y;
-        x.f[e + 1] = u * w.y + v * w.x;
-      }
-      x.store(dst + j * VEC);
+      c0 = 2 * j * VEC;
+      c1 = c0 + VEC < 2 * a.half ? c0 + VEC : -1;
     }
+    Pack<IO, VEC> x, y;
+    x.load(src + c0);
+    y.load(src + (c1 < 0 ? c0 : c1));
+    if (!copy) {
+      if (!a.interleaved || VEC == 1) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 w = cf[j * VEC + e];
+          const float u = x.f[e], v = y.f[e];
+          x.f[e] = u * w.x - v * w.y;
+          y.f[e] = u * w.y + v * w.x;
+        }
+      } else {
+        const float2 *cx = cf + c0 / 2, *cy = cf + (c1 < 0 ? c0 : c1) / 2;
+#pragma unroll
+        for (int e = 0; e + 1 < VEC; e += 2) {
+          const float2 w = cx[e / 2], z = cy[e / 2];
+          const float u = x.f[e], v = x.f[e + 1], s = y.f[e], t2 = y.f[e + 1];
+          x.f[e] = u * w.x - v * w.y;
+          x.f[e + 1] = u * w.y + v * w.x;
+          y.f[e] = s * z.x - t2 * z.y;
+          y.f[e + 1] = s * z.y + t2 * z.x;
+        }
+      }
+    }
+    x.store(dst + c0);
+    if (c1 >= 0) y.store(dst + c1);
   }
 }
 
@@ -159,17 +185,25 @@ hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st) {
     else
       wide = wide && vec_ok(a.k_out, a.dim, e);
   }
-  int tb = 1;
-  while (tb < 8 && a.tokens / (2 * tb) >= 4096 && 2 * tb * a.half <= 2048) tb *= 2;
-  const int grid = (int)((a.tokens + tb - 1) / tb);
-  const size_t lds = (size_t)tb * (a.half > 0 ? a.half : 1) * sizeof(float2);
+  RotaryPlan p;
+  p.tb = 1;
+  while (p.tb < 8 && a.tokens / (2 * p.tb) >= 4096 && 2 * p.tb * a.half <= 2048) p.tb *= 2;
+  const int v = wide ? vec : 1, per = turned_items(a, v) + copy_items(a.dim - 2 * a.half, v);
+  const int v_per = a.slots ? copy_items(a.dim, v) : 0;
+  const int items = (a.q_heads + a.k_heads) * per + a.k_heads * v_per;
+  p.half = make_fast_div(a.half > 0 ? a.half : 1);
+  p.items = make_fast_div(items);
+  p.per = make_fast_div(per);
+  p.v_per = make_fast_div(v_per > 0 ? v_per : 1);
+  const int grid = (int)((a.tokens + p.tb - 1) / p.tb);
+  const size_t lds = (size_t)p.tb * (a.half > 0 ? a.half : 1) * sizeof(float2);
   TimedLaunch tl(K_ROTARY, st);
   if (a.bf16) {
-    if (wide) rotary_kernel<u16, 8><<<grid, 256, lds, st>>>(a, tb);
-    else rotary_kernel<u16, 1><<<grid, 256, lds, st>>>(a, tb);
+    if (wide) rotary_kernel<u16, 8><<<grid, 256, lds, st>>>(a, p);
+    else rotary_kernel<u16, 1><<<grid, 256, lds, st>>>(a, p);
   } else {
-    if (wide) rotary_kernel<float, 4><<<grid, 256, lds, st>>>(a, tb);
-    else rotary_kernel<float, 1><<<grid, 256, lds, st>>>(a, tb);
+    if (wide) rotary_kernel<float, 4><<<grid, 256, lds, st>>>(a, p);
+    else rotary_kernel<float, 1><<<grid, 256, lds, st>>>(a, p);
   }
   return hipGetLastError();
 }

@@ -6,6 +6,7 @@
 //   free_pages[used + sum_{s<r} (need_s - have_s)] on.
 #include <hip/hip_runtime.h>
 
+#include "fast_div.h"
 #include "layer_launch.h"
 
 namespace flare {
@@ -13,24 +14,13 @@ namespace {
 
 constexpr int kThreads = 512;
 
-// n / page for n < 2^31 as a product: with s = ceil(log2 page) and m =
-// floor(2^(31 + s) / page) + 1 (below 2^32), m page = 2^(31 + s) + e with
-// 0 < e <= page <= 2^s, so that n m / 2^(31 + s) lies above n / page by less than
-// n / 2^31 / page < 1 / page: never at or beyond the next whole number.
-struct PageDiv {
-  uint32_t m;
-  int shift;
-};
-__device__ __forceinline__ int32_t div_page(uint32_t n, const PageDiv &d) {
-  return (int32_t)(((uint64_t)n * d.m) >> d.shift);
-}
 // Pages that n tokens take.
-__device__ __forceinline__ int32_t pages_of(uint32_t n, const PageDiv &d) { return n ? div_page(n - 1, d) + 1 : 0; }
+__device__ __forceinline__ int32_t pages_of(uint32_t n, const FastDiv &d) { return n ? fast_div(n - 1, d) + 1 : 0; }
 
 // Every workgroup scans all lengths (8 bytes a request, from the L2) and keeps
 // the two offsets of each request in LDS; then it fills its own share of the
 // rows.  One launch instead of a scan and a fill.
-__global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a, PageDiv pd, int rows_per_block) {
+__global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a, FastDiv pd, int rows_per_block) {
   extern __shared__ int32_t lds[];
   // of each request: tokens and new pages before it, and the tokens it holds
   int32_t *cu = lds, *first = lds + a.num_req, *have = lds + 2 * a.num_req;
@@ -138,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a,
       const int r = req[k];
       const int32_t held = have[r];
       pos[k] = held + ((int32_t)(row0 + i + k * kThreads) - cu[r]);
-      const int32_t pg = div_page(pos[k], pd), old = pages_of(held, pd);
+      const int32_t pg = fast_div(pos[k], pd), old = pages_of(held, pd);
       from[k] = pg >= old ? a.free_pages + (used + first[r] + pg - old) : a.block_table + ((int64_t)r * a.max_pages + pg);
       if (!live[k]) from[k] = a.pages_used;  // padding: any readable place
     }
@@ -148,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a,
     for (int k = 0; k < 4; ++k) {
       const int64_t row = row0 + i + k * kThreads;
       if (i + k * kThreads >= rows_per_block || row >= a.max_tokens) continue;
-      const int32_t pg = div_page(pos[k], pd), off = pos[k] - pg * a.page;
+      const int32_t pg = fast_div(pos[k], pd), off = pos[k] - pg * a.page;
       // the row that opens a page enters it into the table
       if (live[k] && off == 0 && pg >= pages_of(have[req[k]], pd))
         a.block_table[(int64_t)req[k] * a.max_pages + pg] = id[k];
@@ -166,11 +156,7 @@ hipError_t launch_step_tables(const StepTablesArgs &a, hipStream_t st) {
   rows = rows < 1024 ? 1024 : (rows + kThreads - 1) / kThreads * kThreads;
   int64_t grid = (a.max_tokens + rows - 1) / rows;
   if (grid < 1) grid = 1;
-  PageDiv pd;
-  int log = 0;
-  while (((int64_t)1 << log) < a.page) ++log;
-  pd.m = (uint32_t)((((uint64_t)1 << (31 + log)) / a.page) + 1);
-  pd.shift = 31 + log;
+  const FastDiv pd = make_fast_div(a.page);
   TimedLaunch tl(K_STEP_TABLES, st);
   step_tables_kernel<<<(int)grid, kThreads, (size_t)3 * (a.num_req > 0 ? a.num_req : 1) * sizeof(int32_t), st>>>(a, pd, (int)rows);
   return hipGetLastError();
