@@ -1,4 +1,5 @@
-"""torch.autograd wrapper of the dual-stream Gated DeltaNet layer.
+"""torch.autograd wrappers of the dual-stream Gated DeltaNet layer and of the
+norms and rotary positions around it.
 
 ``gdn_dual(varlen, q, k, v, alpha, beta, qn, kn, vn, alpha_n, beta_n,
 block_size, h0=None, scale=0.0, flags=0, ckpt_stride=1, window=0)`` returns
@@ -22,6 +23,7 @@ from __future__ import annotations
 import torch
 
 from . import Varlen, gdn_dual_bwd, gdn_dual_fwd, workspace_bytes, _io_of
+from . import layer as _layer
 
 _GRADS = ("dq", "dk", "dv", "dalpha", "dbeta", "dqn", "dkn", "dvn", "dalpha_n", "dbeta_n")
 
@@ -69,3 +71,91 @@ def gdn_dual(varlen: Varlen, q, k, v, alpha, beta, qn, kn, vn, alpha_n, beta_n, 
     of ckpt_stride)."""
     return GDNDualFunction.apply(varlen, int(block_size), float(scale), int(flags), int(ckpt_stride), int(window),
                                  q, k, v, alpha, beta, qn, kn, vn, alpha_n, beta_n, h0)
+
+
+# ---------------------------------------------------------------- around the GDN step
+# Differentiable forms of the norms and of rotary positions.  A tensor whose
+# token rows are not contiguous (a broadcast one, a transposed view) is copied
+# first; a gradient that reaches the reverse mode in such a form likewise.
+
+def _rows(t):
+    """t, or a packed copy where its tokens' rows are not contiguous."""
+    if t is None or t.is_contiguous():
+        return t
+    row = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != row:
+            return t.contiguous()
+        row *= size
+    return t if t.stride(0) >= row else t.contiguous()
+
+
+class GatedNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, gate, activation, eps):
+        x, gate, weight = _rows(x), _rows(gate), weight.contiguous()
+        y, rstd = _layer.gated_norm(x, weight, gate, activation=activation, eps=eps, want_rstd=True)
+        ctx.activation = activation
+        ctx.save_for_backward(x, weight, gate, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, gate, rstd = ctx.saved_tensors
+        dx, dgate, dweight = _layer.gated_norm_bwd(x, weight, gate, _rows(dy), rstd, activation=ctx.activation)
+        return dx, dweight, dgate, None, None
+
+
+def gated_norm(x, weight, gate=None, activation=_layer.SILU, eps=1e-6):
+    """Differentiable flare_gated_norm (layer.gated_norm): gradients flow to x,
+    weight and gate."""
+    return GatedNormFunction.apply(x, weight, gate, int(activation), float(eps))
+
+
+class ResidualNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, w_pre, w_post, gate, scale, activation, eps):
+        x, gate, residual = _rows(x), _rows(gate), residual.contiguous()
+        w_pre, w_post, scale = (None if w is None else w.contiguous() for w in (w_pre, w_post, scale))
+        h, y, rstd = _layer.residual_norm(x, residual, w_pre, w_post=w_post, gate=gate, scale=scale,
+                                          activation=activation, eps=eps, want_rstd=True)
+        ctx.activation = activation
+        ctx.save_for_backward(x, residual, w_pre, w_post, gate, scale, rstd)
+        return h, y
+
+    @staticmethod
+    def backward(ctx, dh, dy):
+        x, residual, w_pre, w_post, gate, scale, rstd = ctx.saved_tensors
+        g = _layer.residual_norm_bwd(x, residual, w_pre, dy.contiguous(), dh.contiguous(), rstd, w_post=w_post,
+                                     gate=gate, scale=scale, activation=ctx.activation)
+        return g["dx"], g["dresidual"], g["dw_pre"], g["dw_post"], g["dgate"], g["dscale"], None, None
+
+
+def residual_norm(x, residual, w_pre, w_post=None, gate=None, scale=None, activation=_layer.SIGMOID, eps=1e-6):
+    """Differentiable flare_residual_norm (layer.residual_norm): (h, y);
+    gradients flow to x, residual, gate, the weights and the scale."""
+    return ResidualNormFunction.apply(x, residual, w_pre, w_post, gate, scale, int(activation), float(eps))
+
+
+class RotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, positions, freqs, q, k, interleaved, mscale):
+        ctx.interleaved, ctx.mscale = interleaved, mscale
+        ctx.save_for_backward(positions, freqs)
+        q, k = _layer.rotary(positions, freqs, _rows(q), _rows(k), interleaved=interleaved, mscale=mscale)
+        return (q,) if k is None else (q, k)
+
+    @staticmethod
+    def backward(ctx, dq, dk=None):
+        positions, freqs = ctx.saved_tensors
+        # the channels that pass through are not scaled, and neither are their gradients
+        dq, dk = _layer.rotary(positions, freqs, _rows(dq), _rows(dk), interleaved=ctx.interleaved,
+                               mscale=ctx.mscale, inverse=True)
+        return None, None, dq, dk, None, None
+
+
+def rotary(positions, freqs, q, k=None, interleaved=False, mscale=1.0):
+    """Differentiable flare_rotary (layer.rotary): (q, k) turned (k None without
+    one); gradients flow to q and k."""
+    out = RotaryFunction.apply(positions, freqs, q, k, bool(interleaved), float(mscale))
+    return out if k is not None else (out[0], None)

@@ -22,6 +22,7 @@ flare_status flare_gated_norm(int64_t tokens, int32_t heads, int32_t dim, int32_
                               int32_t activation, float eps, void *y, float *rstd, void *stream) {
   clear_error();
   flare_status st = check_gated_norm(tokens, heads, dim, io_dtype, x, x_stride, gate, gate_stride, weight, activation);
+  if (st == FLARE_OK) st = check_eps(eps);
   if (st != FLARE_OK) return st;
   if (tokens == 0) return FLARE_OK;
   if (!y) return fail(FLARE_ERR_NULL, "gated_norm: y is NULL");
@@ -75,6 +76,7 @@ flare_status flare_residual_norm(int64_t tokens, int32_t dim, int32_t io_dtype, 
   clear_error();
   flare_status st = check_residual_norm(tokens, dim, io_dtype, res_dtype, x, x_stride, residual, gate, gate_stride,
                                         w_pre, activation);
+  if (st == FLARE_OK) st = check_eps(eps);
   if (st != FLARE_OK) return st;
   if (tokens == 0) return FLARE_OK;
   if (!h || !y) return fail(FLARE_ERR_NULL, "residual_norm: h or y is NULL");

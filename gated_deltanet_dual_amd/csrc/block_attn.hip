@@ -229,7 +229,9 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
     }
   }
   const float sc = a.scale * kLog2e;
-  const float room = 8.0f / sc;  // how far a score may pass the kept maximum: weights up to 2^8
+  // how far a score may pass the kept maximum: weights up to 2^8 (finite, so that
+  // the first score passes -inf + room)
+  const float room = fminf(8.0f / sc, 1e30f);
 
   floatx4 o[NQ][DT];
   float m[NQ], l[NQ];
@@ -250,13 +252,33 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
     const int r = 4 * grp + (col >> 2);
     va[d] = r * D + v_piece<D>(r, 2 * d + ((col & 3) >> 1)) * 8 + (col & 1) * 4;
   }
+  // V's operands of 32 keys
+  auto read_v = [&](u16 *vb, int h, bf16x8 (&vf)[DT]) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + 32 * h * D));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + (32 * h + 16) * D));
+      vf[d] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
   auto tile = [&](int t, const u16 *kb, u16 *vb, auto ragged) {
     const int kt = k0 + TK * t;
+    bool odd = false;
     if constexpr (ragged.value) {
-      // V rows behind the length hold anything: 0 * NaN must not reach O
-      for (int i = threadIdx.x; i < TK * PIECES; i += 256)
-        if (kt + i / PIECES >= k1) *reinterpret_cast<u32x4v *>(vb + 8 * i) = u32x4v{0, 0, 0, 0};
-      __syncthreads();
+      // V rows behind the length hold anything: 0 * NaN must not reach O.  Rows that
+      // only some of the block's queries see are looked through for infinities and NaN.
+      bool mine = false;
+      for (int i = threadIdx.x; i < TK * PIECES; i += 256) {
+        const int key = kt + i / PIECES;
+        if (key >= k1) {
+          *reinterpret_cast<u32x4v *>(vb + 8 * i) = u32x4v{0, 0, 0, 0};
+        } else if (key >= all) {
+          const u32x4v v = *reinterpret_cast<const u32x4v *>(vb + 8 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine |= (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+        }
+      }
+      odd = __syncthreads_or(mine);
     }
     if (!live) return;
 #pragma unroll
@@ -277,12 +299,7 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
         }
       // V's operands while the scores become weights
       bf16x8 vf[DT];
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + 32 * h * D));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + (32 * h + 16) * D));
-        vf[d] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      }
+      read_v(vb, h, vf);
       float top[NQ];
       bool over = false;
 #pragma unroll
@@ -322,6 +339,37 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
         for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
         pb[n] = __builtin_bit_cast(bf16x8, make_uint4(v[0], v[1], v[2], v[3]));
         l[n] += sum;
+      }
+      if constexpr (ragged.value) {
+        if (odd) {
+          // infinities and NaN out of the product, where the weight 0 of a query that
+          // does not see their key would spread them, and added to those that do
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            u32x4v v = __builtin_bit_cast(u32x4v, vf[d]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
+              if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
+            }
+            vf[d] = __builtin_bit_cast(bf16x8, v);
+          }
+#pragma unroll 1
+          for (int j = 0; j < 32; ++j) {
+            const int row = 32 * h + j;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(vb + row * D + v_piece<D>(row, 2 * d + (grp >> 1)) * 8 + (grp & 1) * 4);
+              const float f[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                                  __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                  o[n][d][r] += (__float_as_uint(f[r]) & 0x7f800000u) == 0x7f800000u && kt + row < lim[n] ? f[r] : 0.0f;
+            }
+          }
+        }
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d)

@@ -92,6 +92,11 @@ flare_status check_gate(const void *gate, int32_t activation, int64_t stride, in
   return FLARE_OK;
 }
 
+flare_status check_eps(float eps) {
+  if (!(eps >= 0.0f && eps < 1e30f)) return fail(FLARE_ERR_SHAPE, "eps must be a number of at least 0");
+  return FLARE_OK;
+}
+
 static flare_status check_norm_rows(int64_t rows, int32_t dim, int64_t x_stride, int64_t row) {
   if (dim < 1) return fail(FLARE_ERR_SHAPE, "dim must be positive");
   if (dim > 16384) return fail(FLARE_ERR_UNSUPPORTED, "dim %d, at most 16384", dim);
@@ -192,6 +197,8 @@ flare_status check_attention_shape(int32_t num_req, const flare_attention_shape 
   if (s->page < 16 || (s->page & (s->page - 1)) != 0)
     return fail(FLARE_ERR_UNSUPPORTED, "block_attention: page %d is no power of two of at least 16", s->page);
   if (s->io_dtype != FLARE_BF16) return fail(FLARE_ERR_UNSUPPORTED, "block_attention: bf16 only");
+  if (!(s->scale < 1e30f) || s->scale < -1e30f)
+    return fail(FLARE_ERR_SHAPE, "block_attention: scale must be a number below 1e30");
   if (s->causal != 0 && s->causal != 1) return fail(FLARE_ERR_UNSUPPORTED, "block_attention: causal %d unknown", s->causal);
   // keys are counted in 32 bits, with room for a tile past the end
   if (max_seq_len > INT32_MAX - 8192 || prefix_len > INT32_MAX - 8192)

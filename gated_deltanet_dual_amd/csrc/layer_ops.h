@@ -88,6 +88,7 @@ int norm_bwd_blocks(int64_t rows, int32_t dim);
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t dim, int weights);
 
 flare_status check_io(int32_t io_dtype);
+flare_status check_eps(float eps);
 flare_status check_gate(const void *gate, int32_t activation, int64_t stride, int64_t row);
 flare_status check_gated_norm(int64_t tokens, int32_t heads, int32_t dim, int32_t io_dtype, const void *x,
                               int64_t x_stride, const void *gate, int64_t gate_stride, const float *weight,

@@ -14,7 +14,7 @@ import math
 
 import numpy as np
 
-from . import BF16, F32, _check, _chk, _chk_buf, _fail, _gpu_device, _io_dtype_of, lib
+from . import BF16, F32, _check, _chk as _chk_slow, _chk_buf, _fail, _gpu_device, _io_dtype_of, lib
 
 _module = None
 
@@ -77,6 +77,13 @@ def _run(dev, fn, *args):
             status = fn(*args, C._cuda_getCurrentRawStream(index))
     if status:
         _check(status)
+
+
+def _chk(t, name, shape, dtype, dev, optional=False):
+    """The package's check, its message formed only where something is wrong: a
+    serving step's calls are as short as their checks."""
+    if t is None or t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _chk_slow(t, name, shape, dtype, dev, optional)
 
 
 def _ptr(t):

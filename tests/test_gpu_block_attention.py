@@ -133,3 +133,55 @@ def test_result_does_not_depend_on_the_batch(g):
         assert torch.allclose(one.float(), whole[r:r + 1].float(), rtol=2.0 ** -6, atol=2.0 ** -7)
     again = g.block_attention(q, kc, vc, bt, lens, prefix_table=pt, prefix_len=90)
     assert torch.equal(whole, again)
+
+
+def test_values_that_are_not_finite(g):
+    """Infinities and NaN in a value row reach exactly the queries that see its
+    key: a later token of the block does not reach the earlier ones."""
+    import torch
+    for d, B, G in [(64, 5, 2), (128, 5, 4), (128, 20, 8), (256, 4, 1)]:
+        args = make(7, 2, B, 1, G, d, 16, [40 + B, B], 70)
+        q, kc, vc, bt, lens, pt = args
+        clean = g.block_attention(q, kc, vc, bt, lens, prefix_table=pt, prefix_len=70, causal=True)
+        bad = vc.clone()
+        for r, n in enumerate([40 + B, B]):
+            for back, value in ((1, float("inf")), (2, float("nan")), (3, float("-inf"))):
+                j = n - back  # seen by the last `back` tokens of the block
+                bad[int(bt[r, j // 16]), 0, j % 16, back] = value
+        o = g.block_attention(q, kc, bad, bt, lens, prefix_table=pt, prefix_len=70, causal=True)
+        for b in range(B):
+            back = B - b  # this token sees keys up to n - back + 1
+            for ch, value in ((1, math.inf), (2, None), (3, -math.inf)):
+                got = o[:, b, :, ch]
+                if ch < back:  # key n - ch lies behind this token's view
+                    assert torch.equal(got, clean[:, b, :, ch]), (d, b, ch)
+                elif value is None:
+                    assert torch.isnan(got).all(), (d, b, ch)
+                else:
+                    assert (got == value).all(), (d, b, ch)
+        assert torch.equal(o[..., 4:], clean[..., 4:]) and torch.equal(o[..., 0], clean[..., 0])
+
+
+def test_extreme_scales(g):
+    """A scale so small that all weights are equal, and one so large that the
+    largest score takes all."""
+    import torch
+    q, kc, vc, bt, lens, pt = args = make(8, 2, 2, 1, 2, 64, 16, [50, 33], 20)
+    o = g.block_attention(q, kc, vc, bt, lens, prefix_table=pt, prefix_len=20, scale=1e-36)
+    ro, _, size = attention64(*args, 20, False, 1e-36)
+    close(o, ro, torch.bfloat16, (2.0 ** -8 + 4e-4) * size, "o")
+    o = g.block_attention(q, kc, vc, bt, lens, prefix_table=pt, prefix_len=20, scale=1e4)
+    ro, _, size = attention64(*args, 20, False, 1e4)
+    close(o, ro, torch.bfloat16, (2.0 ** -8 + 4e-4) * size, "o")
+
+
+def test_table_entries_that_name_no_page_stay_inside(g):
+    """Ids outside the cache read some page of it: finite numbers, no fault, and
+    the other requests' results are untouched."""
+    import torch
+    q, kc, vc, bt, lens, pt = make(9, 3, 1, 2, 2, 128, 16, [40, 40, 40], 0, fill=0.0)
+    want = g.block_attention(q, kc, vc, bt, lens)
+    bt[1, 1] = -5
+    bt[1, 2] = 2 ** 31 - 1
+    o = g.block_attention(q, kc, vc, bt, lens)
+    assert torch.isfinite(o.float()).all() and torch.equal(o[0], want[0]) and torch.equal(o[2], want[2])
