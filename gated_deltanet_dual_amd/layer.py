@@ -66,14 +66,23 @@ def declare(L):
         getattr(L, name).restype = ctypes.c_int
 
 
+def _lead(t, name):
+    """(device, io dtype) of the tensor that sets them for a call."""
+    if t is not None and t.is_cuda:
+        dtype = t.dtype
+        if dtype == _torch().bfloat16 or dtype == _module.float32:
+            return t.device, dtype
+    return _gpu_device(t, name), _io_dtype_of(t, name)
+
+
 def _run(dev, fn, *args):
     """fn(*args, stream) with the tensors' device current, on its current stream."""
-    C = _torch()._C
+    C = _module._C
     index = dev.index
     if C._cuda_getDevice() == index:
         status = fn(*args, C._cuda_getCurrentRawStream(index))
     else:
-        with _torch().cuda.device(dev):
+        with _module.cuda.device(dev):
             status = fn(*args, C._cuda_getCurrentRawStream(index))
     if status:
         _check(status)
@@ -101,9 +110,10 @@ def _token_rows(t, name, shape, dtype, dev):
         _fail("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.device != dev:
         _fail("%s is on %s, expected %s" % (name, t.device, dev))
+    strides = t.stride()
     if shape[0] > 1 and t.is_contiguous():
-        return t.numel() // shape[0]
-    row, strides = 1, t.stride()
+        return strides[0]
+    row = 1
     for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
         if size != 1 and stride != row:
             _fail("%s: a token's row must be contiguous" % name, 3)
@@ -118,13 +128,21 @@ def _token_rows(t, name, shape, dtype, dev):
 def _out(t, name, shape, dtype, dev):
     """An output buffer the caller gave, or a new one."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=dev)
+        return _module.empty(shape, dtype=dtype, device=dev)
     _chk(t, name, shape, dtype, dev)
     return t
 
 
+def _out_like(t, name, x):
+    """The same, packed and like x."""
+    if t is None:
+        return _module.empty_like(x, memory_format=_module.contiguous_format)
+    _chk(t, name, x.shape, x.dtype, x.device)
+    return t
+
+
 def _io(dtype):
-    return BF16 if dtype == _torch().bfloat16 else F32
+    return BF16 if dtype == _module.bfloat16 else F32
 
 
 def _workspace(t, need, dev):
@@ -140,15 +158,17 @@ def _workspace(t, need, dev):
 def _norm_inputs(x, weight, gate):
     """x [T, d] or [T, H, d] io, weight [d] fp32, gate like x or None; returns
     (T, H, d, io dtype, device, x stride, gate stride)."""
-    torch = _torch()
-    dev = _gpu_device(x, "x")
-    io = _io_dtype_of(x, "x")
-    if x.dim() not in (2, 3):
-        _fail("x must be [T, d] or [T, H, d], got shape %s" % (tuple(x.shape),))
-    T, H, d = (x.shape[0], 1, x.shape[1]) if x.dim() == 2 else x.shape
-    xs = _token_rows(x, "x", x.shape, io, dev)
-    _chk(weight, "weight", (d,), torch.float32, dev)
-    gs = _token_rows(gate, "gate", x.shape, io, dev) if gate is not None else 0
+    dev, io = _lead(x, "x")
+    shape = x.shape
+    if len(shape) == 3:
+        T, H, d = shape
+    elif len(shape) == 2:
+        (T, d), H = shape, 1
+    else:
+        _fail("x must be [T, d] or [T, H, d], got shape %s" % (tuple(shape),))
+    xs = _token_rows(x, "x", shape, io, dev)
+    _chk(weight, "weight", (d,), _module.float32, dev)
+    gs = _token_rows(gate, "gate", shape, io, dev) if gate is not None else 0
     return T, H, d, io, dev, xs, gs
 
 
@@ -158,13 +178,12 @@ def gated_norm(x, weight, gate=None, activation=SILU, eps=1e-6, out=None, want_r
     [T, d] io; gate like x or None; both may be slices of wider token rows;
     weight [d] fp32.  Returns y, or (y, rstd) with want_rstd or `rstd` (fp32
     [T, H] or [T], what gated_norm_bwd reads)."""
-    torch = _torch()
     T, H, d, io, dev, xs, gs = _norm_inputs(x, weight, gate)
-    y = _out(out, "out", x.shape, io, dev)
+    y = _out_like(out, "out", x)
     if rstd is not None or want_rstd:
-        rstd = _out(rstd, "rstd", x.shape[:-1], torch.float32, dev)
-    _run(dev, lib().flare_gated_norm, T, H, d, _io(io), _ptr(x), xs, _ptr(gate), gs, _ptr(weight), int(activation),
-         float(eps), _ptr(y), _ptr(rstd))
+        rstd = _out(rstd, "rstd", x.shape[:-1], _module.float32, dev)
+    _run(dev, lib().flare_gated_norm, T, H, d, _io(io), x.data_ptr(), xs, _ptr(gate), gs, weight.data_ptr(), activation,
+         eps, y.data_ptr(), _ptr(rstd))
     return y if rstd is None else (y, rstd)
 
 
@@ -181,8 +200,8 @@ def gated_norm_bwd(x, weight, gate, dy, rstd, activation=SILU, workspace=None, o
     ds = _token_rows(dy, "dy", x.shape, io, dev)
     _chk(rstd, "rstd", x.shape[:-1], torch.float32, dev)
     dx, dgate, dweight = out if out is not None else (None, None, None)
-    dx = _out(dx, "dx", x.shape, io, dev)
-    dgate = _out(dgate, "dgate", x.shape, io, dev) if gate is not None else None
+    dx = _out_like(dx, "dx", x)
+    dgate = _out_like(dgate, "dgate", gate) if gate is not None else None
     dweight = _out(dweight, "dweight", (d,), torch.float32, dev)
     need = gated_norm_bwd_workspace_bytes(T, H, d)
     workspace = _workspace(workspace, need, dev)
@@ -193,14 +212,13 @@ def gated_norm_bwd(x, weight, gate, dy, rstd, activation=SILU, workspace=None, o
 
 
 def _residual_inputs(x, residual, w_pre, w_post, gate, scale):
-    torch = _torch()
-    dev = _gpu_device(x, "x")
-    io = _io_dtype_of(x, "x")
+    dev, io = _lead(x, "x")
+    torch = _module
     if x.dim() != 2:
         _fail("x must be [T, C], got shape %s" % (tuple(x.shape),))
     T, C = x.shape
     xs = _token_rows(x, "x", (T, C), io, dev)
-    res = _io_dtype_of(residual, "residual")
+    res = io if residual is not None and residual.dtype == io else _io_dtype_of(residual, "residual")
     _chk(residual, "residual", (T, C), res, dev)
     _chk(w_pre, "w_pre", (C,), torch.float32, dev)
     _chk(w_post, "w_post", (C,), torch.float32, dev, optional=True)
@@ -219,12 +237,11 @@ def residual_norm(x, residual, w_pre, w_post=None, gate=None, scale=None, activa
     bf16 with bf16 io; weights and scale [C] fp32.  Returns (h, y), or
     (h, y, rstd) with want_rstd or `rstd` (fp32 [T, 2], what
     residual_norm_bwd reads); `out` = (h, y) reuses buffers."""
-    torch = _torch()
     T, C, io, res, dev, xs, gs = _residual_inputs(x, residual, w_pre, w_post, gate, scale)
     h, y = out if out is not None else (None, None)
-    h, y = _out(h, "h", (T, C), res, dev), _out(y, "y", (T, C), io, dev)
+    h, y = _out_like(h, "h", residual), _out_like(y, "y", x)
     if rstd is not None or want_rstd:
-        rstd = _out(rstd, "rstd", (T, 2), torch.float32, dev)
+        rstd = _out(rstd, "rstd", (T, 2), _module.float32, dev)
     _run(dev, lib().flare_residual_norm, T, C, _io(io), _io(res), _ptr(x), xs, _ptr(residual), _ptr(gate), gs,
          _ptr(w_pre), _ptr(w_post), _ptr(scale), int(activation), float(eps), _ptr(h), _ptr(y), _ptr(rstd))
     return (h, y) if rstd is None else (h, y, rstd)
@@ -304,9 +321,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, ori
 
 
 def _rotary_inputs(positions, freqs, q, k, interleaved, mscale):
-    torch = _torch()
-    dev = _gpu_device(q, "q")
-    io = _io_dtype_of(q)
+    dev, io = _lead(q, "q")
+    torch = _module
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         _fail("q and k must be [T, H, d]")
     T, Hq, d = q.shape
@@ -329,8 +345,8 @@ def rotary(positions, freqs, q, k=None, interleaved=False, mscale=1.0, inverse=F
     (q, k) turned, packed; `out` = (q, k) reuses buffers."""
     T, shp, io, dev, qs, ks = _rotary_inputs(positions, freqs, q, k, interleaved, mscale)
     qo, ko = out if out is not None else (None, None)
-    qo = _out(qo, "q out", q.shape, io, dev)
-    ko = _out(ko, "k out", k.shape, io, dev) if k is not None else None
+    qo = _out_like(qo, "q out", q)
+    ko = _out_like(ko, "k out", k) if k is not None else None
     _run(dev, lib().flare_rotary, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs, _ptr(k), ks,
          1 if inverse else 0, _ptr(qo), _ptr(ko))
     return qo, ko
@@ -340,14 +356,13 @@ def rotary_cache(positions, freqs, q, k, v, slots, k_cache, v_cache, interleaved
     """The serving form (flare_rotary_cache): returns q turned; k turned and v
     are written to the cache's pages [num_pages, Hk, page, d], row t at slot
     slots[t] (int64, page id * page + offset; -1 writes nothing)."""
-    torch = _torch()
     if k is None or v is None:
         _fail("k and v are required", 1)
     T, shp, io, dev, qs, ks = _rotary_inputs(positions, freqs, q, k, interleaved, mscale)
     vs = _token_rows(v, "v", k.shape, io, dev)
-    _chk(slots, "slots", (T,), torch.int64, dev)
+    _chk(slots, "slots", (T,), _module.int64, dev)
     pages, page = _chk_cache(k_cache, v_cache, k.shape[1], k.shape[2], io, dev)
-    qo = _out(out, "out", q.shape, io, dev)
+    qo = _out_like(out, "out", q)
     _run(dev, lib().flare_rotary_cache, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs, _ptr(k), ks,
          _ptr(v), vs, _ptr(slots), _ptr(qo), _ptr(k_cache), _ptr(v_cache), pages, page)
     return qo
@@ -391,13 +406,18 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
     M = int(max_tokens)
     if M < 0:
         _fail("max_tokens must not be negative")
-    out = out or {}
-    t = {"cu_new": _out(out.get("cu_new"), "cu_new", (R + 1,), i32, dev),
-         "positions": _out(out.get("positions"), "positions", (M,), i32, dev),
-         "slots": _out(out.get("slots"), "slots", (M,), torch.int64, dev),
-         "seq_lens": _out(out.get("seq_lens"), "seq_lens out", (R,), i32, dev),
-         "pages_used": _out(out.get("pages_used"), "pages_used out", (1,), i32, dev),
-         "status": _out(out.get("status"), "status", (1,), i32, dev)}
+    if out is None:  # the small ones share a buffer
+        cu, lens, used, status = torch.empty((2 * R + 3,), dtype=i32, device=dev).split((R + 1, R, 1, 1))
+        t = {"cu_new": cu, "positions": torch.empty((M,), dtype=i32, device=dev),
+             "slots": torch.empty((M,), dtype=torch.int64, device=dev), "seq_lens": lens, "pages_used": used,
+             "status": status}
+    else:
+        t = {"cu_new": _out(out.get("cu_new"), "cu_new", (R + 1,), i32, dev),
+             "positions": _out(out.get("positions"), "positions", (M,), i32, dev),
+             "slots": _out(out.get("slots"), "slots", (M,), torch.int64, dev),
+             "seq_lens": _out(out.get("seq_lens"), "seq_lens out", (R,), i32, dev),
+             "pages_used": _out(out.get("pages_used"), "pages_used out", (1,), i32, dev),
+             "status": _out(out.get("status"), "status", (1,), i32, dev)}
     _run(dev, lib().flare_step_tables, R, _ptr(seq_lens), _ptr(new_lens), _ptr(block_table), block_table.shape[1],
          _ptr(free_pages), free_pages.shape[0], _ptr(pages_used), int(page), int(position_offset), M,
          _ptr(t["cu_new"]), _ptr(t["positions"]), _ptr(t["slots"]), _ptr(t["seq_lens"]), _ptr(t["pages_used"]),
@@ -450,7 +470,7 @@ def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=Non
         _chk(prefix_table, "prefix_table", prefix_table.shape, torch.int32, dev)
     most = wide * page if max_seq_len is None else int(max_seq_len)
     shp = AttentionShape(B, Hq, Hk, d, page, BF16, 1 if causal else 0, scale)
-    o = _out(out, "out", (R, B, Hq, d), torch.bfloat16, dev)
+    o = _out_like(out, "out", q)
     if lse is not None or want_lse:
         lse = _out(lse, "lse", (R, B, Hq), torch.float32, dev)
     need = int(lib().flare_block_attention_workspace_size(R, ctypes.byref(shp), most, n))
