@@ -333,8 +333,9 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
   const int per = BLOCK ? 1 : blockDim.x / team;
   const int nv = a.dim / VEC;
   float dw2[NV][VEC] = {}, dw1[NV][VEC] = {}, ds[NV][VEC] = {};
-  // the weights of a thread's one vector stay in registers over its rows
-  constexpr bool KEEP = NV == 1;
+  // the weights of a thread's one vector stay in registers over its rows (of 128
+  // registers that larger workgroups leave, they would be 3 VEC too many)
+  constexpr bool KEEP = NV == 1 && THREADS <= 256;
   float w2[VEC] = {}, w1[VEC] = {}, sc[VEC] = {};
   if (KEEP && tm.lane < nv) {
     Vec<float, VEC>::load(a.w_pre + tm.lane * VEC, w2);
@@ -495,25 +496,30 @@ TeamPlan plan_reverse(int nv) {
   KERNEL<__VA_ARGS__, NV, BLK, THREADS><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
 // The last type argument is the vector's width: rows of more than 4 vectors a
 // thread are those of single elements.
-#define NORM_PICK_BLOCK(KERNEL, VEC, ...)                                                          \
-  do {                                                                                             \
-    if (p.nv <= 4) NORM_LAUNCH(4, true, 1024, KERNEL, __VA_ARGS__, VEC);                           \
-    else if constexpr (VEC == 1) NORM_LAUNCH(16, true, 1024, KERNEL, __VA_ARGS__, VEC);            \
-  } while (0)
 #define NORM_PICK_FORWARD(KERNEL, VEC, ...)                                                        \
   do {                                                                                             \
-    if (p.block) NORM_PICK_BLOCK(KERNEL, VEC, __VA_ARGS__);                                        \
-    else if (p.nv == 1) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);                      \
-    else if (p.nv == 2) NORM_LAUNCH(2, false, 256, KERNEL, __VA_ARGS__, VEC);                      \
-    else NORM_LAUNCH(4, false, 256, KERNEL, __VA_ARGS__, VEC);                                     \
+    if (!p.block && p.nv == 1) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);               \
+    else if (!p.block && p.nv == 2) NORM_LAUNCH(2, false, 256, KERNEL, __VA_ARGS__, VEC);          \
+    else if (!p.block) NORM_LAUNCH(4, false, 256, KERNEL, __VA_ARGS__, VEC);                       \
+    else if (p.nv <= 4) NORM_LAUNCH(4, true, 1024, KERNEL, __VA_ARGS__, VEC);                      \
+    else if constexpr (VEC == 1) NORM_LAUNCH(16, true, 1024, KERNEL, __VA_ARGS__, VEC);            \
   } while (0)
+// A thread of the reverse modes holds 8 elements of a row without spilling; 16 (rows
+// of more than 8192) spill.
 #define NORM_PICK_REVERSE(KERNEL, VEC, ...)                                                        \
   do {                                                                                             \
     if (grid == 0) break; /* no rows: the weights' sums are still written */                       \
     if (!p.block) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);                            \
-    else if (p.nv > 1) NORM_PICK_BLOCK(KERNEL, VEC, __VA_ARGS__);                                  \
     else if (p.team <= 256) NORM_LAUNCH(1, true, 256, KERNEL, __VA_ARGS__, VEC);                   \
-    else NORM_LAUNCH(1, true, 1024, KERNEL, __VA_ARGS__, VEC);                                     \
+    else if (p.nv == 1) NORM_LAUNCH(1, true, 1024, KERNEL, __VA_ARGS__, VEC);                      \
+    else if (p.nv == 2) NORM_LAUNCH(2, true, 1024, KERNEL, __VA_ARGS__, VEC);                      \
+    else if constexpr (VEC < 8) {                                                                  \
+      if (p.nv <= 4) NORM_LAUNCH(4, true, 1024, KERNEL, __VA_ARGS__, VEC);                         \
+      else if constexpr (VEC == 1) {                                                               \
+        if (p.nv <= 8) NORM_LAUNCH(8, true, 1024, KERNEL, __VA_ARGS__, VEC);                       \
+        else NORM_LAUNCH(16, true, 1024, KERNEL, __VA_ARGS__, VEC);                                \
+      }                                                                                            \
+    }                                                                                              \
   } while (0)
 
 static int row_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
