@@ -68,9 +68,9 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
 
 
 int norm_bwd_blocks(int64_t rows, int32_t dim) {
-  // what the chip holds at a time: six workgroups of 256 threads a CU where a wave
-  // holds rows, three where the row is a workgroup's
-  const int64_t most = dim <= 512 ? 1536 : 768;
+  // what the chip holds at a time: six workgroups of 256 threads a CU where a wave or
+  // two hold a row, three where a row is the workgroup's
+  const int64_t most = dim <= 1024 ? 1536 : 768;
   return (int)(rows < most ? rows : most);
 }
 

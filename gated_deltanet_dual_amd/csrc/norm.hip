@@ -8,52 +8,11 @@
 //   dx = r (du - u mean(du u)).
 #include <hip/hip_runtime.h>
 
-#include "device_common.h"
 #include "layer_launch.h"
+#include "vec_io.h"
 
 namespace flare {
 namespace {
-
-// VEC consecutive elements of a row, as fp32.
-template <typename IO, int VEC> struct Vec;
-template <> struct Vec<u16, 8> {
-  static __device__ __forceinline__ void load(const u16 *p, float *f) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(w[e] << 16);
-      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ void store(u16 *p, const float *f) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-  }
-};
-template <> struct Vec<float, 4> {
-  static __device__ __forceinline__ void load(const float *p, float *f) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  }
-  static __device__ __forceinline__ void store(float *p, const float *f) {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <> struct Vec<float, 8> {
-  static __device__ __forceinline__ void load(const float *p, float *f) {
-    Vec<float, 4>::load(p, f);
-    Vec<float, 4>::load(p + 4, f + 4);
-  }
-  static __device__ __forceinline__ void store(float *p, const float *f) {
-    Vec<float, 4>::store(p, f);
-    Vec<float, 4>::store(p + 4, f + 4);
-  }
-};
-template <typename IO> struct Vec<IO, 1> {
-  static __device__ __forceinline__ void load(const IO *p, float *f) { f[0] = io_traits<IO>::to_f(*p); }
-  static __device__ __forceinline__ void store(IO *p, const float *f) { *p = io_traits<IO>::from_f(f[0]); }
-};
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
@@ -95,10 +54,10 @@ template <int VEC> __device__ __forceinline__ void gate_values_d(const float *g,
     }
   }
 }
-// The vector c of an fp32 weight, or ones where it is absent.
-template <int VEC> __device__ __forceinline__ void load_or_one(const float *w, int c, float *f) {
+// The vector c of an fp32 weight, n of it, or ones where it is absent.
+template <int VEC, bool TAIL> __device__ __forceinline__ void load_or_one(const float *w, int c, int n, float *f) {
   if (w) {
-    Vec<float, VEC>::load(w + c * VEC, f);
+    load_vec<float, VEC, TAIL>(w + c * VEC, n, f);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) f[e] = 1.0f;
@@ -130,13 +89,13 @@ template <bool BLOCK> struct Team {
 };
 
 // ---------------------------------------------------------------- gated norm
-template <typename IO, int VEC, int NV, bool BLOCK, int THREADS>
+template <typename IO, int VEC, bool TAIL, int NV, bool BLOCK, int THREADS>
 __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a, int team) {
   __shared__ float red[16];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
   const uint32_t rows = (uint32_t)(a.tokens * a.heads);
-  const int nv = a.dim / VEC;
+  const int nv = (a.dim + VEC - 1) / VEC;
   for (uint32_t row = blockIdx.x * per + (BLOCK ? 0 : threadIdx.x / team); row < rows; row += gridDim.x * per) {
     const uint32_t t = row / (uint32_t)a.heads, h = row - t * (uint32_t)a.heads;
     const IO *x = (const IO *)a.x + (int64_t)t * a.x_stride + (int64_t)h * a.dim;
@@ -146,8 +105,8 @@ __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a, in
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        Vec<IO, VEC>::load(x + c * VEC, xv[i]);
-        if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, gv[i]);
+        load_vec<IO, VEC, TAIL>(x + c * VEC, a.dim - c * VEC, xv[i]);
+        if (a.act >= 0) load_vec<IO, VEC, TAIL>(g + c * VEC, a.dim - c * VEC, gv[i]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss += xv[i][e] * xv[i][e];
       }
@@ -161,11 +120,11 @@ __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a, in
       const int c = tm.lane + i * team;
       if (c < nv) {
         float w[VEC], o[VEC];
-        Vec<float, VEC>::load(a.weight + c * VEC, w);
+        load_vec<float, VEC, TAIL>(a.weight + c * VEC, a.dim - c * VEC, w);
         gate_values<VEC>(gv[i], a.act, o);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] *= xv[i][e] * r * w[e];
-        Vec<IO, VEC>::store(y + c * VEC, o);
+        store_vec<IO, VEC, TAIL>(y + c * VEC, a.dim - c * VEC, o);
       }
     }
   }
@@ -173,16 +132,16 @@ __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a, in
 
 // Adds the threads' column sums of a workgroup: `acc` of every team for the
 // vectors it holds, into part[blockIdx.x][dim].
-template <int VEC, int NV, bool BLOCK>
+template <int VEC, bool TAIL, int NV, bool BLOCK>
 __device__ __forceinline__ void write_partial(const float (&acc)[NV][VEC], const Team<BLOCK> &tm, int dim, float *part,
                                               float *lds) {
-  const int nv = dim / VEC;
+  const int nv = (dim + VEC - 1) / VEC;
   float *out = part + (int64_t)blockIdx.x * dim;
   if constexpr (BLOCK) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * tm.size;
-      if (c < nv) Vec<float, VEC>::store(out + c * VEC, acc[i]);
+      if (c < nv) store_vec<float, VEC, TAIL>(out + c * VEC, dim - c * VEC, acc[i]);
     }
   } else {
     // lds [blockDim.x][VEC]: one vector of every thread at a time
@@ -195,7 +154,7 @@ __device__ __forceinline__ void write_partial(const float (&acc)[NV][VEC], const
       __syncthreads();
       for (int j = threadIdx.x; j < tm.size * VEC; j += blockDim.x) {
         const int c = i * tm.size * VEC + j;
-        if (c < nv * VEC) {
+        if (c < dim) {
           float s = 0.0f;
           for (int k = 0; k < teams; ++k) s += lds[k * tm.size * VEC + j];
           out[c] = s;
@@ -205,19 +164,19 @@ __device__ __forceinline__ void write_partial(const float (&acc)[NV][VEC], const
   }
 }
 
-template <typename IO, int VEC, int NV, bool BLOCK, int THREADS>
+template <typename IO, int VEC, bool TAIL, int NV, bool BLOCK, int THREADS>
 __global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a, int team) {
   __shared__ float red[16];
   __shared__ float cols[BLOCK ? 1 : 256 * VEC];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
   const uint32_t rows = (uint32_t)(a.tokens * a.heads);
-  const int nv = a.dim / VEC;
+  const int nv = (a.dim + VEC - 1) / VEC;
   float dw[NV][VEC] = {};
   float w[NV][VEC] = {};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (tm.lane + i * team < nv) Vec<float, VEC>::load(a.weight + (tm.lane + i * team) * VEC, w[i]);
+    if (const int c = tm.lane + i * team; c < nv) load_vec<float, VEC, TAIL>(a.weight + c * VEC, a.dim - c * VEC, w[i]);
   for (uint32_t row = blockIdx.x * per + (BLOCK ? 0 : threadIdx.x / team); row < rows; row += gridDim.x * per) {
     const uint32_t t = row / (uint32_t)a.heads, h = row - t * (uint32_t)a.heads;
     const int64_t hd = (int64_t)h * a.dim;
@@ -230,9 +189,9 @@ __global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        Vec<IO, VEC>::load(x + c * VEC, u[i]);
-        Vec<IO, VEC>::load(dy + c * VEC, du[i]);
-        if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, gv[i]);
+        load_vec<IO, VEC, TAIL>(x + c * VEC, a.dim - c * VEC, u[i]);
+        load_vec<IO, VEC, TAIL>(dy + c * VEC, a.dim - c * VEC, du[i]);
+        if (a.act >= 0) load_vec<IO, VEC, TAIL>(g + c * VEC, a.dim - c * VEC, gv[i]);
         float f[VEC], d[VEC];
         gate_values_d<VEC>(gv[i], a.act, f, d);
 #pragma unroll
@@ -254,21 +213,21 @@ __global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a
         float o[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = r * (du[i][e] - u[i][e] * dot);
-        Vec<IO, VEC>::store((IO *)a.dx + (int64_t)row * a.dim + c * VEC, o);
-        if (a.act >= 0) Vec<IO, VEC>::store((IO *)a.dgate + (int64_t)row * a.dim + c * VEC, gv[i]);
+        store_vec<IO, VEC, TAIL>((IO *)a.dx + (int64_t)row * a.dim + c * VEC, a.dim - c * VEC, o);
+        if (a.act >= 0) store_vec<IO, VEC, TAIL>((IO *)a.dgate + (int64_t)row * a.dim + c * VEC, a.dim - c * VEC, gv[i]);
       }
     }
   }
-  write_partial<VEC, NV, BLOCK>(dw, tm, a.dim, a.part, cols);
+  write_partial<VEC, TAIL, NV, BLOCK>(dw, tm, a.dim, a.part, cols);
 }
 
 // ---------------------------------------------------------------- residual norm
-template <typename IO, typename RES, int VEC, int NV, bool BLOCK, int THREADS>
+template <typename IO, typename RES, int VEC, bool TAIL, int NV, bool BLOCK, int THREADS>
 __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs a, int team) {
   __shared__ float red[16];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
-  const int nv = a.dim / VEC;
+  const int nv = (a.dim + VEC - 1) / VEC;
   for (int64_t row = (int64_t)blockIdx.x * per + (BLOCK ? 0 : threadIdx.x / team); row < a.tokens;
        row += (int64_t)gridDim.x * per) {
     const IO *x = (const IO *)a.x + row * a.x_stride;
@@ -279,9 +238,9 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        Vec<IO, VEC>::load(x + c * VEC, xv[i]);
-        Vec<RES, VEC>::load(res + c * VEC, hv[i]);
-        if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, gv[i]);
+        load_vec<IO, VEC, TAIL>(x + c * VEC, a.dim - c * VEC, xv[i]);
+        load_vec<RES, VEC, TAIL>(res + c * VEC, a.dim - c * VEC, hv[i]);
+        if (a.act >= 0) load_vec<IO, VEC, TAIL>(g + c * VEC, a.dim - c * VEC, gv[i]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss += xv[i][e] * xv[i][e];
       }
@@ -294,15 +253,15 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
       const int c = tm.lane + i * team;
       if (c < nv) {
         float w1[VEC], sc[VEC], f[VEC];
-        load_or_one<VEC>(a.w_post, c, w1);
-        load_or_one<VEC>(a.scale, c, sc);
+        load_or_one<VEC, TAIL>(a.w_post, c, a.dim - c * VEC, w1);
+        load_or_one<VEC, TAIL>(a.scale, c, a.dim - c * VEC, sc);
         gate_values<VEC>(gv[i], a.act, f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           hv[i][e] += xv[i][e] * r1 * w1[e] * f[e] * sc[e];
           ss += hv[i][e] * hv[i][e];
         }
-        Vec<RES, VEC>::store((RES *)a.h + row * a.dim + c * VEC, hv[i]);
+        store_vec<RES, VEC, TAIL>((RES *)a.h + row * a.dim + c * VEC, a.dim - c * VEC, hv[i]);
       }
     }
     // the second norm is of h before h's own rounding
@@ -316,31 +275,32 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
       const int c = tm.lane + i * team;
       if (c < nv) {
         float w2[VEC], o[VEC];
-        Vec<float, VEC>::load(a.w_pre + c * VEC, w2);
+        load_vec<float, VEC, TAIL>(a.w_pre + c * VEC, a.dim - c * VEC, w2);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = hv[i][e] * r2 * w2[e];
-        Vec<IO, VEC>::store((IO *)a.y + row * a.dim + c * VEC, o);
+        store_vec<IO, VEC, TAIL>((IO *)a.y + row * a.dim + c * VEC, a.dim - c * VEC, o);
       }
     }
   }
 }
 
-template <typename IO, typename RES, int VEC, int NV, bool BLOCK, int THREADS>
+template <typename IO, typename RES, int VEC, bool TAIL, int NV, bool BLOCK, int THREADS>
 __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNormArgs a, int team) {
   __shared__ float red[16];
   __shared__ float cols[BLOCK ? 1 : 256 * VEC];
   const Team<BLOCK> tm{team, BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (team - 1))};
   const int per = BLOCK ? 1 : blockDim.x / team;
-  const int nv = a.dim / VEC;
+  const int nv = (a.dim + VEC - 1) / VEC;
   float dw2[NV][VEC] = {}, dw1[NV][VEC] = {}, ds[NV][VEC] = {};
   // the weights of a thread's one vector stay in registers over its rows (of 128
   // registers that larger workgroups leave, they would be 3 VEC too many)
   constexpr bool KEEP = NV == 1 && THREADS <= 256;
   float w2[VEC] = {}, w1[VEC] = {}, sc[VEC] = {};
   if (KEEP && tm.lane < nv) {
-    Vec<float, VEC>::load(a.w_pre + tm.lane * VEC, w2);
-    load_or_one<VEC>(a.w_post, tm.lane, w1);
-    load_or_one<VEC>(a.scale, tm.lane, sc);
+    const int c = tm.lane;
+    load_vec<float, VEC, TAIL>(a.w_pre + c * VEC, a.dim - c * VEC, w2);
+    load_or_one<VEC, TAIL>(a.w_post, c, a.dim - c * VEC, w1);
+    load_or_one<VEC, TAIL>(a.scale, c, a.dim - c * VEC, sc);
   }
   for (int64_t row = (int64_t)blockIdx.x * per + (BLOCK ? 0 : threadIdx.x / team); row < a.tokens;
        row += (int64_t)gridDim.x * per) {
@@ -354,12 +314,12 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
     for (int i = 0; i < NV; ++i) {
       const int c = tm.lane + i * team;
       if (c < nv) {
-        Vec<IO, VEC>::load(x + c * VEC, n[i]);
-        Vec<RES, VEC>::load(res + c * VEC, u[i]);
-        Vec<IO, VEC>::load((const IO *)a.dy + row * a.dim + c * VEC, dy[i]);
-        if (a.act >= 0) Vec<IO, VEC>::load(g + c * VEC, f[i]);
+        load_vec<IO, VEC, TAIL>(x + c * VEC, a.dim - c * VEC, n[i]);
+        load_vec<RES, VEC, TAIL>(res + c * VEC, a.dim - c * VEC, u[i]);
+        load_vec<IO, VEC, TAIL>((const IO *)a.dy + row * a.dim + c * VEC, a.dim - c * VEC, dy[i]);
+        if (a.act >= 0) load_vec<IO, VEC, TAIL>(g + c * VEC, a.dim - c * VEC, f[i]);
         if (a.dh) {
-          Vec<RES, VEC>::load((const RES *)a.dh + row * a.dim + c * VEC, dh[i]);
+          load_vec<RES, VEC, TAIL>((const RES *)a.dh + row * a.dim + c * VEC, a.dim - c * VEC, dh[i]);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) dh[i][e] = 0.0f;
@@ -371,9 +331,9 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
       const int c = tm.lane + i * team;
       if (c < nv) {
         if constexpr (!KEEP) {
-          Vec<float, VEC>::load(a.w_pre + c * VEC, w2);
-          load_or_one<VEC>(a.w_post, c, w1);
-          load_or_one<VEC>(a.scale, c, sc);
+          load_vec<float, VEC, TAIL>(a.w_pre + c * VEC, a.dim - c * VEC, w2);
+          load_or_one<VEC, TAIL>(a.w_post, c, a.dim - c * VEC, w1);
+          load_or_one<VEC, TAIL>(a.scale, c, a.dim - c * VEC, sc);
         }
         gate_values_d<VEC>(f[i], a.act, f[i], df[i]);
 #pragma unroll
@@ -393,8 +353,8 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
       const int c = tm.lane + i * team;
       if (c < nv) {
         if constexpr (!KEEP) {
-          load_or_one<VEC>(a.w_post, c, w1);
-          load_or_one<VEC>(a.scale, c, sc);
+          load_or_one<VEC, TAIL>(a.w_post, c, a.dim - c * VEC, w1);
+          load_or_one<VEC, TAIL>(a.scale, c, a.dim - c * VEC, sc);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -408,8 +368,8 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
           u[i][e] = t * w1[e];
           dot1 += u[i][e] * n[i][e];
         }
-        Vec<RES, VEC>::store((RES *)a.dres + row * a.dim + c * VEC, dh[i]);
-        if (a.act >= 0) Vec<IO, VEC>::store((IO *)a.dgate + row * a.dim + c * VEC, df[i]);
+        store_vec<RES, VEC, TAIL>((RES *)a.dres + row * a.dim + c * VEC, a.dim - c * VEC, dh[i]);
+        if (a.act >= 0) store_vec<IO, VEC, TAIL>((IO *)a.dgate + row * a.dim + c * VEC, a.dim - c * VEC, df[i]);
       }
     }
     // without a post-norm x's gradient is z's
@@ -420,13 +380,13 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
       if (c < nv) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) u[i][e] = r1 * (u[i][e] - n[i][e] * dot1);
-        Vec<IO, VEC>::store((IO *)a.dx + row * a.dim + c * VEC, u[i]);
+        store_vec<IO, VEC, TAIL>((IO *)a.dx + row * a.dim + c * VEC, a.dim - c * VEC, u[i]);
       }
     }
   }
-  write_partial<VEC, NV, BLOCK>(dw2, tm, a.dim, a.part[0], cols);
-  if (a.w_post) write_partial<VEC, NV, BLOCK>(dw1, tm, a.dim, a.part[1], cols);
-  if (a.scale) write_partial<VEC, NV, BLOCK>(ds, tm, a.dim, a.part[2], cols);
+  write_partial<VEC, TAIL, NV, BLOCK>(dw2, tm, a.dim, a.part[0], cols);
+  if (a.w_post) write_partial<VEC, TAIL, NV, BLOCK>(dw1, tm, a.dim, a.part[1], cols);
+  if (a.scale) write_partial<VEC, TAIL, NV, BLOCK>(ds, tm, a.dim, a.part[2], cols);
 }
 
 // out[c] = sum over the workgroups' partial rows, in a fixed order: 64 groups of
@@ -463,156 +423,131 @@ int pow2_at_least(int n) {
   return p;
 }
 
-bool aligned(const void *p, int64_t stride, int elem) {
-  return ((uintptr_t)p & 15) == 0 && (stride * elem) % 16 == 0;
-}
-
-// The shape of a team for rows of nv vectors.
+// The shape of a team for rows of nv vectors of `vec` elements.
 struct TeamPlan {
-  int team, nv, block;
+  int team, nv;
+  int threads;  // 0: teams of up to a wave, in workgroups of 256; else the row's workgroup is of at most so many
 };
 // Forward: a wave holds a row of up to 256 vectors (4 a lane), for the fewest
-// exchanges; longer rows take a workgroup.
+// exchanges; then 256 threads, 4 vectors each (4096 x 4096 bf16: TODO us where 1024
+// threads of one vector take 85).
 TeamPlan plan_forward(int nv) {
   if (nv <= 256) {
     const int team = nv >= 64 ? 64 : pow2_at_least(nv);
     return {team, (nv + team - 1) / team, 0};
   }
-  const int most = nv > 4096 ? 16 : 4;
-  const int team = pow2_at_least((nv + most - 1) / most);
-  return {team, (nv + team - 1) / team, 1};
+  const int team = nv <= 1024 ? 256 : 1024;
+  return {team, (nv + team - 1) / team, team};
 }
 // Reverse: the weights' sums stay in registers beside five inputs, so that a
-// thread holds one vector where 1024 threads can hold the row.
-TeamPlan plan_reverse(int nv) {
-  int team = pow2_at_least(nv);
-  if (team > 1024) team = 1024;
-  return {team, (nv + team - 1) / team, team > 64};
+// thread holds 8 elements, or 16 where it has 256 registers (512 threads); rows
+// of more than 8192 spill.
+TeamPlan plan_reverse(int nv, int vec) {
+  const int one = 8 / vec;  // vectors of 8 elements
+  if (nv <= 64 * one) {
+    const int team = nv >= 64 ? 64 : pow2_at_least(nv);
+    return {team, (nv + team - 1) / team, 0};
+  }
+  int team;
+  if (nv <= 256 * one) team = pow2_at_least((nv + one - 1) / one);
+  else if (nv <= 512 * one) team = vec == 8 ? 256 : 512;
+  else team = vec == 8 && nv <= 1024 ? 512 : 1024;
+  return {team, (nv + team - 1) / team, team <= 256 ? 256 : team};
 }
 
-}  // namespace
-
-#define NORM_LAUNCH(NV, BLK, THREADS, KERNEL, ...)                                                 \
-  KERNEL<__VA_ARGS__, NV, BLK, THREADS><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
-// The last type argument is the vector's width: rows of more than 4 vectors a
-// thread are those of single elements.
-#define NORM_PICK_FORWARD(KERNEL, VEC, ...)                                                        \
-  do {                                                                                             \
-    if (!p.block && p.nv == 1) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);               \
-    else if (!p.block && p.nv == 2) NORM_LAUNCH(2, false, 256, KERNEL, __VA_ARGS__, VEC);          \
-    else if (!p.block) NORM_LAUNCH(4, false, 256, KERNEL, __VA_ARGS__, VEC);                       \
-    else if (p.nv <= 4) NORM_LAUNCH(4, true, 1024, KERNEL, __VA_ARGS__, VEC);                      \
-    else if constexpr (VEC == 1) NORM_LAUNCH(16, true, 1024, KERNEL, __VA_ARGS__, VEC);            \
-  } while (0)
-// A thread of the reverse modes holds 8 elements of a row without spilling; 16 (rows
-// of more than 8192) spill.
-#define NORM_PICK_REVERSE(KERNEL, VEC, ...)                                                        \
-  do {                                                                                             \
-    if (grid == 0) break; /* no rows: the weights' sums are still written */                       \
-    if (!p.block) NORM_LAUNCH(1, false, 256, KERNEL, __VA_ARGS__, VEC);                            \
-    else if (p.team <= 256) NORM_LAUNCH(1, true, 256, KERNEL, __VA_ARGS__, VEC);                   \
-    else if (p.nv == 1) NORM_LAUNCH(1, true, 1024, KERNEL, __VA_ARGS__, VEC);                      \
-    else if (p.nv == 2) NORM_LAUNCH(2, true, 1024, KERNEL, __VA_ARGS__, VEC);                      \
-    else if constexpr (VEC < 8) {                                                                  \
-      if (p.nv <= 4) NORM_LAUNCH(4, true, 1024, KERNEL, __VA_ARGS__, VEC);                         \
-      else if constexpr (VEC == 1) {                                                               \
-        if (p.nv <= 8) NORM_LAUNCH(8, true, 1024, KERNEL, __VA_ARGS__, VEC);                       \
-        else NORM_LAUNCH(16, true, 1024, KERNEL, __VA_ARGS__, VEC);                                \
-      }                                                                                            \
-    }                                                                                              \
-  } while (0)
-
-static int row_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
-  const int64_t per = p.block ? 1 : 256 / p.team;
+int row_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
+  const int64_t per = p.threads ? 1 : 256 / p.team;
   const int64_t n = (rows + per - 1) / per;
   return (int)(n < most ? n : most);
 }
 
 // Workgroups of a reverse mode: one alone where it passes the rows in four steps
-// (its sums are the weights' gradients: no second launch), else up to `most`.
-static int reverse_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
-  const int64_t per = p.block ? 1 : 256 / p.team;
+// (its sums are the weights' gradients: no second launch), else up to `most` or
+// what the chip holds at a time.
+int reverse_blocks(int64_t rows, const TeamPlan &p, int64_t most) {
+  const int64_t per = p.threads ? 1 : 256 / p.team;
   if (rows > 0 && rows <= 4 * per) return 1;
-  if (p.team >= 512) most = most < 256 * (1024 / p.team) ? most : 256 * (1024 / p.team);
-  return row_blocks(rows, p, most);
+  const int64_t hold = p.threads == 0 ? 1536 : p.threads > 256 ? 256 : p.nv > 1 ? 512 : 768 * (256 / p.team);
+  return row_blocks(rows, p, most < hold ? most : hold);
 }
 
-hipError_t launch_gated_norm(const GatedNormArgs &a, hipStream_t st) {
-  const int64_t rows = a.tokens * a.heads;
-  const int e = a.bf16 ? 2 : 4, vec = 16 / e;
-  const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.y, a.dim, e) &&
-                    aligned(a.weight, 4, 4) && (a.act < 0 || aligned(a.gate, a.gate_stride, e));
-  const TeamPlan p = plan_forward(wide ? a.dim / vec : a.dim);
-  const int grid = row_blocks(rows, p, 1 << 20);
-  TimedLaunch tl(K_NORM, st);
-  if (a.bf16) {
-    if (wide) NORM_PICK_FORWARD(gated_norm_kernel, 8, u16);
-    else NORM_PICK_FORWARD(gated_norm_kernel, 1, u16);
-  } else {
-    if (wide) NORM_PICK_FORWARD(gated_norm_kernel, 4, float);
-    else NORM_PICK_FORWARD(gated_norm_kernel, 1, float);
-  }
-  return hipGetLastError();
+template <int VEC, bool TAIL> struct Width {
+  static constexpr int vec = VEC;
+  static constexpr bool tail = TAIL;
+};
+// f(Width<VEC, TAIL>) for rows of `dim` channels
+template <int VEC, typename F> void with_width(int dim, F f) {
+  if (dim % VEC == 0) f(Width<VEC, false>{});
+  else f(Width<VEC, true>{});
 }
 
-hipError_t launch_gated_norm_bwd(const GatedNormArgs &args, hipStream_t st) {
-  GatedNormArgs a = args;
+// LAUNCH(vectors a thread, a workgroup holds the row, its threads at most)
+#define NORM_FORWARD(LAUNCH)                                                    \
+  do {                                                                          \
+    if (p.threads == 0 && p.nv == 1) LAUNCH(1, false, 256);                     \
+    else if (p.threads == 0 && p.nv == 2) LAUNCH(2, false, 256);                \
+    else if (p.threads == 0) LAUNCH(4, false, 256);                             \
+    else if (p.threads == 256) LAUNCH(4, true, 256);                            \
+    else if (p.nv == 2) LAUNCH(2, true, 1024);                                  \
+    else if constexpr (W::vec < 8) LAUNCH(4, true, 1024);                       \
+  } while (0)
+#define NORM_REVERSE(LAUNCH)                                                    \
+  do {                                                                          \
+    if (grid == 0) break; /* no rows: the weights' sums are still written */    \
+    if (p.threads == 0 && p.nv == 1) LAUNCH(1, false, 256);                     \
+    else if (p.threads == 256 && p.nv == 1) LAUNCH(1, true, 256);               \
+    else if (p.threads == 256) LAUNCH(2, true, 256);                            \
+    else if (p.threads == 512) LAUNCH(2, true, 512);                            \
+    else if (p.threads == 1024 && p.nv == 2) LAUNCH(2, true, 1024);             \
+    else if constexpr (W::vec < 8) {                                            \
+      if (p.threads == 0) LAUNCH(2, false, 256);                                \
+      else LAUNCH(4, true, 1024);                                               \
+    }                                                                           \
+  } while (0)
+
+template <typename IO, int VEC> void gated_forward(const GatedNormArgs &a, hipStream_t st) {
+  const TeamPlan p = plan_forward((a.dim + VEC - 1) / VEC);
+  const int grid = row_blocks(a.tokens * a.heads, p, 1 << 20);
+  with_width<VEC>(a.dim, [&](auto w) {
+    using W = decltype(w);
+#define LAUNCH(NV, BLK, N) \
+  gated_norm_kernel<IO, W::vec, W::tail, NV, BLK, N><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
+    NORM_FORWARD(LAUNCH);
+#undef LAUNCH
+  });
+}
+
+template <typename IO, int VEC> void gated_reverse(GatedNormArgs a, hipStream_t st) {
   const int64_t rows = a.tokens * a.heads;
-  const int e = a.bf16 ? 2 : 4, vec = 16 / e;
-  const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.dy, a.dy_stride, e) &&
-                    aligned(a.dx, a.dim, e) && aligned(a.weight, 4, 4) && aligned(a.dweight, a.dim, 4) &&
-                    (a.act < 0 || (aligned(a.gate, a.gate_stride, e) && aligned(a.dgate, a.dim, e)));
-  const TeamPlan p = plan_reverse(wide ? a.dim / vec : a.dim);
+  const TeamPlan p = plan_reverse((a.dim + VEC - 1) / VEC, VEC);
   const int grid = reverse_blocks(rows, p, norm_bwd_blocks(rows, a.dim));
   float *const part = a.part;
   if (grid == 1) a.part = a.dweight;
-  TimedLaunch tl(K_NORM_BWD, st);
-  if (a.bf16) {
-    if (wide) NORM_PICK_REVERSE(gated_norm_bwd_kernel, 8, u16);
-    else NORM_PICK_REVERSE(gated_norm_bwd_kernel, 1, u16);
-  } else {
-    if (wide) NORM_PICK_REVERSE(gated_norm_bwd_kernel, 4, float);
-    else NORM_PICK_REVERSE(gated_norm_bwd_kernel, 1, float);
-  }
+  with_width<VEC>(a.dim, [&](auto w) {
+    using W = decltype(w);
+#define LAUNCH(NV, BLK, N) \
+  gated_norm_bwd_kernel<IO, W::vec, W::tail, NV, BLK, N><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
+    NORM_REVERSE(LAUNCH);
+#undef LAUNCH
+  });
   if (grid != 1)
     norm_partials_kernel<<<dim3((a.dim + 15) / 16, 1), 1024, 0, st>>>(part, grid, a.dim, a.dweight, nullptr, nullptr);
-  return hipGetLastError();
 }
 
-hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t st) {
-  const int e = a.bf16 ? 2 : 4, re = a.res_bf16 ? 2 : 4, vec = 16 / e;
-  const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.residual, a.dim, re) &&
-                    aligned(a.h, a.dim, re) && aligned(a.y, a.dim, e) && aligned(a.w_pre, 4, 4) &&
-                    (!a.w_post || aligned(a.w_post, 4, 4)) && (!a.scale || aligned(a.scale, 4, 4)) &&
-                    (a.act < 0 || aligned(a.gate, a.gate_stride, e));
-  const TeamPlan p = plan_forward(wide ? a.dim / vec : a.dim);
+template <typename IO, typename RES, int VEC> void residual_forward(const ResidualNormArgs &a, hipStream_t st) {
+  const TeamPlan p = plan_forward((a.dim + VEC - 1) / VEC);
   const int grid = row_blocks(a.tokens, p, 1 << 20);
-  TimedLaunch tl(K_NORM, st);
-  if (a.bf16) {
-    if (a.res_bf16) {
-      if (wide) NORM_PICK_FORWARD(residual_norm_kernel, 8, u16, u16);
-      else NORM_PICK_FORWARD(residual_norm_kernel, 1, u16, u16);
-    } else {
-      if (wide) NORM_PICK_FORWARD(residual_norm_kernel, 8, u16, float);
-      else NORM_PICK_FORWARD(residual_norm_kernel, 1, u16, float);
-    }
-  } else {
-    if (wide) NORM_PICK_FORWARD(residual_norm_kernel, 4, float, float);
-    else NORM_PICK_FORWARD(residual_norm_kernel, 1, float, float);
-  }
-  return hipGetLastError();
+  with_width<VEC>(a.dim, [&](auto w) {
+    using W = decltype(w);
+#define LAUNCH(NV, BLK, N) \
+  residual_norm_kernel<IO, RES, W::vec, W::tail, NV, BLK, N><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
+    NORM_FORWARD(LAUNCH);
+#undef LAUNCH
+  });
 }
 
-hipError_t launch_residual_norm_bwd(const ResidualNormArgs &args, hipStream_t st) {
-  ResidualNormArgs a = args;
-  const int e = a.bf16 ? 2 : 4, re = a.res_bf16 ? 2 : 4, vec = 16 / e;
-  const bool wide = a.dim % vec == 0 && aligned(a.x, a.x_stride, e) && aligned(a.residual, a.dim, re) &&
-                    aligned(a.dy, a.dim, e) && aligned(a.dx, a.dim, e) && aligned(a.dres, a.dim, re) &&
-                    (!a.dh || aligned(a.dh, a.dim, re)) && aligned(a.dw_pre, a.dim, 4) &&
-                    (!a.w_post || aligned(a.dw_post, a.dim, 4)) && (!a.scale || aligned(a.dscale, a.dim, 4)) && aligned(a.w_pre, 4, 4) &&
-                    (!a.w_post || aligned(a.w_post, 4, 4)) && (!a.scale || aligned(a.scale, 4, 4)) &&
-                    (a.act < 0 || (aligned(a.gate, a.gate_stride, e) && aligned(a.dgate, a.dim, e)));
-  const TeamPlan p = plan_reverse(wide ? a.dim / vec : a.dim);
+template <typename IO, typename RES, int VEC> void residual_reverse(ResidualNormArgs a, hipStream_t st) {
+  const TeamPlan p = plan_reverse((a.dim + VEC - 1) / VEC, VEC);
   const int grid = reverse_blocks(a.tokens, p, norm_bwd_blocks(a.tokens, a.dim));
   float *const part = a.part[0];
   a.part[1] = part + (int64_t)grid * a.dim;
@@ -622,22 +557,47 @@ hipError_t launch_residual_norm_bwd(const ResidualNormArgs &args, hipStream_t st
     a.part[1] = a.dw_post;
     a.part[2] = a.dscale;
   }
-  TimedLaunch tl(K_NORM_BWD, st);
-  if (a.bf16) {
-    if (a.res_bf16) {
-      if (wide) NORM_PICK_REVERSE(residual_norm_bwd_kernel, 8, u16, u16);
-      else NORM_PICK_REVERSE(residual_norm_bwd_kernel, 1, u16, u16);
-    } else {
-      if (wide) NORM_PICK_REVERSE(residual_norm_bwd_kernel, 8, u16, float);
-      else NORM_PICK_REVERSE(residual_norm_bwd_kernel, 1, u16, float);
-    }
-  } else {
-    if (wide) NORM_PICK_REVERSE(residual_norm_bwd_kernel, 4, float, float);
-    else NORM_PICK_REVERSE(residual_norm_bwd_kernel, 1, float, float);
-  }
+  with_width<VEC>(a.dim, [&](auto w) {
+    using W = decltype(w);
+#define LAUNCH(NV, BLK, N) \
+  residual_norm_bwd_kernel<IO, RES, W::vec, W::tail, NV, BLK, N><<<grid, BLK ? p.team : 256, 0, st>>>(a, p.team)
+    NORM_REVERSE(LAUNCH);
+#undef LAUNCH
+  });
   if (grid != 1)
     norm_partials_kernel<<<dim3((a.dim + 15) / 16, 3), 1024, 0, st>>>(
         part, grid, a.dim, a.dw_pre, a.w_post ? a.dw_post : nullptr, a.scale ? a.dscale : nullptr);
+}
+
+}  // namespace
+
+hipError_t launch_gated_norm(const GatedNormArgs &a, hipStream_t st) {
+  TimedLaunch tl(K_NORM, st);
+  if (a.bf16) gated_forward<u16, 8>(a, st);
+  else gated_forward<float, 4>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_norm_bwd(const GatedNormArgs &a, hipStream_t st) {
+  TimedLaunch tl(K_NORM_BWD, st);
+  if (a.bf16) gated_reverse<u16, 8>(a, st);
+  else gated_reverse<float, 4>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t st) {
+  TimedLaunch tl(K_NORM, st);
+  if (a.bf16 && a.res_bf16) residual_forward<u16, u16, 8>(a, st);
+  else if (a.bf16) residual_forward<u16, float, 8>(a, st);
+  else residual_forward<float, float, 4>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t st) {
+  TimedLaunch tl(K_NORM_BWD, st);
+  if (a.bf16 && a.res_bf16) residual_reverse<u16, u16, 8>(a, st);
+  else if (a.bf16) residual_reverse<u16, float, 8>(a, st);
+  else residual_reverse<float, float, 4>(a, st);
   return hipGetLastError();
 }
 
