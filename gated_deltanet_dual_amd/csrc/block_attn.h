@@ -15,6 +15,7 @@ namespace flare {
 struct AttnPlan {
   int prefix_tiles, own_tiles;  // 16-row query tiles of a wave (4 waves a workgroup)
   int page_shift;
+  int merged;                   // a short prefix: every request passes it before its own keys
   int prefix_parts, prefix_chunk, prefix_groups;  // parts of the prefix, keys a part, row groups
   int own_parts, own_chunk, own_groups;
   int64_t prefix_blocks, own_blocks;              // prefix: a multiple of 8, some of them empty

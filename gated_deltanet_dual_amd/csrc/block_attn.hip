@@ -97,6 +97,7 @@ __device__ __forceinline__ int k_piece(int row, int c) {
 struct Part {
   uint32_t row0, row_end;
   int head, k0, k1, out;  // out: the part's place in the workspace
+  int pre;                // keys of the prefix that come before k0 (a short prefix, not shared)
   int len, req;           // own keys of the request; req < 0: the prefix
   const int32_t *table;
 };
@@ -122,6 +123,7 @@ __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan
     w.k0 = part * p.prefix_chunk;
     w.k1 = w.len - w.k0 < p.prefix_chunk ? w.len : w.k0 + p.prefix_chunk;
     w.out = part;
+    w.pre = 0;
     w.req = -1;
     w.table = a.prefix_table;
     return true;
@@ -141,6 +143,7 @@ __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan
   w.k0 = part * p.own_chunk;
   w.k1 = w.len - w.k0 < p.own_chunk ? w.len : w.k0 + p.own_chunk;
   w.out = p.prefix_parts + part;
+  w.pre = p.merged ? a.prefix_len : 0;
   w.table = a.block_table + (int64_t)w.req * a.max_pages;
   // a part behind the request's length is not read by the joining launch; the
   // only part is written in any case
@@ -166,21 +169,26 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
   const uint32_t G = a.q_heads / a.kv_heads;
   const uint32_t row0 = w.row0 + ((wave + turn) & 3) * (NQ * 16);
   const bool live = row0 < w.row_end;
-  const int tiles = k1 > k0 ? (k1 - k0 + TK - 1) / TK : 0;
-  // keys below `all` are seen by every row: the tiles below it need no mask
+  const int pre_tiles = (w.pre + TK - 1) / TK;
+  const int tiles = pre_tiles + (k1 > k0 ? (k1 - k0 + TK - 1) / TK : 0);
+  // own keys below `all` are seen by every row: the tiles below it need no mask
   const bool causal = a.causal && w.req >= 0;
   int all = causal ? w.len - (a.block - 1) : w.len;
   if (all > k1) all = k1;
-  const int full = all > k0 ? (all - k0) / TK : 0;
 
-  // lane i holds the page of the subtile of tile i that this wave loads
-  const int last = (k1 - 1) & ~15;
+  // the first key of this wave's subtile of tile t, no later than the last subtile
+  // that holds keys: of the prefix for the first pre_tiles, else of the own keys
   const int sub = wave % SUBS;
+  auto subtile = [&](int t) {
+    const int end = t < pre_tiles ? w.pre : k1;
+    const int j = (t < pre_tiles ? TK * t : k0 + TK * (t - pre_tiles)) + 16 * sub, last = (end - 1) & ~15;
+    return j < last ? j : last;
+  };
+  // lane i holds the page of tile i's
   int page_id = 0;
   if (tiles > 0) {
-    int j = k0 + TK * lane + 16 * sub;
-    if (j > last) j = last;
-    page_id = w.table[j >> p.page_shift];
+    const int t = lane < tiles ? lane : tiles - 1;
+    page_id = (t < pre_tiles ? a.prefix_table : w.table)[subtile(t) >> p.page_shift];
     if (page_id < 0) page_id = 0;
     if (page_id >= a.num_pages) page_id = (int)a.num_pages - 1;
   }
@@ -192,9 +200,7 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
   const uint32_t vy = 2 * (lane / PIECES * D + v_piece<D>(lane / PIECES, lane % PIECES) * 8);
   const uint32_t k_at = lds_at(&kt_lds[0][sub * 16 * D]), v_at = lds_at(&vt_lds[0][sub * 16 * D]);
   auto stage = [&](int t, int buf) {
-    int j = k0 + TK * t + 16 * sub;
-    if (j > last) j = last;
-    const int pg = __builtin_amdgcn_readlane(page_id, t);
+    const int j = subtile(t), pg = __builtin_amdgcn_readlane(page_id, t);
     const int64_t at = ((((int64_t)pg * a.kv_heads + head) << p.page_shift) + (j & (a.page - 1))) * D;
     const u16 *kp = uniform((const u16 *)a.k_cache + at), *vp = uniform((const u16 *)a.v_cache + at);
     const uint32_t to = buf * (TK * D * 2);
@@ -206,7 +212,9 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
       if (SUBS == 4 || wave >= 2) load_lds16<NT>(vp, vy ^ vx, v_at + to + i * 1024);
     }
   };
-  if (tiles > 0) stage(0, 0);
+  // tile t's buffer: the own keys' first is buffer 0
+  auto buffer = [&](int t) { return (t + pre_tiles) & 1; };
+  if (tiles > 0) stage(0, buffer(0));
 
   // the queries, and in the last tiles of a request how many keys each sees
   bf16x8 q[NQ][KS];
@@ -243,12 +251,14 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
     for (int d = 0; d < DT; ++d) o[n][d] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
   // this lane's places in a tile: K operand step e, V channel tile d; rows
-  // further down by multiples of 16 are constant offsets from them
-  int ka[KS], va[DT];
+  // further down by multiples of 16 are constant offsets from them, and so are
+  // steps and channel tiles beyond the 256 bytes in which the pieces change places
+  constexpr int KA = KS < 4 ? KS : 4, VA = DT < 8 ? DT : 8;
+  int ka[KA], va[VA];
 #pragma unroll
-  for (int e = 0; e < KS; ++e) ka[e] = col * D + k_piece<D>(col, 4 * e + grp) * 8;
+  for (int e = 0; e < KA; ++e) ka[e] = col * D + k_piece<D>(col, 4 * e + grp) * 8;
 #pragma unroll
-  for (int d = 0; d < DT; ++d) {
+  for (int d = 0; d < VA; ++d) {
     const int r = 4 * grp + (col >> 2);
     va[d] = r * D + v_piece<D>(r, 2 * d + ((col & 3) >> 1)) * 8 + (col & 1) * 4;
   }
@@ -256,29 +266,32 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
   auto read_v = [&](u16 *vb, int h, bf16x8 (&vf)[DT]) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + 32 * h * D));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d] + (32 * h + 16) * D));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d % VA] + d / VA * 128 + 32 * h * D));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d % VA] + d / VA * 128 + (32 * h + 16) * D));
       vf[d] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   };
-  auto tile = [&](int t, const u16 *kb, u16 *vb, auto ragged) {
-    const int kt = k0 + TK * t;
+  // keys kt .. of a tile, of which those below `end` exist; ragged: not all of them
+  // are seen by every row
+  auto tile = [&](int kt, int end, bool own, const u16 *kb, u16 *vb, auto ragged) {
     bool odd = false;
     if constexpr (ragged.value) {
       // V rows behind the length hold anything: 0 * NaN must not reach O.  Rows that
       // only some of the block's queries see are looked through for infinities and NaN.
-      bool mine = false;
-      for (int i = threadIdx.x; i < TK * PIECES; i += 256) {
-        const int key = kt + i / PIECES;
-        if (key >= k1) {
-          *reinterpret_cast<u32x4v *>(vb + 8 * i) = u32x4v{0, 0, 0, 0};
-        } else if (key >= all) {
-          const u32x4v v = *reinterpret_cast<const u32x4v *>(vb + 8 * i);
+      if (kt + TK > end || (own && kt + TK > all)) {
+        bool mine = false;
+        for (int i = threadIdx.x; i < TK * PIECES; i += 256) {
+          const int key = kt + i / PIECES;
+          if (key >= end) {
+            *reinterpret_cast<u32x4v *>(vb + 8 * i) = u32x4v{0, 0, 0, 0};
+          } else if (own && key >= all) {
+            const u32x4v v = *reinterpret_cast<const u32x4v *>(vb + 8 * i);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mine |= (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+            for (int e = 0; e < 4; ++e) mine |= (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+          }
         }
+        odd = __syncthreads_or(mine);
       }
-      odd = __syncthreads_or(mine);
     }
     if (!live) return;
 #pragma unroll
@@ -290,7 +303,7 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
           const bf16x8 kf =
-              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4v *>(kb + ka[e] + (32 * h + 16 * sb) * D));
+              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4v *>(kb + ka[e % KA] + e / KA * 128 + (32 * h + 16 * sb) * D));
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
             if (e == 0) s[n][sb] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -307,7 +320,7 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
         if constexpr (ragged.value) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (kt + 32 * h + 16 * (e >> 2) + 4 * grp + (e & 3) >= lim[n]) s[n][e >> 2][e & 3] = -INFINITY;
+            if (kt + 32 * h + 16 * (e >> 2) + 4 * grp + (e & 3) >= (own ? lim[n] : end)) s[n][e >> 2][e & 3] = -INFINITY;
         }
         top[n] = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), s[n][0][2]), s[n][0][3]);
         top[n] = fmaxf(fmaxf(fmaxf(fmaxf(top[n], s[n][1][0]), s[n][1][1]), s[n][1][2]), s[n][1][3]);
@@ -378,20 +391,42 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
     }
   };
   meet();
+  // The prefix's tiles (with masks: one loop for all that may need them), then the
+  // own keys that every row sees, two tiles a pass so that the buffers are
+  // constants (at d = 256 one: two spill, 69 us where one takes 35), then the last
+  // ones with masks.
+  const int whole = pre_tiles + (all > k0 ? (all - k0) / TK : 0);
   int t = 0;
-  for (; t < full; t += 2) {
-    if (t + 1 < tiles) stage(t + 1, 1);
-    tile(t, kt_lds[0], vt_lds[0], Const<false>{});
-    meet();
-    if (t + 1 >= full) break;
-    if (t + 2 < tiles) stage(t + 2, 0);
-    tile(t + 1, kt_lds[1], vt_lds[1], Const<false>{});
-    meet();
-  }
-  for (t = full; t < tiles; ++t) {
-    if (t + 1 < tiles) stage(t + 1, (t + 1) & 1);
-    tile(t, kt_lds[t & 1], vt_lds[t & 1], Const<true>{});
-    meet();
+#pragma unroll 1
+  for (int own = pre_tiles > 0 ? 0 : 1; own < 2; ++own) {
+    if (own && D == 256) {
+#pragma unroll 1
+      for (; t < whole; ++t) {
+        if (t + 1 < tiles) stage(t + 1, buffer(t + 1));
+        tile(0, 0, true, kt_lds[buffer(t)], vt_lds[buffer(t)], Const<false>{});
+        meet();
+      }
+    } else if (own) {
+      for (; t < whole; t += 2) {
+        if (t + 1 < tiles) stage(t + 1, 1);
+        tile(0, 0, true, kt_lds[0], vt_lds[0], Const<false>{});
+        meet();
+        if (t + 1 >= whole) {
+          ++t;
+          break;
+        }
+        if (t + 2 < tiles) stage(t + 2, 0);
+        tile(0, 0, true, kt_lds[1], vt_lds[1], Const<false>{});
+        meet();
+      }
+    }
+    const int stop = own ? tiles : pre_tiles, end = own ? k1 : w.pre;
+#pragma unroll 1
+    for (; t < stop; ++t) {
+      if (t + 1 < tiles) stage(t + 1, buffer(t + 1));
+      tile(own ? k0 + TK * (t - pre_tiles) : TK * t, end, own, kt_lds[buffer(t)], vt_lds[buffer(t)], Const<true>{});
+      meet();
+    }
   }
 
   const int64_t rows_all = (int64_t)a.num_req * a.block * a.q_heads;

@@ -61,6 +61,23 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
       p.own_parts = (int)parts;
     }
   }
+  // A short prefix is passed by every request before its own keys, in one part: no
+  // join and no second launch, where that takes less than its sharing does.
+  const int64_t tile = a.dim == 256 ? 32 : 64;
+  if (a.prefix_len > 0 && ceil_div(a.prefix_len, tile) + ceil_div(a.max_seq_len, tile) <= 64) {
+    const int64_t together = ceil_div(units, kSlots) * (a.prefix_len + a.max_seq_len + kStart);
+    const int64_t longer = p.prefix_chunk < a.prefix_len ? p.prefix_chunk : a.prefix_len;
+    const int64_t own = p.own_chunk < a.max_seq_len ? p.own_chunk : a.max_seq_len;
+    const int64_t apart = ceil_div(p.prefix_blocks + units * p.own_parts, kSlots) * ((longer > own ? longer : own) + kStart) +
+                          (p.prefix_parts + p.own_parts) * join + kStart;
+    if (together <= apart) {
+      p.merged = 1;
+      p.prefix_parts = 0;
+      p.prefix_blocks = 0;
+      p.own_parts = 1;
+      p.own_chunk = (int)longest;
+    }
+  }
   if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
   p.own_blocks = units * p.own_parts;
   return p;

@@ -90,6 +90,13 @@ CASES = [
     (33, 2, 1, 2, 256, 16, [(i * 7) % 40 for i in range(33)], 700),
     (64, 1, 1, 1, 64, 16, [0] * 64, 1000),
     (13, 1, 1, 8, 128, 128, [0] * 13, 200),
+    # prefixes too long for one part with the own keys: shared by the requests' rows, few and many, parts joined
+    (3, 2, 2, 2, 128, 16, [0, 33, 70], 4100),
+    (9, 8, 1, 3, 128, 64, [8 + 9 * i for i in range(9)], 4200),
+    (20, 2, 1, 4, 64, 32, [(i * 17) % 60 for i in range(20)], 4300),
+    (5, 4, 1, 4, 256, 16, [4, 0, 16, 37, 300], 2100),
+    (2, 20, 1, 8, 128, 32, [20, 131], 5000),
+    (1, 1, 1, 1, 64, 16, [1], 4097),
 ]
 
 

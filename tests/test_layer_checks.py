@@ -110,7 +110,7 @@ def test_step_tables(L):
 
 
 def attention(L, R=2, block=4, qh=8, kh=2, d=128, page=64, io=g.BF16, causal=0, scale=0.0, q=FAKE, pages=100, bt=FAKE, wide=8,
-              lens=FAKE, most=512, pt=FAKE, n=100, ws=FAKE & ~255, nbytes=1 << 40):
+              lens=FAKE, most=512, pt=FAKE, n=5000, ws=FAKE & ~255, nbytes=1 << 40):
     s = g.AttentionShape(block, qh, kh, d, page, io, causal, scale)
     return L.flare_block_attention(R, ctypes.byref(s), q, FAKE, FAKE, pages, bt, wide, lens, most, pt, n, FAKE, None, ws,
                                    nbytes, None)
@@ -126,12 +126,13 @@ def test_block_attention(L):
     for bad in ("q", "bt", "lens", "pt"):
         assert attention(L, **{bad: None}) == 1, bad
     assert attention(L, q=FAKE + 8) == 3
-    need = g.block_attention_workspace_bytes(2, 4, 8, 2, 128, 64, 512, 100)
+    need = g.block_attention_workspace_bytes(2, 4, 8, 2, 128, 64, 512, 5000)
     assert need > 0 and attention(L, nbytes=need - 1) == 5 and attention(L, ws=None) == 5
     assert attention(L, ws=(FAKE & ~255) + 64) == 5
     assert attention(L, R=0, q=None, lens=None, bt=None, pt=None) == 0
-    # one part alone is written without a workspace
+    # one part alone is written without a workspace, a short prefix in it
     assert g.block_attention_workspace_bytes(2, 4, 8, 2, 128, 64, 64, 0) == 0
+    assert g.block_attention_workspace_bytes(2, 4, 8, 2, 128, 64, 64, 100) == 0
     assert g.block_attention_workspace_bytes(2, 4, 8, 2, 100, 64, 512, 100) == 0  # not instantiated
 
 
@@ -141,11 +142,11 @@ def test_attention_workspace_is_rows_times_parts(L, R, B, Hq, Hk, d, own, prefix
     """The workspace holds d + 2 floats a row and part, plus its alignment; the
     parts of at most 4096 keys (2048 at d = 256) cover the lengths."""
     n = g.block_attention_workspace_bytes(R, B, Hq, Hk, d, 16, own, prefix)
+    longest = 2048 if d == 256 else 4096
     if n == 0:
-        assert own <= 4096 and prefix == 0
+        assert own + prefix <= longest
         return
     parts, rest = divmod(n - 256, R * B * Hq * (d + 2) * 4)
-    longest = 2048 if d == 256 else 4096
     assert rest == 0 and parts >= -(-own // longest) + -(-prefix // longest) and parts >= 2
 
 
