@@ -12,6 +12,10 @@
 
 namespace flare {
 
+// Workgroups come in octets, one for each XCD, and runs of 32 octets, one for each of
+// an XCD's CUs.
+constexpr int kOctets = 32;
+
 struct AttnPlan {
   int prefix_tiles, own_tiles;  // 16-row query tiles of a wave (4 waves a workgroup)
   int page_shift;
@@ -19,6 +23,7 @@ struct AttnPlan {
   int prefix_parts, prefix_chunk, prefix_groups;  // parts of the prefix, keys a part, row groups
   int own_parts, own_chunk, own_groups;
   int64_t prefix_blocks, own_blocks;              // prefix: a multiple of 8, some of them empty
+  int prefix_runs, own_runs;                      // and how many runs each fills
 };
 
 // A request's own keys: never more than its table or the caller's bound holds.

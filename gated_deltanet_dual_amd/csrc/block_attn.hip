@@ -102,17 +102,20 @@ struct Part {
   const int32_t *table;
 };
 
-// Workgroups of the prefix and of the requests' own keys alternate in octets
-// (one for each XCD), in proportion: the prefix is bound by its products, the
-// own keys by memory, so a CU holds both kinds at a time.  The units (head, part)
-// of the prefix go round the XCDs and a unit's row groups stay on one: they read
-// the same keys from its L2.
+// Workgroups of the prefix and of the requests' own keys alternate in runs of one
+// workgroup for each CU, in proportion and the prefix first: the prefix is bound by
+// its products, the own keys by memory, so a CU holds both kinds at a time (256
+// requests x 4, 16 query and 4 kv heads of 128, prefix 8192 and own 1024: 120 us
+// where alternating octets, which leave some CUs two of a kind, took 145).  The units
+// (head, part) of the prefix go round the XCDs and a unit's row groups stay on one:
+// they read the same keys from its L2.
 template <int PREFIX_ROWS, int OWN_ROWS>
 __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan &p, Part &w) {
   const uint32_t G = a.q_heads / a.kv_heads, BG = a.block * G;
-  const uint64_t po = p.prefix_blocks / 8, all = po + (p.own_blocks + 7) / 8, oct = blockIdx.x / 8;
-  const uint32_t pi = (uint32_t)(oct * po / all);  // octets of the prefix before this one
-  if ((oct + 1) * po / all > pi) {
+  const uint32_t run = blockIdx.x / 8 / kOctets, in = blockIdx.x / 8 % kOctets, all = p.prefix_runs + p.own_runs;
+  const uint32_t before = ((uint64_t)run * p.prefix_runs + all - 1) / all;  // runs of the prefix before this one
+  if (((uint64_t)(run + 1) * p.prefix_runs + all - 1) / all > before) {
+    const uint32_t pi = before * kOctets + in;
     const uint32_t unit = pi / p.prefix_groups * 8 + blockIdx.x % 8, rg = pi % p.prefix_groups;
     if (unit >= (uint32_t)(a.kv_heads * p.prefix_parts)) return false;
     const int part = (int)(unit / a.kv_heads);
@@ -128,7 +131,7 @@ __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan
     w.table = a.prefix_table;
     return true;
   }
-  uint32_t id = (uint32_t)(oct - pi) * 8 + blockIdx.x % 8;
+  uint32_t id = ((run - before) * kOctets + in) * 8 + blockIdx.x % 8;
   if (id >= p.own_blocks) return false;
   w.head = (int)(id % (uint32_t)a.kv_heads);
   id /= (uint32_t)a.kv_heads;
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPla
 
 template <int D, int NQP, int NQO, int TK, int WPS>
 hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
-  const int64_t blocks = p.prefix_blocks + (p.own_blocks + 7) / 8 * 8;
+  const int64_t blocks = (int64_t)(p.prefix_runs + p.own_runs) * kOctets * 8;
   attn_kernel<D, NQP, NQO, TK, WPS><<<(unsigned)blocks, 256, 0, st>>>(a, p);
   if (p.prefix_parts + p.own_parts > 1) {
     const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;

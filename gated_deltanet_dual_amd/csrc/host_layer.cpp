@@ -23,53 +23,52 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   const int64_t longest = a.dim == 256 ? 2048 : 4096;
 
   // How long the parts are: the shortest time, counted in keys that a workgroup
-  // passes (64 in about 1.3 us).  512 workgroups run at a time (two a CU); a
-  // round of them costs its keys and 384 more for its start and end, and every
-  // part is written and read again by the joining launch, rows * dim * 8 bytes at
-  // 5 TB/s and a little.  Measured against parts twice as long and as short:
-  // 16 requests x 4 over 4096 own keys (16 q, 4 kv heads, d = 128) 24.9 us at the
-  // chosen 512 keys, 29.2 at 256, 28.5 at 1024; 16 x 4 over a prefix of 4096:
-  // 21.6 us at 256, 23.8 at 128 and at 512; 37 x 7 at d = 256 over own 777 keys
-  // 41.6 us at 512, 45.1 at 256, 53.5 at 1024.
+  // passes (64 in about 1.3 us).  512 workgroups run at a time (two a CU); one costs
+  // its keys and 384 more for its start and end; the whole takes no less than all of
+  // them over the 512, nor than the rounds of either kind alone; and every part is
+  // written and read again by the joining launch, rows * dim * 8 bytes at 5 TB/s and a
+  // little.  Measured, with the chosen lengths first:
+  //   256 requests x 4 (16 q, 4 kv heads, d = 128), prefix 8192, own 1024: prefix parts
+  //   of 4096 120 us, 2048 131, 1024 152 (long ones leave a slot of every CU to the
+  //   own keys throughout); 16 x 4 over 4096 own keys: parts of 512 27.0 us, 256 31.1,
+  //   1024 29.8; 16 x 4 over a prefix of 4096: 256 21.5 us, 128 24.6, 512 24.4;
+  //   37 x 7 at d = 256, own 777: parts of 512 41 us, 128 50.
   constexpr int64_t kSlots = 512, kStart = 384;
   const int64_t join = all_rows * a.kv_heads * a.dim / 12500 + 2;
-
-  // A unit (kv head, part) of the prefix stays on one of 8 XCDs.
-  p.prefix_chunk = (int)longest;
-  int64_t best = INT64_MAX;
-  for (int64_t n = ceil_div(a.prefix_len, longest), most = n + 128; a.prefix_len > 0 && n <= most; n += 1 + n / 8) {
-    const int64_t chunk = ceil_div(ceil_div(a.prefix_len, n), 64) * 64, parts = ceil_div(a.prefix_len, chunk);
-    const int64_t rounds = ceil_div(ceil_div(parts * a.kv_heads, 8) * p.prefix_groups, kSlots / 8);
-    const int64_t cost = rounds * (chunk + kStart) + parts * join;
-    if (cost < best) {
-      best = cost;
-      p.prefix_chunk = (int)chunk;
-      p.prefix_parts = (int)parts;
+  const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
+  p.prefix_chunk = p.own_chunk = (int)longest;
+  int64_t best = INT64_MAX, own_top = longest;
+  while (own_top > 128 && own_top / 2 >= a.max_seq_len) own_top /= 2;
+  const int64_t least = ceil_div(a.prefix_len, longest), most = ceil_div(a.prefix_len, 128);
+  for (int64_t n = least; n <= most; n += 1 + n / 4) {
+    // a unit (kv head, part) of the prefix stays on one of 8 XCDs
+    const int64_t chunk = n > 0 ? ceil_div(ceil_div(a.prefix_len, n), 64) * 64 : longest;
+    const int64_t parts = ceil_div(a.prefix_len, chunk), units8 = ceil_div(parts * a.kv_heads, 8) * p.prefix_groups;
+    const int64_t prefix_rounds = ceil_div(units8, kSlots / 8) * (chunk + kStart);
+    for (int64_t c = own_top; c >= 128; c /= 2) {
+      const int64_t own_parts = ceil_div(a.max_seq_len, c);
+      const int64_t own_keys = (c < a.max_seq_len ? c : a.max_seq_len) + kStart;
+      int64_t cost = (8 * units8 * (chunk + kStart) + units * own_parts * own_keys) / kSlots;
+      const int64_t own_rounds = ceil_div(units * own_parts, kSlots) * own_keys;
+      if (parts > 0 && cost < prefix_rounds) cost = prefix_rounds;
+      if (cost < own_rounds) cost = own_rounds;
+      cost += (parts + own_parts) * join;
+      if (cost < best) {
+        best = cost;
+        p.prefix_chunk = (int)chunk;
+        p.prefix_parts = (int)parts;
+        p.own_chunk = (int)c;
+        p.own_parts = (int)own_parts;
+      }
     }
   }
   p.prefix_blocks = ceil_div((int64_t)p.prefix_parts * a.kv_heads, 8) * 8 * p.prefix_groups;
-  // The own keys share the rounds with the prefix.
-  const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
-  best = INT64_MAX;
-  p.own_chunk = (int)longest;
-  for (int64_t c = longest; a.max_seq_len > 0 && c >= 128; c /= 2) {
-    const int64_t parts = ceil_div(a.max_seq_len, c), rounds = ceil_div(p.prefix_blocks + units * parts, kSlots);
-    const int64_t cost = rounds * ((c < a.max_seq_len ? c : a.max_seq_len) + kStart) + parts * join;
-    if (cost < best) {
-      best = cost;
-      p.own_chunk = (int)c;
-      p.own_parts = (int)parts;
-    }
-  }
   // A short prefix is passed by every request before its own keys, in one part: no
   // join and no second launch, where that takes less than its sharing does.
   const int64_t tile = a.dim == 256 ? 32 : 64;
   if (a.prefix_len > 0 && ceil_div(a.prefix_len, tile) + ceil_div(a.max_seq_len, tile) <= 64) {
     const int64_t together = ceil_div(units, kSlots) * (a.prefix_len + a.max_seq_len + kStart);
-    const int64_t longer = p.prefix_chunk < a.prefix_len ? p.prefix_chunk : a.prefix_len;
-    const int64_t own = p.own_chunk < a.max_seq_len ? p.own_chunk : a.max_seq_len;
-    const int64_t apart = ceil_div(p.prefix_blocks + units * p.own_parts, kSlots) * ((longer > own ? longer : own) + kStart) +
-                          (p.prefix_parts + p.own_parts) * join + kStart;
+    const int64_t apart = best + kStart;  // and the second launch
     if (together <= apart) {
       p.merged = 1;
       p.prefix_parts = 0;
@@ -80,6 +79,8 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   }
   if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
   p.own_blocks = units * p.own_parts;
+  p.prefix_runs = (int)ceil_div(p.prefix_blocks, 8 * kOctets);
+  p.own_runs = (int)ceil_div(p.own_blocks, 8 * kOctets);
   return p;
 }
 
