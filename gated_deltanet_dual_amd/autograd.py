@@ -21,6 +21,7 @@ injection into the causal chain).
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import Varlen, gdn_dual_bwd, gdn_dual_fwd, workspace_bytes, _io_of
 from . import layer as _layer
@@ -100,6 +101,7 @@ class GatedNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, gate, rstd = ctx.saved_tensors
         dx, dgate, dweight = _layer.gated_norm_bwd(x, weight, gate, _rows(dy), rstd, activation=ctx.activation)
@@ -121,13 +123,17 @@ class ResidualNormFunction(torch.autograd.Function):
                                           activation=activation, eps=eps, want_rstd=True)
         ctx.activation = activation
         ctx.save_for_backward(x, residual, w_pre, w_post, gate, scale, rstd)
+        ctx.set_materialize_grads(False)
         return h, y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dy):
         x, residual, w_pre, w_post, gate, scale, rstd = ctx.saved_tensors
-        g = _layer.residual_norm_bwd(x, residual, w_pre, dy.contiguous(), dh.contiguous(), rstd, w_post=w_post,
-                                     gate=gate, scale=scale, activation=ctx.activation)
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
+        dh = None if dh is None else dh.contiguous()  # h is not used further: nothing is read for it
+        g = _layer.residual_norm_bwd(x, residual, w_pre, dy, dh, rstd, w_post=w_post, gate=gate, scale=scale,
+                                     activation=ctx.activation)
         return g["dx"], g["dresidual"], g["dw_pre"], g["dw_post"], g["dgate"], g["dscale"], None, None
 
 
@@ -146,6 +152,7 @@ class RotaryFunction(torch.autograd.Function):
         return (q,) if k is None else (q, k)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk=None):
         positions, freqs = ctx.saved_tensors
         # the channels that pass through are not scaled, and neither are their gradients

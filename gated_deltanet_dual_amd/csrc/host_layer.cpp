@@ -172,8 +172,8 @@ flare_status check_rotary(int64_t tokens, const flare_rotary_shape *s, const int
   if (tokens > INT32_MAX) return fail(FLARE_ERR_UNSUPPORTED, "rotary: too many tokens");
   if (s->dim > 1024) return fail(FLARE_ERR_UNSUPPORTED, "rotary: dim %d, at most 1024", s->dim);
   if (s->q_heads > 65536 || s->k_heads > 65536) return fail(FLARE_ERR_UNSUPPORTED, "rotary: at most 65536 heads");
-  if (2 * s->half > s->dim)
-    return fail(FLARE_ERR_SHAPE, "rotary: 2 * half = %d beyond the head's %d channels", 2 * s->half, s->dim);
+  if (s->half > s->dim / 2)  // 2 * half itself can pass 32 bits
+    return fail(FLARE_ERR_SHAPE, "rotary: half = %d, of a head of %d channels", s->half, s->dim);
   if (s->interleaved != 0 && s->interleaved != 1)
     return fail(FLARE_ERR_UNSUPPORTED, "rotary: interleaved %d unknown", s->interleaved);
   flare_status st = check_io(s->io_dtype);
@@ -197,7 +197,8 @@ flare_status check_step_tables(const StepTablesArgs &a) {
       (a.num_req > 0 && (!a.seq_lens || !a.new_lens || !a.seq_lens_out)) || (a.num_req > 0 && a.max_pages > 0 && !a.block_table) ||
       (a.num_free > 0 && !a.free_pages) || (a.max_tokens > 0 && (!a.positions || !a.slots)))
     return fail(FLARE_ERR_NULL, "step_tables: a required pointer is NULL");
-  if (a.pages_used == a.pages_used_out || (a.num_req > 0 && a.seq_lens == a.seq_lens_out))
+  if (a.pages_used == a.pages_used_out ||
+      (a.num_req > 0 && (a.seq_lens == a.seq_lens_out || a.new_lens == a.seq_lens_out)))
     return fail(FLARE_ERR_SHAPE, "step_tables: an output is the memory of its input");
   return FLARE_OK;
 }

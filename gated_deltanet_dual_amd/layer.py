@@ -95,6 +95,14 @@ def _chk(t, name, shape, dtype, dev, optional=False):
         _chk_slow(t, name, shape, dtype, dev, optional)
 
 
+def _i32(value, name):
+    """A size as the library's 32 bits hold it."""
+    value = int(value)
+    if not -0x80000000 <= value <= 0x7FFFFFFF:
+        _fail("%s = %d is beyond 32 bits" % (name, value), 4)
+    return value
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -166,6 +174,8 @@ def _norm_inputs(x, weight, gate):
         (T, d), H = shape, 1
     else:
         _fail("x must be [T, d] or [T, H, d], got shape %s" % (tuple(shape),))
+    if H > 0x7FFFFFFF or d > 0x7FFFFFFF:
+        _fail("x: %d heads of %d channels" % (H, d), 4)
     xs = _token_rows(x, "x", shape, io, dev)
     _chk(weight, "weight", (d,), _module.float32, dev)
     gs = _token_rows(gate, "gate", shape, io, dev) if gate is not None else 0
@@ -217,6 +227,7 @@ def _residual_inputs(x, residual, w_pre, w_post, gate, scale):
     if x.dim() != 2:
         _fail("x must be [T, C], got shape %s" % (tuple(x.shape),))
     T, C = x.shape
+    _i32(C, "C")
     xs = _token_rows(x, "x", (T, C), io, dev)
     res = io if residual is not None and residual.dtype == io else _io_dtype_of(residual, "residual")
     _chk(residual, "residual", (T, C), res, dev)
@@ -327,6 +338,8 @@ def _rotary_inputs(positions, freqs, q, k, interleaved, mscale):
         _fail("q and k must be [T, H, d]")
     T, Hq, d = q.shape
     Hk = 0 if k is None else k.shape[1]
+    if Hq > 0x7FFFFFFF or Hk > 0x7FFFFFFF or d > 0x7FFFFFFF:
+        _fail("rotary: %d and %d heads of %d channels" % (Hq, Hk, d), 4)
     qs = _token_rows(q, "q", q.shape, io, dev)
     ks = 0 if k is None else _token_rows(k, "k", (T, Hk, d), io, dev)
     _chk(positions, "positions", (T,), torch.int32, dev)
@@ -395,7 +408,9 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
     dev = _gpu_device(seq_lens, "seq_lens")
     if seq_lens.dim() != 1 or block_table is None or block_table.dim() != 2:
         _fail("seq_lens must be [R] and block_table [R, max_pages]")
-    R = seq_lens.shape[0]
+    R = _i32(seq_lens.shape[0], "requests")
+    _i32(block_table.shape[1], "max_pages")
+    page, position_offset = _i32(page, "page"), _i32(position_offset, "position_offset")
     _chk(seq_lens, "seq_lens", (R,), i32, dev)
     _chk(new_lens, "new_lens", (R,), i32, dev)
     _chk(block_table, "block_table", (R, block_table.shape[1]), i32, dev)
@@ -419,7 +434,7 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
              "pages_used": _out(out.get("pages_used"), "pages_used out", (1,), i32, dev),
              "status": _out(out.get("status"), "status", (1,), i32, dev)}
     _run(dev, lib().flare_step_tables, R, _ptr(seq_lens), _ptr(new_lens), _ptr(block_table), block_table.shape[1],
-         _ptr(free_pages), free_pages.shape[0], _ptr(pages_used), int(page), int(position_offset), M,
+         _ptr(free_pages), free_pages.shape[0], _ptr(pages_used), page, position_offset, M,
          _ptr(t["cu_new"]), _ptr(t["positions"]), _ptr(t["slots"]), _ptr(t["seq_lens"]), _ptr(t["pages_used"]),
          _ptr(t["status"]))
     return t
@@ -442,7 +457,8 @@ def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=Non
     the block's included.  causal=False: every query sees all of them;
     causal=True: query b sees the prefix and the first seq_lens[r] - (B - 1 - b)
     own keys.  Caches [num_pages, Hk, page, d] bf16.  max_seq_len bounds seq_lens
-    (default: what the table holds); lengths beyond it are cut.  Returns o, or
+    (default: what the table holds), and the work is cut by it: lengths beyond it
+    are cut.  Returns o, or
     (o, lse) with want_lse or `lse` (fp32 [R, B, Hq])."""
     torch = _torch()
     dev = _gpu_device(q, "q")
@@ -451,6 +467,8 @@ def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=Non
     if q.dtype != torch.bfloat16:
         _fail("block_attention is built for bfloat16, got %s" % q.dtype, 4)
     R, B, Hq, d = q.shape
+    if max(R, B, Hq, d) > 0x7FFFFFFF:
+        _fail("q: shape %s" % (tuple(q.shape),), 4)
     _chk(q, "q", (R, B, Hq, d), torch.bfloat16, dev)
     if k_cache is None or k_cache.dim() != 4:
         _fail("k_cache must be [num_pages, Hk, page, d]")
@@ -461,14 +479,14 @@ def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=Non
     wide = block_table.shape[1]
     _chk(block_table, "block_table", (R, wide), torch.int32, dev)
     _chk(seq_lens, "seq_lens", (R,), torch.int32, dev)
-    n = int(prefix_len)
+    n = _i32(prefix_len, "prefix_len")
     if n < 0:
         _fail("prefix_len must not be negative")
     if n > 0:
         if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] * page < n:
             _fail("prefix_table must be int32 with a page for every %d of the prefix's %d keys" % (page, n))
         _chk(prefix_table, "prefix_table", prefix_table.shape, torch.int32, dev)
-    most = wide * page if max_seq_len is None else int(max_seq_len)
+    most = _i32(wide * page if max_seq_len is None else max_seq_len, "max_seq_len")
     shp = AttentionShape(B, Hq, Hk, d, page, BF16, 1 if causal else 0, scale)
     o = _out_like(out, "out", q)
     if lse is not None or want_lse:

@@ -565,9 +565,8 @@ flare_status flare_qkv_prologue_bwd_noalloc(const flare_varlen *varlen,
  * serving keeps a causal cache that denoising forwards only read) needs these
  * next to the entry points above.  io: FLARE_F32 or FLARE_BF16; weights, gates'
  * arithmetic, statistics and sums are fp32.  Token strides count elements; the
- * last dimensions are contiguous.  Rows of any width and alignment are taken;
- * 16-byte aligned rows whose width is a multiple of 16 bytes are moved 16 bytes
- * at a time. */
+ * last dimensions are contiguous.  The norms and rotary positions take rows of
+ * any width and alignment. */
 
 /* What a gate g is turned into before it multiplies. */
 enum { FLARE_GATE_LINEAR = 0, FLARE_GATE_SILU = 1, FLARE_GATE_SIGMOID = 2 };
@@ -693,8 +692,8 @@ flare_status flare_rotary_cache(int64_t tokens, const flare_rotary_shape *shape,
  *   status     int32 [1] device: FLARE_TABLES_OK, or why nothing was allocated:
  *              then cu_new is all zero, every slot is -1, and the table, the
  *              lengths and pages_used are unchanged
- * Rows behind the last new token get position 0 and slot -1.  pages_used,
- * seq_lens and their _out buffers must not be the same memory.
+ * Rows behind the last new token get position 0 and slot -1.  No output may be
+ * an input's memory.
  * num_req <= 8192; any page >= 1. */
 enum {
   FLARE_TABLES_OK = 0,
@@ -714,8 +713,9 @@ flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens,
                                int32_t *status, void *stream);
 
 /* The block step of a softmax layer: the B = block queries of each request over
- * a prefix of prefix_len keys that every request shares, computed once for all
- * of them, and over the request's own seq_lens[r] keys, the block's included.
+ * a prefix of prefix_len keys that every request shares, read once for all of
+ * them where it is long, and over the request's own seq_lens[r] keys, the
+ * block's included.
  *   causal = 0  every query sees all of them (a denoising read: the block is
  *               seen whole by each of its positions)
  *   causal = 1  query b sees the prefix and its request's first

@@ -308,3 +308,23 @@ def test_binding_mistakes_on_the_gpu(g):
     with pytest.raises(g.FlareError, match="memory of its input"):
         g.step_tables(lens, i32(1), i32(0, 0).view(1, 2), i32(5), i32(0), 16, 4, out={"seq_lens": lens})
     torch.cuda.synchronize()
+
+
+def test_gradients_of_one_output_alone(g):
+    """residual_norm's h or y unused: the other's gradients are those with zeros in
+    its place; gradients of the gradients are refused."""
+    import torch
+    from gated_deltanet_dual_amd import autograd as ag
+    T, C = 7, 96
+    x, res, w = (rnd(i, *s, io=io).requires_grad_() for i, s, io in ((1, (T, C), "bf16"), (2, (T, C), "f32"), (3, (C,), "f32")))
+    h, y = ag.residual_norm(x, res, w)
+    dh, dy = rnd(4, T, C, io="f32"), rnd(5, T, C)
+    zh, zy = torch.zeros_like(dh), torch.zeros_like(dy)
+    for outs, grads, full in (((h,), (dh,), (dh, zy)), ((y,), (dy,), (zh, dy))):
+        some = torch.autograd.grad(outs, (x, res, w), grads, retain_graph=True)
+        both = torch.autograd.grad((h, y), (x, res, w), full, retain_graph=True)
+        for a, b in zip(some, both):
+            assert torch.equal(a, b)
+    dx, = torch.autograd.grad(y, x, dy.clone().requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|differentiat"):
+        dx.float().sum().backward()

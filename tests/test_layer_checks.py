@@ -210,3 +210,19 @@ def test_fast_division_rule():
         for n in [0, 1, d - 1, d, 2 ** 31 - 1, *(int(x) for x in rng.integers(0, 2 ** 31, 2000)), *(k * d - 1 for k in range(1, 2000))]:
             if 0 <= n < 2 ** 31:
                 assert (n * m) >> (31 + s) == n // d, (d, n)
+
+
+def test_sizes_whose_products_pass_32_bits(L):
+    assert rotary(L, half=2 ** 30) == 2 and rotary(L, half=2 ** 31 - 1) == 2 and rotary(L, dim=63, half=32) == 2
+    # 2^20 requests x 8 heads x 2^18 parts: more workgroups than a launch holds
+    assert attention(L, R=2 ** 20, block=1, qh=8, kh=8, most=2 ** 30, wide=2 ** 10, page=2 ** 20, n=0, pt=None, nbytes=2 ** 62) == 4
+    assert b"workgroups" in L.flare_last_error()
+    from gated_deltanet_dual_amd.layer import _i32
+    assert _i32(2 ** 31 - 1, "n") == 2 ** 31 - 1
+    for bad in (2 ** 31, 2 ** 32, -2 ** 31 - 1):
+        with pytest.raises(g.FlareError, match="beyond 32 bits"):
+            _i32(bad, "n")
+
+
+def test_step_tables_outputs_are_not_their_inputs(L):
+    assert tables(L, lens_out=FAKE + 64) == 2  # the added lengths, read by every workgroup
