@@ -6,7 +6,8 @@
 // for the pairs (i, half + i) or (2i, 2i + 1) of a head's first 2 half
 // channels; the others pass through.  The reverse mode turns by the negative
 // angle.  position * freq in turns is formed and reduced in 64 bits: in 32 an
-// angle at position 10^6 is off by 0.06 rad.
+// angle at position 10^6 is off by 0.06 rad.  The product is off by some 2^-52 of
+// itself, 2^-32 turns at position 2^20; sine and cosine of what is left are fp32's.
 #include <hip/hip_runtime.h>
 
 #include "fast_div.h"
@@ -31,6 +32,9 @@ struct RotaryPlan {
 
 // One workgroup: `tb` tokens.  Their coefficients first, to LDS, so that a
 // token's angles are formed once for all its heads; then the heads' vectors.
+// Memory bounds it: 32768 tokens, 16 + 4 heads of 128, 32 of them turned, bf16: 336 MB
+// in 71 us, 4.7 TB/s.  The serving form over 1024 tokens takes 5.3 us, mostly a
+// launch's and the coefficients' latency.
 // A head's work items hold two vectors each, so that a thread has two loads in
 // flight.  First those that turn: a vector of each half, or in the interleaved
 // layout two whole vectors; then copies.  The last vectors can be short.
@@ -146,11 +150,14 @@ static void launch(const RotaryArgs &a, hipStream_t st) {
   const bool tail = (a.interleaved ? 2 * a.half : a.half) % VEC != 0 || (a.dim - 2 * a.half) % VEC != 0 ||
                     (a.slots && a.dim % VEC != 0);
   RotaryPlan p;
-  p.tb = 1;
-  while (p.tb < 8 && a.tokens / (2 * p.tb) >= 4096 && 2 * p.tb * a.half <= 2048) p.tb *= 2;
   const int per = turned_items(a, VEC) + copy_items(a.dim - 2 * a.half, VEC);
   const int v_per = a.slots ? copy_items(a.dim, VEC) : 0;
   const int items = (a.q_heads + a.k_heads) * per + a.k_heads * v_per;
+  // more tokens a workgroup while its work items stay below two a thread and 1024
+  // workgroups are left: 65536 tokens of 6 heads of 64, tb 1 to 16: 55, 32, 25, 22, 20
+  // us; 32768 of 20 heads of 128: 71, 62, 63, 65, 74
+  p.tb = 1;
+  while (p.tb < 16 && 2 * p.tb * items <= 512 && a.tokens / (2 * p.tb) >= 1024 && 2 * p.tb * a.half <= 2048) p.tb *= 2;
   p.half = make_fast_div(a.half > 0 ? a.half : 1);
   p.items = make_fast_div(items);
   p.per = make_fast_div(per);
