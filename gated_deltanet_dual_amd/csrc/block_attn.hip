@@ -17,6 +17,21 @@
 // 4q..4q+3 of two 16-key subtiles, and V^T is read in that same key order by
 // the LDS transpose read (16 lanes read four 32-byte row pieces, each lane
 // receives one column of four rows).
+//
+// The weights go into the second product in bf16 (each off by at most half a step,
+// 2^-8 of it, as the output's own rounding is; the matrix instructions take no wider
+// ones beside bf16 values), while their sum l takes them unrounded; scores, m, l, O
+// and the parts are fp32.
+//
+// What bounds it.  A prefix under many rows: the matrix instructions and the vector
+// ones between them (a wave does its exponentials and its products in turn; the other
+// workgroup of its CU fills some of the gaps): 16 query heads of 128, 1024 tokens x
+// 8192 keys 880 TFLOP/s, 32768 keys 1025, of the 1222 that a large library product
+// reaches; d = 64 868, d = 256 781.  A request's own keys: memory, 256 requests x up
+// to 1024 keys, 4 heads of 128, 403 MB in 71 us, 5.7 TB/s.  Both together, side by
+// side on each CU: 118 us where one after the other they take 147.  One request's
+// token over 16384 keys: 8.6 us and 3.9 for the join, a launch and a few latencies
+// of memory each.
 #include <hip/hip_runtime.h>
 
 #include "block_attn.h"
@@ -30,11 +45,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // 16 bytes of memory a lane, at base + offset bytes, straight into LDS: lane i's at
-// lds + 16 i.  Written as
-// an instruction because the compiler, which cannot tell the tile in flight from
-// the tile being read, waits for the one before reading the other; whoever reads
-// waits for the load counter, then meets the others at a barrier.  No register is
-// written but M0, which nothing else in these kernels uses.
+// lds + 16 i.  Written as an instruction because the compiler, which cannot tell the
+// tile in flight from the tile being read, waits for the one before reading the other;
+// whoever reads waits for the load counter, then meets the others at a barrier.  No
+// register is written but M0, which nothing else in these kernels uses.  NT: keys that
+// no other workgroup reads, kept from pushing others out of the caches (256 requests'
+// own 1024 keys, 4 heads of 128, from memory: 76 us where they take 85 otherwise, 32 MB
+// 16 us alike; but keys that four row groups read, 64 requests x 32 tokens at d = 256:
+// 346 us where they take 293).
 template <bool NT>
 __device__ __forceinline__ void load_lds16(const u16 *base, uint32_t offset, uint32_t lds) {
   if constexpr (NT)
@@ -396,8 +414,8 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
   meet();
   // The prefix's tiles (with masks: one loop for all that may need them), then the
   // own keys that every row sees, two tiles a pass so that the buffers are
-  // constants (at d = 256 one: two spill, 69 us where one takes 35), then the last
-  // ones with masks.
+  // constants (at d = 256 one, with the buffer computed: two would spill registers),
+  // then the last ones with masks.
   const int whole = pre_tiles + (all > k0 ? (all - k0) / TK : 0);
   int t = 0;
 #pragma unroll 1
@@ -462,8 +480,8 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
 }
 
 // NQP, NQO: row tiles of a wave for the prefix (rows of all requests) and for a
-// request's own keys.
-template <int D, int NQP, int NQO, int TK, int WPS>
+// request's own keys; NT: those are read by one row group.
+template <int D, int NQP, int NQO, int TK, int WPS, bool NT>
 __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPlan p) {
   __shared__ __align__(16) u16 kt_lds[2][TK * D];
   __shared__ __align__(16) u16 vt_lds[2][TK * D];
@@ -473,12 +491,14 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
     attn_part<D, NQP, TK, false>(a, p, w, 0, kt_lds, vt_lds);
   } else {
     const uint32_t oct = blockIdx.x / 8;
-    attn_part<D, NQO, TK, NQO == 1>(a, p, w, (oct + oct / 32) & 3, kt_lds, vt_lds);
+    attn_part<D, NQO, TK, NT>(a, p, w, (oct + oct / 32) & 3, kt_lds, vt_lds);
   }
 }
 
 // Joins the parts of a row: D / 4 lanes hold 16 bytes of it each.  With `split`
-// above 1 that many lane groups share a row's parts and add up through LDS.
+// above 1 that many lane groups share a row's parts and add up through LDS.  Bound by
+// memory where there are many rows (16384 of 128 from 3 parts: 29 MB in 7.6 us), by
+// a launch and two latencies where there are few (16 rows from 128 parts: 3.9 us).
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPlan p, int split) {
   constexpr int L = D / 4;   // lanes a row
@@ -526,10 +546,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPla
   if (a.lse && c == 0) a.lse[row] = any ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <int D, int NQP, int NQO, int TK, int WPS>
+template <int D, int NQP, int NQO, int TK, int WPS, bool NT>
 hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   const int64_t blocks = (int64_t)(p.prefix_runs + p.own_runs) * kOctets * 8;
-  attn_kernel<D, NQP, NQO, TK, WPS><<<(unsigned)blocks, 256, 0, st>>>(a, p);
+  attn_kernel<D, NQP, NQO, TK, WPS, NT><<<(unsigned)blocks, 256, 0, st>>>(a, p);
   if (p.prefix_parts + p.own_parts > 1) {
     const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;
     // few rows: every lane group of a workgroup on one
@@ -546,14 +566,14 @@ hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
 hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   TimedLaunch tl(K_BLOCK_ATTN, st);
   if (a.dim == 64) {
-    if (p.own_tiles == 2) return launch_d<64, 2, 2, 64, 3>(a, p, st);
-    return p.prefix_tiles == 2 ? launch_d<64, 2, 1, 64, 3>(a, p, st) : launch_d<64, 1, 1, 64, 3>(a, p, st);
+    if (p.own_tiles == 2) return launch_d<64, 2, 2, 64, 3, false>(a, p, st);
+    return p.prefix_tiles == 2 ? launch_d<64, 2, 1, 64, 3, true>(a, p, st) : launch_d<64, 1, 1, 64, 3, true>(a, p, st);
   }
   if (a.dim == 128) {
-    if (p.own_tiles == 2) return launch_d<128, 2, 2, 64, 2>(a, p, st);
-    return p.prefix_tiles == 2 ? launch_d<128, 2, 1, 64, 2>(a, p, st) : launch_d<128, 1, 1, 64, 2>(a, p, st);
+    if (p.own_tiles == 2) return launch_d<128, 2, 2, 64, 2, false>(a, p, st);
+    return p.prefix_tiles == 2 ? launch_d<128, 2, 1, 64, 2, true>(a, p, st) : launch_d<128, 1, 1, 64, 2, true>(a, p, st);
   }
-  return launch_d<256, 1, 1, 32, 2>(a, p, st);
+  return p.own_groups == 1 ? launch_d<256, 1, 1, 32, 2, true>(a, p, st) : launch_d<256, 1, 1, 32, 2, false>(a, p, st);
 }
 
 }  // namespace flare
