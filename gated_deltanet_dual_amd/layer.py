@@ -212,7 +212,7 @@ def gated_norm_bwd(x, weight, gate, dy, rstd, activation=SILU, workspace=None, o
     dx, dgate, dweight = out if out is not None else (None, None, None)
     dx = _out_like(dx, "dx", x)
     dgate = _out_like(dgate, "dgate", gate) if gate is not None else None
-    dweight = _out(dweight, "dweight", (d,), torch.float32, dev)
+    dweight = _out_like(dweight, "dweight", weight)
     need = gated_norm_bwd_workspace_bytes(T, H, d)
     workspace = _workspace(workspace, need, dev)
     _run(dev, lib().flare_gated_norm_bwd, T, H, d, _io(io), _ptr(x), xs, _ptr(gate), gs, _ptr(weight),
@@ -275,13 +275,12 @@ def residual_norm_bwd(x, residual, w_pre, dy, dh, rstd, w_post=None, gate=None, 
     _chk(dh, "dh", (T, C), res, dev, optional=True)
     _chk(rstd, "rstd", (T, 2), torch.float32, dev)
     out = out or {}
-    f32 = torch.float32
-    g = {"dx": _out(out.get("dx"), "dx", (T, C), io, dev),
-         "dresidual": _out(out.get("dresidual"), "dresidual", (T, C), res, dev),
-         "dgate": _out(out.get("dgate"), "dgate", (T, C), io, dev) if gate is not None else None,
-         "dw_pre": _out(out.get("dw_pre"), "dw_pre", (C,), f32, dev),
-         "dw_post": _out(out.get("dw_post"), "dw_post", (C,), f32, dev) if w_post is not None else None,
-         "dscale": _out(out.get("dscale"), "dscale", (C,), f32, dev) if scale is not None else None}
+    g = {"dx": _out_like(out.get("dx"), "dx", x),
+         "dresidual": _out_like(out.get("dresidual"), "dresidual", residual),
+         "dgate": _out_like(out.get("dgate"), "dgate", gate) if gate is not None else None,
+         "dw_pre": _out_like(out.get("dw_pre"), "dw_pre", w_pre),
+         "dw_post": _out_like(out.get("dw_post"), "dw_post", w_post) if w_post is not None else None,
+         "dscale": _out_like(out.get("dscale"), "dscale", scale) if scale is not None else None}
     workspace = _workspace(workspace, residual_norm_bwd_workspace_bytes(T, C), dev)
     _run(dev, lib().flare_residual_norm_bwd, T, C, _io(io), _io(res), _ptr(x), xs, _ptr(residual), _ptr(gate), gs,
          _ptr(w_pre), _ptr(w_post), _ptr(scale), int(activation), _ptr(rstd), _ptr(dy), _ptr(dh), _ptr(g["dx"]),
