@@ -407,12 +407,13 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
     dev = _gpu_device(seq_lens, "seq_lens")
     if seq_lens.dim() != 1 or block_table is None or block_table.dim() != 2:
         _fail("seq_lens must be [R] and block_table [R, max_pages]")
-    R = _i32(seq_lens.shape[0], "requests")
-    _i32(block_table.shape[1], "max_pages")
-    page, position_offset = _i32(page, "page"), _i32(position_offset, "position_offset")
+    R, wide = seq_lens.shape[0], block_table.shape[1]
+    page, position_offset = int(page), int(position_offset)
+    if max(R, wide, page, position_offset) > 0x7FFFFFFF or min(page, position_offset) < 0:
+        _i32(R, "requests"), _i32(wide, "max_pages"), _i32(page, "page"), _i32(position_offset, "position_offset")
     _chk(seq_lens, "seq_lens", (R,), i32, dev)
     _chk(new_lens, "new_lens", (R,), i32, dev)
-    _chk(block_table, "block_table", (R, block_table.shape[1]), i32, dev)
+    _chk(block_table, "block_table", (R, wide), i32, dev)
     if free_pages is None or free_pages.dim() != 1:
         _fail("free_pages must be int32 [F]")
     _chk(free_pages, "free_pages", free_pages.shape, i32, dev)
@@ -421,10 +422,9 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
     if M < 0:
         _fail("max_tokens must not be negative")
     if out is None:  # the small ones share a buffer
-        cu, lens, used, status = torch.empty((2 * R + 3,), dtype=i32, device=dev).split((R + 1, R, 1, 1))
-        t = {"cu_new": cu, "positions": torch.empty((M,), dtype=i32, device=dev),
-             "slots": torch.empty((M,), dtype=torch.int64, device=dev), "seq_lens": lens, "pages_used": used,
-             "status": status}
+        cu, lens, used, status = torch.split_with_sizes(seq_lens.new_empty(2 * R + 3), (R + 1, R, 1, 1))
+        t = {"cu_new": cu, "positions": seq_lens.new_empty(M), "slots": seq_lens.new_empty(M, dtype=torch.int64),
+             "seq_lens": lens, "pages_used": used, "status": status}
     else:
         t = {"cu_new": _out(out.get("cu_new"), "cu_new", (R + 1,), i32, dev),
              "positions": _out(out.get("positions"), "positions", (M,), i32, dev),
@@ -432,7 +432,7 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
              "seq_lens": _out(out.get("seq_lens"), "seq_lens out", (R,), i32, dev),
              "pages_used": _out(out.get("pages_used"), "pages_used out", (1,), i32, dev),
              "status": _out(out.get("status"), "status", (1,), i32, dev)}
-    _run(dev, lib().flare_step_tables, R, _ptr(seq_lens), _ptr(new_lens), _ptr(block_table), block_table.shape[1],
+    _run(dev, lib().flare_step_tables, R, _ptr(seq_lens), _ptr(new_lens), _ptr(block_table), wide,
          _ptr(free_pages), free_pages.shape[0], _ptr(pages_used), page, position_offset, M,
          _ptr(t["cu_new"]), _ptr(t["positions"]), _ptr(t["slots"]), _ptr(t["seq_lens"]), _ptr(t["pages_used"]),
          _ptr(t["status"]))
