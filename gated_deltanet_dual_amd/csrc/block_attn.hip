@@ -487,12 +487,10 @@ __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPla
   __shared__ __align__(16) u16 vt_lds[2][TK * D];
   Part w;
   if (!find_part<64 * NQP, 64 * NQO>(a, p, w)) return;
-  if (w.req < 0) {
-    attn_part<D, NQP, TK, false>(a, p, w, 0, kt_lds, vt_lds);
-  } else {
-    const uint32_t oct = blockIdx.x / 8;
-    attn_part<D, NQO, TK, NT>(a, p, w, (oct + oct / 32) & 3, kt_lds, vt_lds);
-  }
+  const uint32_t oct = blockIdx.x / 8;
+  const int turn = w.req < 0 ? 0 : (oct + oct / 32) & 3;
+  if (w.req < 0 || (NQP == NQO && !NT)) attn_part<D, NQP, TK, false>(a, p, w, turn, kt_lds, vt_lds);
+  else attn_part<D, NQO, TK, NT>(a, p, w, turn, kt_lds, vt_lds);
 }
 
 // Joins the parts of a row: D / 4 lanes hold 16 bytes of it each.  With `split`
