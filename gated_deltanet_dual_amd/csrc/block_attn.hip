@@ -480,7 +480,7 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
 }
 
 // NQP, NQO: row tiles of a wave for the prefix (rows of all requests) and for a
-// request's own keys; NT: those are read by one row group.
+// request's own keys; NT: those are read by one row group (measured at load_lds16).
 template <int D, int NQP, int NQO, int TK, int WPS, bool NT>
 __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPlan p) {
   __shared__ __align__(16) u16 kt_lds[2][TK * D];
@@ -563,15 +563,18 @@ hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
 
 hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   TimedLaunch tl(K_BLOCK_ATTN, st);
+  const bool alone = p.own_groups == 1;
   if (a.dim == 64) {
     if (p.own_tiles == 2) return launch_d<64, 2, 2, 64, 3, false>(a, p, st);
-    return p.prefix_tiles == 2 ? launch_d<64, 2, 1, 64, 3, true>(a, p, st) : launch_d<64, 1, 1, 64, 3, true>(a, p, st);
+    if (p.prefix_tiles == 2) return alone ? launch_d<64, 2, 1, 64, 3, true>(a, p, st) : launch_d<64, 2, 1, 64, 3, false>(a, p, st);
+    return alone ? launch_d<64, 1, 1, 64, 3, true>(a, p, st) : launch_d<64, 1, 1, 64, 3, false>(a, p, st);
   }
   if (a.dim == 128) {
     if (p.own_tiles == 2) return launch_d<128, 2, 2, 64, 2, false>(a, p, st);
-    return p.prefix_tiles == 2 ? launch_d<128, 2, 1, 64, 2, true>(a, p, st) : launch_d<128, 1, 1, 64, 2, true>(a, p, st);
+    if (p.prefix_tiles == 2) return alone ? launch_d<128, 2, 1, 64, 2, true>(a, p, st) : launch_d<128, 2, 1, 64, 2, false>(a, p, st);
+    return alone ? launch_d<128, 1, 1, 64, 2, true>(a, p, st) : launch_d<128, 1, 1, 64, 2, false>(a, p, st);
   }
-  return p.own_groups == 1 ? launch_d<256, 1, 1, 32, 2, true>(a, p, st) : launch_d<256, 1, 1, 32, 2, false>(a, p, st);
+  return alone ? launch_d<256, 1, 1, 32, 2, true>(a, p, st) : launch_d<256, 1, 1, 32, 2, false>(a, p, st);
 }
 
 }  // namespace flare

@@ -15,7 +15,10 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
   const int64_t all_rows = rows * a.num_req;
-  p.own_tiles = a.dim <= 128 && rows > 64 ? 2 : 1;
+  // Two row tiles a wave where that leaves a workgroup for every CU: half the reads of
+  // K and V.  30 requests x 32, 32 query and 4 kv heads of 128, 1000 own keys (240
+  // workgroups of two): 26 us with one, 39 with two; 60 requests (480): 50 and 44.
+  p.own_tiles = a.dim <= 128 && rows > 64 && ceil_div(rows, 128) * a.kv_heads * a.num_req >= 256 ? 2 : 1;
   p.prefix_tiles = a.dim <= 128 && (all_rows > 64 || p.own_tiles == 2) ? 2 : 1;
   p.own_groups = (int)ceil_div(rows, 64 * p.own_tiles);
   p.prefix_groups = (int)ceil_div(all_rows, 64 * p.prefix_tiles);

@@ -107,6 +107,15 @@ def test_attention(g, i, causal):
     check(g, make(i, R, B, Hk, G, d, page, lens, prefix), prefix, causal)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,Hk,prefix", [(64, 2, 0), (64, 2, 200), (128, 2, 77), (128, 2, 4130), (128, 1, 0)])
+def test_many_requests_with_many_rows(g, d, Hk, prefix, causal):
+    """Enough rows in all that a wave takes two tiles of them (Hk = 2: 260 workgroups of
+    80 rows; Hk = 1: one below), own keys from none to several tiles."""
+    R, B, G = 130, 20, 4
+    check(g, make(11, R, B, Hk, G, d, 16, [(i * 29) % 150 for i in range(R)], prefix), prefix, causal)
+
+
 def test_sharp_scores_and_scale(g):
     """Scores far apart (the running maximum moves, weights vanish) and a scale of
     the caller's own."""
