@@ -29,7 +29,7 @@
 // 8192 keys 880 TFLOP/s, 32768 keys 1025, of the 1222 that a large library product
 // reaches; d = 64 868, d = 256 781.  A request's own keys: memory, 256 requests x up
 // to 1024 keys, 4 heads of 128, 403 MB in 71 us, 5.7 TB/s.  Both together, side by
-// side on each CU: 118 us where one after the other they take 147.  One request's
+// side on each CU: 116 us where one after the other they take 147.  One request's
 // token over 16384 keys: 8.6 us and 3.9 for the join, a launch and a few latencies
 // of memory each.
 #include <hip/hip_runtime.h>
