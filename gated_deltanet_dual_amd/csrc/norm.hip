@@ -18,7 +18,16 @@
 namespace flare {
 namespace {
 
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+// exp(-g) = 2^hi 2^lo with hi the rounded product -g log2 e and lo what its rounding and
+// the constant's left over: off by 4 half steps for every g, where 2^hi alone is off by |g|
+// of them.  A product beyond every exponent (or NaN) has no rest to add.  (32768 x 16 rows
+// of 128, both directions: 210 us with the rest and without, 214 with the library's expf.)
+__device__ __forceinline__ float exp_minus(float g) {
+  constexpr float kLog2e = 1.44269504088896340736, kLog2eRest = 1.44269504088896340736 - (double)kLog2e;
+  const float hi = -g * kLog2e, rest = __builtin_fmaf(-g, kLog2eRest, __builtin_fmaf(-g, kLog2e, -hi));
+  return __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(fabsf(hi) < 256.0f ? rest : 0.0f, 0.69314718055994530942f, 1.0f);
+}
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + exp_minus(g)); }
 
 // f = act(g) of a vector's elements (1 without a gate, act < 0).  The choice is
 // made once for the vector: inside the element loop it would cut the code at
