@@ -243,8 +243,9 @@ flare_status flare_block_attention(int32_t num_req, const flare_attention_shape 
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != FLARE_OK) return st;
   }
-  if (p.prefix_blocks + p.own_blocks > INT32_MAX - 2 * 8 * kOctets)  // both are filled up to runs
-    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: too many workgroups");
+  if (attn_launch_blocks(p) > kMaxBlocks)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: %lld workgroups, at most %lld", (long long)attn_launch_blocks(p),
+                (long long)kMaxBlocks);
   a.num_pages = num_pages;
   a.max_pages = max_pages;
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;

@@ -34,6 +34,9 @@ FLARE_HD int attn_own_len(const BlockAttnArgs &a, int32_t len) {
 
 // a.max_seq_len <= max_pages * page
 AttnPlan attn_plan(const BlockAttnArgs &a);
+// The workgroups that a plan launches: those of the prefix and of the own keys, each
+// filled up to whole runs.
+int64_t attn_launch_blocks(const AttnPlan &p);
 size_t block_attention_workspace_bytes(const BlockAttnArgs &a, const AttnPlan &p);
 
 }  // namespace flare

@@ -546,8 +546,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPla
 
 template <int D, int NQP, int NQO, int TK, int WPS, bool NT>
 hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
-  const int64_t blocks = (int64_t)(p.prefix_runs + p.own_runs) * kOctets * 8;
-  attn_kernel<D, NQP, NQO, TK, WPS, NT><<<(unsigned)blocks, 256, 0, st>>>(a, p);
+  attn_kernel<D, NQP, NQO, TK, WPS, NT><<<(unsigned)attn_launch_blocks(p), 256, 0, st>>>(a, p);
   if (p.prefix_parts + p.own_parts > 1) {
     const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;
     // few rows: every lane group of a workgroup on one

@@ -87,6 +87,10 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   return p;
 }
 
+int64_t attn_launch_blocks(const AttnPlan &p) {
+  const int64_t run = 8 * kOctets;
+  return (ceil_div(p.prefix_blocks, run) + ceil_div(p.own_blocks, run)) * run;
+}
 
 int norm_bwd_blocks(int64_t rows, int32_t dim) {
   // what the chip holds at a time: six workgroups of 256 threads a CU where a wave or

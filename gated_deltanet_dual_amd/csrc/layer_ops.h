@@ -81,6 +81,9 @@ struct BlockAttnArgs {
 };
 
 // ---------------------------------------------------------------- host checks
+// A launch dimension holds fewer than 2^32 work items: so many workgroups of 256.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 32) / 256 - 1;
+
 // Workgroups of a norm's reverse mode over this many rows at most: each sums the
 // weight gradients of its rows and writes one partial row, which a second launch
 // adds in a fixed order.  And the bytes of its workspace with `weights` weights.

@@ -739,7 +739,9 @@ flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens,
  * Rows of a page that no length reaches may hold anything, NaN included.
  * Requirements: io_dtype FLARE_BF16; head_dim in {64, 128, 256}; page a power of
  * two of at least 16; q_heads a multiple of kv_heads; 16-byte aligned q,
- * caches and o.  scale <= 0 selects 1 / sqrt(head_dim). */
+ * caches and o; num_req * block * q_heads below 2^25, and fewer than 2^24 units
+ * of work (64 or 128 rows of a kv head by a part of at most 4096 keys): larger
+ * calls are FLARE_ERR_UNSUPPORTED.  scale <= 0 selects 1 / sqrt(head_dim). */
 typedef struct {
   int32_t block, q_heads, kv_heads, head_dim, page;
   int32_t io_dtype;

@@ -1,0 +1,89 @@
+"""What the operators around the GDN step launch, without a GPU: a child process
+loads a stub of HIP's launch functions before the library (device pointers are
+dummies, nothing runs).  A launch dimension holds fewer than 2^32 work items:
+calls that need more are refused by the host's checks, before anything is enqueued."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+import gated_deltanet_dual_amd as g
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CHILD = """
+import ctypes, json, sys
+stub = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+stub.stub_items.restype = ctypes.c_uint64
+sys.path.insert(0, sys.argv[2])
+import gated_deltanet_dual_amd as g
+from gated_deltanet_dual_amd import layer
+L = ctypes.CDLL(g.LIB_PATH)
+layer.declare(L)
+FAKE = 0x7F0000001000
+WS = FAKE & ~255
+
+def attention(R, block=1, qh=8, kh=8, d=64, page=1024, most=2 ** 20, n=0):
+    s = g.AttentionShape(block, qh, kh, d, page, g.BF16, 0, 0.0)
+    return L.flare_block_attention(R, ctypes.byref(s), FAKE, FAKE, FAKE, 100, FAKE, -(-most // page), FAKE, most, FAKE, n,
+                                   FAKE, None, WS, 2 ** 62, None)
+
+def rotary(tokens, qh=16, kh=4, d=128, half=64, io=g.BF16):
+    s = g.RotaryShape(qh, kh, d, half, io, 0, 1.0)
+    return L.flare_rotary(tokens, ctypes.byref(s), FAKE, FAKE, FAKE, qh * d, FAKE, kh * d, 0, FAKE, FAKE, None)
+
+def gated_bwd(tokens, heads=4, d=128):
+    return L.flare_gated_norm_bwd(tokens, heads, d, g.BF16, FAKE, heads * d, FAKE, heads * d, FAKE, 1, FAKE, FAKE, heads * d,
+                                  FAKE, FAKE, FAKE, WS, 2 ** 40, None)
+
+def residual_bwd(tokens, d=2048):
+    return L.flare_residual_norm_bwd(tokens, d, g.BF16, g.F32, FAKE, d, FAKE, FAKE, d, FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE,
+                                     FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, WS, 2 ** 40, None)
+
+out = []
+for call in json.loads(sys.argv[3]):
+    stub.stub_reset()
+    stub.stub_fail_at(call.get("fail_at", -1))
+    status = globals()[call["op"]](**call["args"])
+    out.append([status, [stub.stub_items(i) for i in range(stub.stub_launches())]])
+print(json.dumps(out))
+"""
+
+
+@pytest.fixture(scope="module")
+def calls(tmp_path_factory):
+    if not os.path.exists(g.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
+    lib = str(tmp_path_factory.mktemp("stub") / "launches.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-o", lib, os.path.join(ROOT, "tests", "hip_stub", "launches.c")],
+                   check=True)
+
+    def run(*todo):
+        r = subprocess.run([sys.executable, "-c", CHILD, lib, ROOT, json.dumps(todo)], capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-2000:]
+        return json.loads(r.stdout)
+    return run
+
+
+def call(op, fail_at=-1, **args):
+    return {"op": op, "fail_at": fail_at, "args": args}
+
+
+def test_the_stub_sees_the_launches(calls):
+    for status, items in calls(call("attention", R=2), call("gated_bwd", tokens=4000), call("residual_bwd", tokens=4000)):
+        assert status == 0 and len(items) == 2 and all(0 < n < 2 ** 32 for n in items)
+    (status, items), = calls(call("rotary", tokens=1000))
+    assert status == 0 and len(items) == 1
+
+
+def test_attention_of_more_workgroups_than_a_launch_holds(calls):
+    # 8192 requests x 8 heads x 256 parts of 4096 keys are 2^24 workgroups of 256 threads
+    most, fewer = calls(call("attention", R=8192), call("attention", R=8160))
+    assert most == [4, []]
+    assert fewer[0] == 0 and len(fewer[1]) == 2 and 2 ** 31 < fewer[1][0] < 2 ** 32
+    # the prefix's workgroups count likewise, and both together
+    for R, more in ((2 ** 22, dict(n=2 ** 21, most=1024)), (4096, dict(n=2 ** 21, block=64, qh=64, kh=8, most=2 ** 20))):
+        status, items = calls(call("attention", R=R, **more))[0]
+        assert (status == 4 and items == []) or (status == 0 and all(n < 2 ** 32 for n in items))
