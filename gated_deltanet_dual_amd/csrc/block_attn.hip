@@ -547,6 +547,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(BlockAttnArgs a, AttnPla
 template <int D, int NQP, int NQO, int TK, int WPS, bool NT>
 hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   attn_kernel<D, NQP, NQO, TK, WPS, NT><<<(unsigned)attn_launch_blocks(p), 256, 0, st>>>(a, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (p.prefix_parts + p.own_parts > 1) {
     const int64_t rows = (int64_t)a.num_req * a.block * a.q_heads;
     // few rows: every lane group of a workgroup on one

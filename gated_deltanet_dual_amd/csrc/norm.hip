@@ -541,7 +541,7 @@ template <typename IO, int VEC> void gated_forward(const GatedNormArgs &a, hipSt
   });
 }
 
-template <typename IO, int VEC> void gated_reverse(GatedNormArgs a, hipStream_t st) {
+template <typename IO, int VEC> hipError_t gated_reverse(GatedNormArgs a, hipStream_t st) {
   const int64_t rows = a.tokens * a.heads;
   const TeamPlan p = plan_reverse((a.dim + VEC - 1) / VEC, VEC);
   const int grid = reverse_blocks(rows, p, norm_bwd_blocks(rows, a.dim));
@@ -554,8 +554,11 @@ template <typename IO, int VEC> void gated_reverse(GatedNormArgs a, hipStream_t 
     NORM_REVERSE(LAUNCH);
 #undef LAUNCH
   });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (grid != 1)
     norm_partials_kernel<<<dim3((a.dim + 15) / 16, 1), 1024, 0, st>>>(part, grid, a.dim, a.dweight, nullptr, nullptr);
+  return hipGetLastError();
 }
 
 template <typename IO, typename RES, int VEC> void residual_forward(const ResidualNormArgs &a, hipStream_t st) {
@@ -570,7 +573,7 @@ template <typename IO, typename RES, int VEC> void residual_forward(const Residu
   });
 }
 
-template <typename IO, typename RES, int VEC> void residual_reverse(ResidualNormArgs a, hipStream_t st) {
+template <typename IO, typename RES, int VEC> hipError_t residual_reverse(ResidualNormArgs a, hipStream_t st) {
   const TeamPlan p = plan_reverse((a.dim + VEC - 1) / VEC, VEC);
   const int grid = reverse_blocks(a.tokens, p, norm_bwd_blocks(a.tokens, a.dim));
   float *const part = a.part[0];
@@ -588,9 +591,12 @@ template <typename IO, typename RES, int VEC> void residual_reverse(ResidualNorm
     NORM_REVERSE(LAUNCH);
 #undef LAUNCH
   });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (grid != 1)
     norm_partials_kernel<<<dim3((a.dim + 15) / 16, 3), 1024, 0, st>>>(
         part, grid, a.dim, a.dw_pre, a.w_post ? a.dw_post : nullptr, a.scale ? a.dscale : nullptr);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -604,9 +610,7 @@ hipError_t launch_gated_norm(const GatedNormArgs &a, hipStream_t st) {
 
 hipError_t launch_gated_norm_bwd(const GatedNormArgs &a, hipStream_t st) {
   TimedLaunch tl(K_NORM_BWD, st);
-  if (a.bf16) gated_reverse<u16, 8>(a, st);
-  else gated_reverse<float, 4>(a, st);
-  return hipGetLastError();
+  return a.bf16 ? gated_reverse<u16, 8>(a, st) : gated_reverse<float, 4>(a, st);
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t st) {
@@ -619,10 +623,8 @@ hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t st) {
 
 hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t st) {
   TimedLaunch tl(K_NORM_BWD, st);
-  if (a.bf16 && a.res_bf16) residual_reverse<u16, u16, 8>(a, st);
-  else if (a.bf16) residual_reverse<u16, float, 8>(a, st);
-  else residual_reverse<float, float, 4>(a, st);
-  return hipGetLastError();
+  if (a.bf16 && a.res_bf16) return residual_reverse<u16, u16, 8>(a, st);
+  return a.bf16 ? residual_reverse<u16, float, 8>(a, st) : residual_reverse<float, float, 4>(a, st);
 }
 
 }  // namespace flare

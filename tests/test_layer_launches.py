@@ -87,3 +87,11 @@ def test_attention_of_more_workgroups_than_a_launch_holds(calls):
     for R, more in ((2 ** 22, dict(n=2 ** 21, most=1024)), (4096, dict(n=2 ** 21, block=64, qh=64, kh=8, most=2 ** 20))):
         status, items = calls(call("attention", R=R, **more))[0]
         assert (status == 4 and items == []) or (status == 0 and all(n < 2 ** 32 for n in items))
+
+
+def test_nothing_is_enqueued_after_a_launch_that_failed(calls):
+    """The join and the weights' sums read what the first launch writes."""
+    todo = [call("attention", fail_at=0, R=2), call("gated_bwd", fail_at=0, tokens=4000),
+            call("residual_bwd", fail_at=0, tokens=4000)]
+    for status, items in calls(*todo):
+        assert status == 6 and len(items) == 1
