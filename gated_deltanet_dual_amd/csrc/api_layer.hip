@@ -161,6 +161,8 @@ flare_status flare_rotary(int64_t tokens, const flare_rotary_shape *shape, const
   RotaryArgs a = rotary_args(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out);
   if (inverse) a.sign = -1.0f;
   a.k_out = k_out;
+  st = check_rotary_blocks(a);
+  if (st != FLARE_OK) return st;
   return hip_status(launch_rotary(a, (hipStream_t)stream), "rotary launch");
 }
 
@@ -184,6 +186,8 @@ flare_status flare_rotary_cache(int64_t tokens, const flare_rotary_shape *shape,
   a.v_cache = v_cache;
   a.num_pages = num_pages;
   a.page = page;
+  st = check_rotary_blocks(a);
+  if (st != FLARE_OK) return st;
   return hip_status(launch_rotary(a, (hipStream_t)stream), "rotary_cache launch");
 }
 

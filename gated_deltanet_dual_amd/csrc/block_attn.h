@@ -4,12 +4,6 @@
 
 #include "layer_ops.h"
 
-#ifdef __HIPCC__
-#define FLARE_HD __host__ __device__ inline
-#else
-#define FLARE_HD inline
-#endif
-
 namespace flare {
 
 // Workgroups come in octets, one for each XCD, and runs of 32 octets, one for each of

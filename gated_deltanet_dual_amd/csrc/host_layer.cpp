@@ -192,6 +192,24 @@ flare_status check_rotary(int64_t tokens, const flare_rotary_shape *s, const int
   return FLARE_OK;
 }
 
+int rotary_block_tokens(const RotaryArgs &a) {
+  // more tokens a workgroup while its work items stay below two a thread and 1024
+  // workgroups are left: 65536 tokens of 6 heads of 64, 1 to 16 of them: 55, 32, 25, 22,
+  // 20 us; 32768 of 20 heads of 128: 71, 62, 63, 65, 74
+  const int items = rotary_items(a, rotary_vec(a.bf16)).token;
+  int tb = 1;
+  while (tb < 16 && 2 * tb * items <= 512 && a.tokens / (2 * tb) >= 1024 && 2 * tb * a.half <= 2048) tb *= 2;
+  return tb;
+}
+
+flare_status check_rotary_blocks(const RotaryArgs &a) {
+  const int64_t tb = rotary_block_tokens(a);
+  if (ceil_div(a.tokens, tb) > kMaxBlocks)
+    return fail(FLARE_ERR_UNSUPPORTED, "rotary: %lld tokens, at most %lld of so many heads", (long long)a.tokens,
+                (long long)(kMaxBlocks * tb));
+  return FLARE_OK;
+}
+
 flare_status check_step_tables(const StepTablesArgs &a) {
   if (a.num_req < 0 || a.max_pages < 0 || a.num_free < 0 || a.max_tokens < 0 || a.position_offset < 0)
     return fail(FLARE_ERR_SHAPE, "step_tables: a negative size");

@@ -8,6 +8,12 @@
 
 #include "../../include/flare_gdn.h"
 
+#ifdef __HIPCC__
+#define FLARE_HD __host__ __device__ inline
+#else
+#define FLARE_HD inline
+#endif
+
 namespace flare {
 
 // ---------------------------------------------------------------- norms
@@ -54,6 +60,26 @@ struct RotaryArgs {
   int64_t num_pages;
   int page;
 };
+
+// A head's work items hold two vectors each, so that a thread has two loads in
+// flight.  First those that turn: a vector of each half, or in the interleaved
+// layout two whole vectors; then copies.  The last vectors can be short.
+FLARE_HD int rotary_vectors(int channels, int vec) { return (channels + vec - 1) / vec; }
+FLARE_HD int rotary_turned_items(const RotaryArgs &a, int vec) {
+  return a.interleaved ? (rotary_vectors(2 * a.half, vec) + 1) / 2 : rotary_vectors(a.half, vec);
+}
+FLARE_HD int rotary_copy_items(int channels, int vec) { return (rotary_vectors(channels, vec) + 1) / 2; }
+
+struct RotaryItems {
+  int per, v_per, token;  // work items of a q or k head, of a v head (0: none) and of a token
+};
+FLARE_HD RotaryItems rotary_items(const RotaryArgs &a, int vec) {
+  const int per = rotary_turned_items(a, vec) + rotary_copy_items(a.dim - 2 * a.half, vec);
+  const int v_per = a.slots ? rotary_copy_items(a.dim, vec) : 0;
+  return {per, v_per, (a.q_heads + a.k_heads) * per + a.k_heads * v_per};
+}
+constexpr int rotary_vec(bool bf16) { return bf16 ? 8 : 4; }  // 16 bytes
+int rotary_block_tokens(const RotaryArgs &a);                 // tokens a workgroup
 
 // ---------------------------------------------------------------- step tables
 constexpr int kTablesMaxReq = 8192;  // three int32 per request in LDS
@@ -102,6 +128,8 @@ flare_status check_residual_norm(int64_t tokens, int32_t dim, int32_t io_dtype, 
 flare_status check_workspace(const void *workspace, size_t bytes, size_t need);
 flare_status check_rotary(int64_t tokens, const flare_rotary_shape *s, const int32_t *positions, const double *freqs,
                           const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_out);
+// the launch's limit, once the arguments are laid out
+flare_status check_rotary_blocks(const RotaryArgs &a);
 flare_status check_step_tables(const StepTablesArgs &a);
 // shape alone (for the size query), then everything
 flare_status check_attention_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,

@@ -35,15 +35,6 @@ struct RotaryPlan {
 // Memory bounds it: 32768 tokens, 16 + 4 heads of 128, 32 of them turned, bf16: 336 MB
 // in 71 us, 4.7 TB/s.  The serving form over 1024 tokens takes 5.3 us, mostly a
 // launch's and the coefficients' latency.
-// A head's work items hold two vectors each, so that a thread has two loads in
-// flight.  First those that turn: a vector of each half, or in the interleaved
-// layout two whole vectors; then copies.  The last vectors can be short.
-__host__ __device__ inline int vectors(int channels, int vec) { return (channels + vec - 1) / vec; }
-__host__ __device__ inline int turned_items(const RotaryArgs &a, int vec) {
-  return a.interleaved ? (vectors(2 * a.half, vec) + 1) / 2 : vectors(a.half, vec);
-}
-__host__ __device__ inline int copy_items(int channels, int vec) { return (vectors(channels, vec) + 1) / 2; }
-
 template <typename IO, int VEC, bool TAIL>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, RotaryPlan p) {
   extern __shared__ float2 coef[];  // [tb][half]
@@ -54,10 +45,8 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, RotaryPlan p)
     coef[i] = turn(a.positions[t0 + t], a.freqs[j], a.mscale, a.sign);
   }
   __syncthreads();
-  const int turned = turned_items(a, VEC), per = turned + copy_items(a.dim - 2 * a.half, VEC);
-  const int heads = a.q_heads + a.k_heads;
-  const int v_per = a.slots ? copy_items(a.dim, VEC) : 0;
-  const int items = heads * per + a.k_heads * v_per;
+  const auto [per, v_per, items] = rotary_items(a, VEC);
+  const int turned = rotary_turned_items(a, VEC), heads = a.q_heads + a.k_heads;
   const int64_t cache_tokens = a.num_pages * a.page;
   for (int i = threadIdx.x; i < n * items; i += blockDim.x) {
     const int t = fast_div(i, p.items), r = i - t * items;
@@ -149,19 +138,13 @@ template <typename IO, int VEC>
 static void launch(const RotaryArgs &a, hipStream_t st) {
   const bool tail = (a.interleaved ? 2 * a.half : a.half) % VEC != 0 || (a.dim - 2 * a.half) % VEC != 0 ||
                     (a.slots && a.dim % VEC != 0);
+  const RotaryItems it = rotary_items(a, VEC);
   RotaryPlan p;
-  const int per = turned_items(a, VEC) + copy_items(a.dim - 2 * a.half, VEC);
-  const int v_per = a.slots ? copy_items(a.dim, VEC) : 0;
-  const int items = (a.q_heads + a.k_heads) * per + a.k_heads * v_per;
-  // more tokens a workgroup while its work items stay below two a thread and 1024
-  // workgroups are left: 65536 tokens of 6 heads of 64, tb 1 to 16: 55, 32, 25, 22, 20
-  // us; 32768 of 20 heads of 128: 71, 62, 63, 65, 74
-  p.tb = 1;
-  while (p.tb < 16 && 2 * p.tb * items <= 512 && a.tokens / (2 * p.tb) >= 1024 && 2 * p.tb * a.half <= 2048) p.tb *= 2;
+  p.tb = rotary_block_tokens(a);
   p.half = make_fast_div(a.half > 0 ? a.half : 1);
-  p.items = make_fast_div(items);
-  p.per = make_fast_div(per);
-  p.v_per = make_fast_div(v_per > 0 ? v_per : 1);
+  p.items = make_fast_div(it.token);
+  p.per = make_fast_div(it.per);
+  p.v_per = make_fast_div(it.v_per > 0 ? it.v_per : 1);
   const int grid = (int)((a.tokens + p.tb - 1) / p.tb);
   const size_t lds = (size_t)p.tb * (a.half > 0 ? a.half : 1) * sizeof(float2);
   if (tail) rotary_kernel<IO, VEC, true><<<grid, 256, lds, st>>>(a, p);
@@ -171,8 +154,8 @@ static void launch(const RotaryArgs &a, hipStream_t st) {
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   TimedLaunch tl(K_ROTARY, st);
-  if (a.bf16) launch<u16, 8>(a, st);
-  else launch<float, 4>(a, st);
+  if (a.bf16) launch<u16, rotary_vec(true)>(a, st);
+  else launch<float, rotary_vec(false)>(a, st);
   return hipGetLastError();
 }
 

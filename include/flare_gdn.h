@@ -652,7 +652,8 @@ flare_status flare_residual_norm_bwd(
  *   q, k       io [tokens, q_heads / k_heads, dim] with token strides;
  *              k_heads = 0: q alone
  *   q_out, k_out  packed
- * Requirements: 0 <= 2 * half <= dim <= 1024. */
+ * Requirements: 0 <= 2 * half <= dim <= 1024; tokens < 2^24, or up to 16 times
+ * as many of few heads (a workgroup takes 1 to 16 tokens). */
 typedef struct {
   int32_t q_heads, k_heads, dim, half;
   int32_t io_dtype;

@@ -33,6 +33,11 @@ def rotary(tokens, qh=16, kh=4, d=128, half=64, io=g.BF16):
     s = g.RotaryShape(qh, kh, d, half, io, 0, 1.0)
     return L.flare_rotary(tokens, ctypes.byref(s), FAKE, FAKE, FAKE, qh * d, FAKE, kh * d, 0, FAKE, FAKE, None)
 
+def rotary_cache(tokens, qh=64, kh=8, d=128, half=64, io=g.BF16):
+    s = g.RotaryShape(qh, kh, d, half, io, 0, 1.0)
+    return L.flare_rotary_cache(tokens, ctypes.byref(s), FAKE, FAKE, FAKE, qh * d, FAKE, kh * d, FAKE, kh * d, FAKE, FAKE,
+                                FAKE, FAKE, 100, 64, None)
+
 def gated_bwd(tokens, heads=4, d=128):
     return L.flare_gated_norm_bwd(tokens, heads, d, g.BF16, FAKE, heads * d, FAKE, heads * d, FAKE, 1, FAKE, FAKE, heads * d,
                                   FAKE, FAKE, FAKE, WS, 2 ** 40, None)
@@ -95,3 +100,19 @@ def test_nothing_is_enqueued_after_a_launch_that_failed(calls):
             call("residual_bwd", fail_at=0, tokens=4000)]
     for status, items in calls(*todo):
         assert status == 6 and len(items) == 1
+
+
+def test_rotary_of_more_workgroups_than_a_launch_holds(calls):
+    wide, small = dict(qh=64, kh=8), dict(qh=1, kh=1, d=64, half=32)  # one token a workgroup, and sixteen
+    for op in ("rotary", "rotary_cache"):
+        got = calls(call(op, tokens=2 ** 24, **wide), call(op, tokens=2 ** 24 - 1, **wide), call(op, tokens=2 ** 31 - 1, **wide),
+                    call(op, tokens=2 ** 28, **small), call(op, tokens=2 ** 28 - 16, **small))
+        assert [s for s, _ in got] == [4, 0, 4, 4, 0]
+        assert [len(items) for _, items in got] == [0, 1, 0, 0, 1] and all(n < 2 ** 32 for _, items in got for n in items)
+
+
+def test_the_other_operators_stay_below_it(calls):
+    """Norms pass their rows in rounds: the largest sizes launch."""
+    for status, items in calls(call("gated_bwd", tokens=2 ** 31 - 1, heads=1, d=1), call("gated_bwd", tokens=2 ** 27, heads=15, d=128),
+                               call("residual_bwd", tokens=2 ** 31 - 1, d=16384)):
+        assert status == 0 and len(items) == 2 and all(n < 2 ** 32 for n in items)
