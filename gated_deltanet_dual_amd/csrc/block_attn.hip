@@ -44,23 +44,36 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// 16 bytes of memory a lane, at base + offset bytes, straight into LDS: lane i's at
-// lds + 16 i.  Written as an instruction because the compiler, which cannot tell the
+// Four loads of 16 bytes of memory a lane, at base + offset bytes, straight into LDS: lane
+// i's at lds + 16 i.  Written as instructions because the compiler, which cannot tell the
 // tile in flight from the tile being read, waits for the one before reading the other;
-// whoever reads waits for the load counter, then meets the others at a barrier.  No
-// register is written but M0, which nothing else in these kernels uses.  NT: keys that
-// no other workgroup reads, kept from pushing others out of the caches (256 requests'
-// own 1024 keys, 4 heads of 128, from memory: 76 us where they take 85 otherwise, 32 MB
-// 16 us alike; but keys that four row groups read, 64 requests x 32 tokens at d = 256:
-// 346 us where they take 293).
-template <bool NT>
-__device__ __forceinline__ void load_lds16(const u16 *base, uint32_t offset, uint32_t lds) {
-  if constexpr (NT)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+// whoever reads waits for the load counter, then meets the others at a barrier.  M0, which
+// names the place in LDS, is left as it was, since the compiler does not take a reserved
+// register as overwritten: once for four loads (256 requests x 4 over a prefix of 8192 and
+// 1024 own keys: 116.6 us, 119 once for each load, 116.1 never).  NT: keys that no other workgroup
+// reads, kept from pushing others out of the caches (256 requests' own 1024 keys, 4 heads
+// of 128, from memory: 76 us where they take 85 otherwise, 32 MB 16 us alike; but keys that
+// four row groups read, 64 requests x 32 tokens at d = 256: 346 us where they take 293).
+struct LdsLoad {
+  const u16 *base;
+  uint32_t offset, lds;
+};
+template <bool NT> __device__ __forceinline__ void load_lds16(const LdsLoad (&a)[4]) {
+  uint32_t m0;
+#define FLARE_LOAD4(HINT)                                                                                              \
+  asm volatile("s_mov_b32 %0, m0\n\t"                                                                                  \
+               "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %9" HINT "\n\t"                             \
+               "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %6, %10" HINT "\n\t"                            \
+               "s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %7, %11" HINT "\n\t"                            \
+               "s_mov_b32 m0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %8, %12" HINT "\n\t"                            \
+               "s_mov_b32 m0, %0"                                                                                      \
+               : "=&s"(m0)                                                                                             \
+               : "s"(a[0].lds), "s"(a[1].lds), "s"(a[2].lds), "s"(a[3].lds), "v"(a[0].offset), "v"(a[1].offset),       \
+                 "v"(a[2].offset), "v"(a[3].offset), "s"(a[0].base), "s"(a[1].base), "s"(a[2].base), "s"(a[3].base)    \
+               : "memory")
+  if constexpr (NT) FLARE_LOAD4(" nt");
+  else FLARE_LOAD4("");
+#undef FLARE_LOAD4
 }
 // The LDS address of p, the same in all lanes.
 __device__ __forceinline__ uint32_t lds_at(const u16 *p) {
@@ -225,12 +238,22 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
     const int64_t at = ((((int64_t)pg * a.kv_heads + head) << p.page_shift) + (j & (a.page - 1))) * D;
     const u16 *kp = uniform((const u16 *)a.k_cache + at), *vp = uniform((const u16 *)a.v_cache + at);
     const uint32_t to = buf * (TK * D * 2);
+    constexpr int RPI = 64 / PIECES;
+    auto k_load = [&](int i) {
+      return LdsLoad{kp, ky ^ uint32_t(2 * (i * RPI * D + k_piece<D>(i * RPI, 0) * 8)), k_at + to + i * 1024};
+    };
+    auto v_load = [&](int i) {
+      return LdsLoad{vp, vy ^ uint32_t(2 * (i * RPI * D + v_piece<D>(i * RPI, 0) * 8)), v_at + to + i * 1024};
+    };
+    if constexpr (SUBS == 4) {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      constexpr int RPI = 64 / PIECES;
-      const uint32_t kx = 2 * (i * RPI * D + k_piece<D>(i * RPI, 0) * 8), vx = 2 * (i * RPI * D + v_piece<D>(i * RPI, 0) * 8);
-      if (SUBS == 4 || wave < 2) load_lds16<NT>(kp, ky ^ kx, k_at + to + i * 1024);
-      if (SUBS == 4 || wave >= 2) load_lds16<NT>(vp, vy ^ vx, v_at + to + i * 1024);
+      for (int i = 0; i < LOADS; i += 2) load_lds16<NT>({k_load(i), v_load(i), k_load(i + 1), v_load(i + 1)});
+    } else if (wave < 2) {
+#pragma unroll
+      for (int i = 0; i < LOADS; i += 4) load_lds16<NT>({k_load(i), k_load(i + 1), k_load(i + 2), k_load(i + 3)});
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS; i += 4) load_lds16<NT>({v_load(i), v_load(i + 1), v_load(i + 2), v_load(i + 3)});
     }
   };
   // tile t's buffer: the own keys' first is buffer 0
