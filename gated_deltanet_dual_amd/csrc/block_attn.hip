@@ -50,10 +50,13 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // whoever reads waits for the load counter, then meets the others at a barrier.  M0, which
 // names the place in LDS, is left as it was, since the compiler does not take a reserved
 // register as overwritten: once for four loads (256 requests x 4 over a prefix of 8192 and
-// 1024 own keys: 116.6 us, 119 once for each load, 116.1 never).  NT: keys that no other workgroup
-// reads, kept from pushing others out of the caches (256 requests' own 1024 keys, 4 heads
-// of 128, from memory: 76 us where they take 85 otherwise, 32 MB 16 us alike; but keys that
-// four row groups read, 64 requests x 32 tokens at d = 256: 346 us where they take 293).
+// 1024 own keys: 116.6 us, 119 once for each load, 116.1 never).  NT: own keys that no
+// other workgroup reads, kept from pushing others out of the caches (256 requests' own
+// 1024 keys, 4 heads of 128, from memory: 76 us where they take 85 otherwise, 32 MB 16 us
+// alike; but keys that four row groups read, 64 requests x 32 tokens at d = 256: 346 us where
+// they take 293).  A short prefix that every request passes goes the same way: without the
+// hint for its tiles alone, 128 requests over 512 + 512 keys take 31.2 us in place of 31.7,
+// over 512 + 64 keys 16.3 in place of 15.9, 256 of d = 64 over 512 + 512 20.0 in place of 20.3.
 struct LdsLoad {
   const u16 *base;
   uint32_t offset, lds;
@@ -503,7 +506,8 @@ __device__ __forceinline__ void attn_part(const BlockAttnArgs &a, const AttnPlan
 }
 
 // NQP, NQO: row tiles of a wave for the prefix (rows of all requests) and for a
-// request's own keys; NT: those are read by one row group (measured at load_lds16).
+// request's own keys; NT: the own keys, and a short prefix that comes before them, in loads
+// that the caches do not keep, where a request's rows are one group (measured at load_lds16).
 template <int D, int NQP, int NQO, int TK, int WPS, bool NT>
 __global__ __launch_bounds__(256, WPS) void attn_kernel(BlockAttnArgs a, AttnPlan p) {
   __shared__ __align__(16) u16 kt_lds[2][TK * D];
