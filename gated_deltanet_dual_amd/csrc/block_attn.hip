@@ -591,16 +591,17 @@ hipError_t launch_d(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
 
 hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st) {
   TimedLaunch tl(K_BLOCK_ATTN, st);
+  // one tile a wave for the prefix up to d = 128: at most 64 rows in all, so one row group
   const bool alone = p.own_groups == 1;
   if (a.dim == 64) {
     if (p.own_tiles == 2) return launch_d<64, 2, 2, 64, 3, false>(a, p, st);
     if (p.prefix_tiles == 2) return alone ? launch_d<64, 2, 1, 64, 3, true>(a, p, st) : launch_d<64, 2, 1, 64, 3, false>(a, p, st);
-    return alone ? launch_d<64, 1, 1, 64, 3, true>(a, p, st) : launch_d<64, 1, 1, 64, 3, false>(a, p, st);
+    return launch_d<64, 1, 1, 64, 3, true>(a, p, st);
   }
   if (a.dim == 128) {
     if (p.own_tiles == 2) return launch_d<128, 2, 2, 64, 2, false>(a, p, st);
     if (p.prefix_tiles == 2) return alone ? launch_d<128, 2, 1, 64, 2, true>(a, p, st) : launch_d<128, 2, 1, 64, 2, false>(a, p, st);
-    return alone ? launch_d<128, 1, 1, 64, 2, true>(a, p, st) : launch_d<128, 1, 1, 64, 2, false>(a, p, st);
+    return launch_d<128, 1, 1, 64, 2, true>(a, p, st);
   }
   return alone ? launch_d<256, 1, 1, 32, 2, true>(a, p, st) : launch_d<256, 1, 1, 32, 2, false>(a, p, st);
 }

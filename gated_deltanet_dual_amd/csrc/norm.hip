@@ -519,14 +519,13 @@ template <int VEC, typename F> void with_width(int dim, F f) {
   do {                                                                          \
     if (grid == 0) break; /* no rows: the weights' sums are still written */    \
     if (p.threads == 0 && p.nv == 1) LAUNCH(1, false, 256);                     \
-    else if (p.threads == 256 && p.nv == 1) LAUNCH(1, true, 256);               \
-    else if (p.threads == 256) LAUNCH(2, true, 256);                            \
+    else if (p.threads == 256 && p.nv == 2) LAUNCH(2, true, 256);               \
     else if (p.threads == 512) LAUNCH(2, true, 512);                            \
     else if (p.threads == 1024 && p.nv == 2) LAUNCH(2, true, 1024);             \
     else if constexpr (W::vec < 8) {                                            \
       if (p.threads == 0) LAUNCH(2, false, 256);                                \
       else LAUNCH(4, true, 1024);                                               \
-    }                                                                           \
+    } else LAUNCH(1, true, 256); /* fp32's are of two vectors a thread */       \
   } while (0)
 
 template <typename IO, int VEC> void gated_forward(const GatedNormArgs &a, hipStream_t st) {

@@ -13,6 +13,7 @@ static dim3 pushed_grid, pushed_block;
 static size_t pushed_shared;
 static void *pushed_stream;
 static uint64_t items[kMost];
+static const void *functions[kMost];
 static int launches, fail_at = -1;
 static hipError_t last;
 
@@ -20,6 +21,7 @@ void stub_reset(void) { launches = 0, fail_at = -1, last = 0; }
 void stub_fail_at(int n) { fail_at = n; }
 int stub_launches(void) { return launches; }
 uint64_t stub_items(int n) { return items[n]; }
+const void *stub_function(int n) { return functions[n]; }
 
 hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t shared, void *stream) {
   pushed_grid = grid, pushed_block = block, pushed_shared = shared, pushed_stream = stream;
@@ -30,10 +32,10 @@ hipError_t __hipPopCallConfiguration(dim3 *grid, dim3 *block, size_t *shared, vo
   return 0;
 }
 hipError_t hipLaunchKernel(const void *f, dim3 grid, dim3 block, void **args, size_t shared, void *stream) {
-  (void)f, (void)args, (void)shared, (void)stream;
+  (void)args, (void)shared, (void)stream;
   const uint64_t x = (uint64_t)grid.x * block.x;
   const int refused = launches == fail_at || x >> 32 || grid.x == 0 || grid.y == 0;
-  if (launches < kMost) items[launches] = x;
+  if (launches < kMost) items[launches] = x, functions[launches] = f;
   ++launches;
   if (refused) last = kInvalidConfiguration;
   return refused ? kInvalidConfiguration : 0;
