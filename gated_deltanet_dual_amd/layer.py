@@ -199,7 +199,7 @@ def gated_norm(x, weight, gate=None, activation=SILU, eps=1e-6, out=None, want_r
 
 def gated_norm_bwd_workspace_bytes(T, H, d) -> int:
     """flare_gated_norm_bwd_workspace_size."""
-    return int(lib().flare_gated_norm_bwd_workspace_size(int(T), int(H), int(d)))
+    return int(lib().flare_gated_norm_bwd_workspace_size(int(T), _i32(H, "H"), _i32(d, "d")))
 
 
 def gated_norm_bwd(x, weight, gate, dy, rstd, activation=SILU, workspace=None, out=None):
@@ -260,7 +260,7 @@ def residual_norm(x, residual, w_pre, w_post=None, gate=None, scale=None, activa
 
 def residual_norm_bwd_workspace_bytes(T, C) -> int:
     """flare_residual_norm_bwd_workspace_size."""
-    return int(lib().flare_residual_norm_bwd_workspace_size(int(T), int(C)))
+    return int(lib().flare_residual_norm_bwd_workspace_size(int(T), _i32(C, "C")))
 
 
 def residual_norm_bwd(x, residual, w_pre, dy, dh, rstd, w_post=None, gate=None, scale=None, activation=SIGMOID,
@@ -385,6 +385,8 @@ def _chk_cache(k_cache, v_cache, heads, d, io, dev):
     if k_cache is None or k_cache.dim() != 4:
         _fail("k_cache must be [num_pages, heads, page, d]")
     pages, page = k_cache.shape[0], k_cache.shape[2]
+    if heads > 0x7FFFFFFF or page > 0x7FFFFFFF:
+        _i32(heads, "cache heads"), _i32(page, "page")
     _chk(k_cache, "k_cache", (pages, heads, page, d), io, dev)
     _chk(v_cache, "v_cache", (pages, heads, page, d), io, dev)
     return pages, page
@@ -443,9 +445,11 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
 
 def block_attention_workspace_bytes(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len) -> int:
     """flare_block_attention_workspace_size (bf16)."""
+    sizes = (("R", R), ("B", B), ("q_heads", q_heads), ("kv_heads", kv_heads), ("d", d), ("page", page),
+             ("max_seq_len", max_seq_len), ("prefix_len", prefix_len))
+    R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len = (_i32(n, name) for name, n in sizes)
     shp = AttentionShape(B, q_heads, kv_heads, d, page, BF16, 0, 0.0)
-    return int(lib().flare_block_attention_workspace_size(int(R), ctypes.byref(shp), int(max_seq_len),
-                                                          int(prefix_len)))
+    return int(lib().flare_block_attention_workspace_size(R, ctypes.byref(shp), max_seq_len, prefix_len))
 
 
 def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=None, prefix_len=0, causal=False,
