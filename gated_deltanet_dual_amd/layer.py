@@ -302,7 +302,9 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, ori
                 is stretched by the factor, the fastest not at all
       "yarn"    pairs that turn more than beta_fast times within original_length
                 keep their frequency, those below beta_slow are divided by the
-                factor, a linear ramp between; mscale = 1 + 0.1 ln(factor)"""
+                factor, a linear ramp between, whose ends are rounded outwards to
+                whole pairs (as programs that trained with it have it);
+                mscale = 1 + 0.1 ln(factor)"""
     torch = _torch()
     n = int(rotary_dim)
     if n < 0 or n % 2:
@@ -323,6 +325,7 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, ori
         pair = lambda turns: n * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
         low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), n - 1)
         ramp = np.clip((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+        ramp[i > pair(beta_slow)] = 1.0  # the first pair too, where the ramp ends before it
         f = f * (1 - ramp) + f / factor * ramp
         mscale = 1.0 + 0.1 * math.log(factor)
     elif scaling not in ("none", "ntk"):
