@@ -321,6 +321,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, ori
     elif scaling == "yarn":
         if original_length <= 0:
             _fail("yarn scaling needs the original length")
+        if not beta_fast >= beta_slow > 0:
+            _fail("yarn scaling needs beta_fast of at least beta_slow, both above 0 (got %s and %s)" % (beta_fast, beta_slow))
         # the (real) index of the pair that turns `turns` times within original_length
         pair = lambda turns: n * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
         low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), n - 1)

@@ -18,3 +18,9 @@ def test_slow_pairs_are_divided_and_fast_ones_kept(n, length):
     turns = length * base / (2 * math.pi)
     assert torch.equal(y[turns < 1], base[turns < 1] / 4) and torch.equal(y[turns > 32], base[turns > 32])
     assert (y <= base).all() and (y >= base / 4).all() and m == 1 + 0.1 * math.log(4.0)
+
+
+def test_ramps_without_two_ends_are_refused():
+    for bad in (dict(beta_slow=0.0), dict(beta_slow=-1.0), dict(beta_fast=0.5), dict(beta_fast=math.nan)):
+        with pytest.raises(g.FlareError, match="beta"):
+            g.rotary_frequencies(64, scaling="yarn", factor=4.0, original_length=4096, device="cpu", **bad)
