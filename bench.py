@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import argparse
 import ctypes
+import gc
 import hashlib
 import json
 import os
@@ -153,9 +154,14 @@ class Timer:
     def run(self, name, fn):
         s = self.torch.cuda.Event(enable_timing=True)
         e = self.torch.cuda.Event(enable_timing=True)
+        # a garbage collection between the events (30 to 50 ms) would count as the call's
+        collecting = gc.isenabled()
+        gc.disable()
         s.record()
         out = fn()
         e.record()
+        if collecting:
+            gc.enable()
         self.times.setdefault(name, []).append((s, e))
         return out
 
