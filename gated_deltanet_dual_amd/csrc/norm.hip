@@ -102,8 +102,8 @@ template <bool BLOCK> struct Team {
 };
 
 // ---------------------------------------------------------------- gated norm
-// 32768 x 16 rows of 128, bf16: 403 MB in 78 us, 5.2 TB/s (a copy of that size
-// reaches 5.1 to 5.5).
+// 32768 x 16 rows of 128, bf16: 403 MB in 79 to 82 us, 4.9 to 5.1 TB/s (a copy of that
+// size reaches 5.1 to 5.5).
 template <typename IO, int VEC, bool TAIL, int NV, bool BLOCK, int THREADS>
 __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a, int team) {
   __shared__ float red[16];

@@ -33,8 +33,10 @@ struct RotaryPlan {
 // One workgroup: `tb` tokens.  Their coefficients first, to LDS, so that a
 // token's angles are formed once for all its heads; then the heads' vectors.
 // Memory bounds it: 32768 tokens, 16 + 4 heads of 128, 32 of them turned, bf16: 336 MB
-// in 71 us, 4.7 TB/s.  The serving form over 1024 tokens takes 5.3 us, mostly a
-// launch's and the coefficients' latency.
+// in 64 to 66 us, 5.2 TB/s (two tokens a workgroup).  The serving form over 1024 tokens
+// takes 5.2 us where a launch takes 3.7: positions and frequencies, the slot, and the row
+// itself are three latencies in a row, and in the interleaved layout 71 % of the cycles of
+// the coefficients' LDS reads are bank conflicts.
 template <typename IO, int VEC, bool TAIL>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, RotaryPlan p) {
   extern __shared__ float2 coef[];  // [tb][half]

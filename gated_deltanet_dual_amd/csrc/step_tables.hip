@@ -21,8 +21,8 @@ __device__ __forceinline__ int32_t pages_of(uint32_t n, const FastDiv &d) { retu
 // the two offsets of each request in LDS; then it fills its own share of the
 // rows.  One launch instead of a scan and a fill.  Latency bounds it: the lengths'
 // loads, the scan's two barriers, a search of log2 R steps and a page's load follow on
-// each other.  256 requests x 4 tokens 4.8 us; 700 requests with 700 K tokens, 16 a
-// page, 14.5 us for 8.6 MB.
+// each other.  256 requests x 4 tokens 5.1 us; 700 requests with 700 K tokens, 16 a
+// page, in 1.4 M rows 13.3 us for 17 MB (rows behind the last token are written too).
 __global__ __launch_bounds__(kThreads) void step_tables_kernel(StepTablesArgs a, FastDiv pd, int rows_per_block) {
   extern __shared__ int32_t lds[];
   // of each request: tokens and new pages before it, and the tokens it holds

@@ -5,7 +5,9 @@ serving step, and the block attention of the softmax layers.
 Marshalling and checks only, as in the package's other entry points: every
 function names the entry point of ``include/flare_gdn.h`` it calls, checks
 every tensor (dtype, shape, strides, device) before the library sees its
-pointer, and enqueues on the current stream of the tensors' device.
+pointer, and enqueues on the current stream of the tensors' device.  As the
+package's other calls they record no graph, whatever their inputs require:
+``autograd`` has the differentiable forms, under the same names.
 """
 from __future__ import annotations
 

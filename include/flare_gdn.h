@@ -738,6 +738,8 @@ flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens,
  *   workspace  flare_block_attention_workspace_size bytes, 256-byte aligned
  *              (the parts' outputs and statistics); NULL when that is 0
  * Rows of a page that no length reaches may hold anything, NaN included.
+ * Made for blocks of a few tokens: a long causal block (a prompt) is right but
+ * passes every key up to the request's length for each of its rows.
  * Requirements: io_dtype FLARE_BF16; head_dim in {64, 128, 256}; page a power of
  * two of at least 16; q_heads a multiple of kv_heads; 16-byte aligned q,
  * caches and o; num_req * block * q_heads below 2^25, and fewer than 2^24 units
