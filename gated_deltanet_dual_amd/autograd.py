@@ -166,3 +166,31 @@ def rotary(positions, freqs, q, k=None, interleaved=False, mscale=1.0):
     one); gradients flow to q and k."""
     out = RotaryFunction.apply(positions, freqs, q, k, bool(interleaved), float(mscale))
     return out if k is not None else (out[0], None)
+
+
+class QkNormRotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, positions, freqs, q, k, q_weight, k_weight, eps, interleaved, mscale):
+        q, k = _rows(q), _rows(k)
+        q_weight, k_weight = (None if w is None else w.contiguous() for w in (q_weight, k_weight))
+        ctx.eps, ctx.interleaved, ctx.mscale = eps, interleaved, mscale
+        ctx.save_for_backward(positions, freqs, q, k, q_weight, k_weight)
+        y, z = _layer.qk_norm_rotary(positions, freqs, q, k, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                     interleaved=interleaved, mscale=mscale)
+        return (y,) if k is None else (y, z)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk=None):
+        positions, freqs, q, k, q_weight, k_weight = ctx.saved_tensors
+        g = _layer.qk_norm_rotary_bwd(positions, freqs, q, k, _rows(dq), _rows(dk), q_weight=q_weight, k_weight=k_weight,
+                                      eps=ctx.eps, interleaved=ctx.interleaved, mscale=ctx.mscale)
+        return None, None, g["dq"], g["dk"], g["dq_weight"], g["dk_weight"], None, None, None
+
+
+def qk_norm_rotary(positions, freqs, q, k=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, mscale=1.0):
+    """Differentiable flare_qk_norm_rotary (layer.qk_norm_rotary): (q, k) normed
+    and turned (k None without one); gradients flow to q, k and the weights."""
+    out = QkNormRotaryFunction.apply(positions, freqs, q, k, q_weight, k_weight, float(eps), bool(interleaved),
+                                     float(mscale))
+    return out if k is not None else (out[0], None)

@@ -1,5 +1,5 @@
 // api_layer.hip -- extern "C" entry points of the operators around the GDN step
-// (norms, rotary positions, serving-step tables, block attention).  As in
+// (norms, rotary positions, caches, serving-step tables, block attention).  As in
 // api.hip: everything is validated on the host before anything is enqueued, and
 // nothing is allocated, freed or synchronised.
 #include <hip/hip_runtime.h>
@@ -189,6 +189,147 @@ flare_status flare_rotary_cache(int64_t tokens, const flare_rotary_shape *shape,
   st = check_rotary_blocks(a);
   if (st != FLARE_OK) return st;
   return hip_status(launch_rotary(a, (hipStream_t)stream), "rotary_cache launch");
+}
+
+static QkNormArgs qk_norm_args(const RotaryArgs &r, const float *q_weight, const float *k_weight, float eps) {
+  QkNormArgs a{};
+  a.r = r;
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  a.eps = eps;
+  return a;
+}
+
+flare_status flare_qk_norm_rotary(int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+                                  const double *freqs, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                  const float *q_weight, const float *k_weight, float eps, void *q_out, void *k_out,
+                                  void *stream) {
+  clear_error();
+  flare_status st = check_rotary(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out);
+  if (st != FLARE_OK) return st;
+  if (tokens > 0 && shape->k_heads > 0 && !k_out) return fail(FLARE_ERR_NULL, "qk_norm_rotary: k_out is NULL");
+  QkNormArgs a = qk_norm_args(rotary_args(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out), q_weight,
+                              k_weight, eps);
+  a.r.k_out = k_out;
+  st = check_qk_norm(a, tokens);
+  if (st != FLARE_OK) return st;
+  return hip_status(launch_qk_norm_rotary(a, (hipStream_t)stream), "qk_norm_rotary launch");
+}
+
+size_t flare_qk_norm_rotary_bwd_workspace_size(int64_t tokens, int32_t dim) {
+  if (tokens < 0 || tokens > INT32_MAX || dim < 1 || dim > 1024) return 0;
+  return qk_norm_bwd_workspace_bytes(tokens, dim);
+}
+
+flare_status flare_qk_norm_rotary_bwd(int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+                                      const double *freqs, const void *q, int64_t q_stride, const void *k,
+                                      int64_t k_stride, const float *q_weight, const float *k_weight, float eps,
+                                      const void *dq_out, int64_t dq_out_stride, const void *dk_out,
+                                      int64_t dk_out_stride, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                                      void *workspace, size_t workspace_bytes, void *stream) {
+  clear_error();
+  flare_status st = check_rotary(tokens, shape, positions, freqs, q, q_stride, k, k_stride, dq);
+  if (st != FLARE_OK) return st;
+  if (dq_out_stride < (int64_t)shape->q_heads * shape->dim ||
+      (shape->k_heads > 0 && dk_out_stride < (int64_t)shape->k_heads * shape->dim))
+    return fail(FLARE_ERR_SHAPE, "qk_norm_rotary_bwd: a gradient's token stride is below a row");
+  if ((q_weight && !dq_weight) || (k_weight && !dk_weight) ||
+      (tokens > 0 && (!dq_out || (shape->k_heads > 0 && (!dk_out || !dk)))))
+    return fail(FLARE_ERR_NULL, "qk_norm_rotary_bwd: a required pointer is NULL");
+  QkNormArgs a = qk_norm_args(rotary_args(tokens, shape, positions, freqs, q, q_stride, k, k_stride, nullptr), q_weight,
+                              k_weight, eps);
+  a.r.sign = -1.0f;
+  a.dout[0] = dq_out; a.dout[1] = dk_out;
+  a.dout_stride[0] = dq_out_stride; a.dout_stride[1] = dk_out_stride;
+  a.dx[0] = dq; a.dx[1] = dk;
+  a.dweight[0] = dq_weight; a.dweight[1] = dk_weight;
+  st = check_qk_norm(a, tokens);
+  if (st != FLARE_OK) return st;
+  if (q_weight || k_weight) {
+    st = check_workspace(workspace, workspace_bytes, qk_norm_bwd_workspace_bytes(tokens, shape->dim));
+    if (st != FLARE_OK) return st;
+  }
+  a.part = reinterpret_cast<float *>(workspace);
+  return hip_status(launch_qk_norm_rotary_bwd(a, (hipStream_t)stream), "qk_norm_rotary_bwd launch");
+}
+
+flare_status flare_qk_norm_rotary_cache(int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+                                        const double *freqs, const void *q, int64_t q_stride, const void *k,
+                                        int64_t k_stride, const void *v, int64_t v_stride, const float *q_weight,
+                                        const float *k_weight, float eps, const int64_t *slots, void *q_out,
+                                        void *k_cache, void *v_cache, int64_t num_pages, int32_t page, void *stream) {
+  clear_error();
+  flare_status st = check_rotary(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out);
+  if (st != FLARE_OK) return st;
+  if (page < 1 || num_pages < 0 || num_pages > INT32_MAX)
+    return fail(FLARE_ERR_SHAPE, "qk_norm_rotary_cache: page or num_pages");
+  if (tokens == 0) return FLARE_OK;
+  if (!slots || (num_pages > 0 && (!k_cache || !v_cache)))
+    return fail(FLARE_ERR_NULL, "qk_norm_rotary_cache: a required pointer is NULL");
+  QkNormArgs a = qk_norm_args(rotary_args(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out), q_weight,
+                              k_weight, eps);
+  a.r.v = v;
+  a.r.v_stride = v_stride;
+  a.r.slots = slots;
+  a.r.k_cache = k_cache;
+  a.r.v_cache = v_cache;
+  a.r.num_pages = num_pages;
+  a.r.page = page;
+  st = check_qk_norm(a, tokens);
+  if (st != FLARE_OK) return st;
+  return hip_status(launch_qk_norm_rotary(a, (hipStream_t)stream), "qk_norm_rotary_cache launch");
+}
+
+flare_status flare_qk_norm_rotary_cache_fp4(int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+                                            const double *freqs, const void *q, int64_t q_stride, const void *k,
+                                            int64_t k_stride, const void *v, int64_t v_stride, const float *q_weight,
+                                            const float *k_weight, float eps, const int64_t *slots, void *q_out,
+                                            uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales,
+                                            int64_t num_pages, int32_t page, void *stream) {
+  clear_error();
+  flare_status st = check_rotary(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out);
+  if (st != FLARE_OK) return st;
+  const Cache4 k4{k_codes, k_scales}, v4{v_codes, v_scales};
+  st = check_cache4("qk_norm_rotary_cache_fp4", shape->dim, num_pages, page, k4, v4);
+  if (st != FLARE_OK) return st;
+  if (tokens == 0) return FLARE_OK;
+  if (!slots) return fail(FLARE_ERR_NULL, "qk_norm_rotary_cache_fp4: slots is NULL");
+  QkNormArgs a = qk_norm_args(rotary_args(tokens, shape, positions, freqs, q, q_stride, k, k_stride, q_out), q_weight,
+                              k_weight, eps);
+  a.r.v = v;
+  a.r.v_stride = v_stride;
+  a.r.slots = slots;
+  a.r.num_pages = num_pages;
+  a.r.page = page;
+  a.into4 = true;
+  a.k4 = k4;
+  a.v4 = v4;
+  st = check_qk_norm(a, tokens);
+  if (st != FLARE_OK) return st;
+  return hip_status(launch_qk_norm_rotary(a, (hipStream_t)stream), "qk_norm_rotary_cache_fp4 launch");
+}
+
+flare_status flare_cache_fp4_rows(int64_t rows, int32_t heads, int32_t dim, int32_t io_dtype, const int64_t *slots,
+                                  const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                                  const uint8_t *v_scales, int64_t num_pages, int32_t page, void *k_out, void *v_out,
+                                  void *stream) {
+  clear_error();
+  flare_status st = check_io(io_dtype);
+  if (st != FLARE_OK) return st;
+  if (rows < 0 || heads < 1) return fail(FLARE_ERR_SHAPE, "cache_fp4_rows: rows must not be negative, heads positive");
+  if (rows > INT32_MAX || heads > 65536 || dim > 1024)
+    return fail(FLARE_ERR_UNSUPPORTED, "cache_fp4_rows: beyond 2^31 - 1 rows, 65536 heads or 1024 channels");
+  const Cache4 k4{const_cast<uint8_t *>(k_codes), const_cast<uint8_t *>(k_scales)};
+  const Cache4 v4{const_cast<uint8_t *>(v_codes), const_cast<uint8_t *>(v_scales)};
+  st = check_cache4("cache_fp4_rows", dim, num_pages, page, k4, v_out ? v4 : k4);
+  if (st != FLARE_OK) return st;
+  if (rows == 0) return FLARE_OK;
+  if (!slots || !k_out) return fail(FLARE_ERR_NULL, "cache_fp4_rows: a required pointer is NULL");
+  if ((((uintptr_t)k_out | (uintptr_t)v_out) & 15u) != 0)
+    return fail(FLARE_ERR_ALIGN, "cache_fp4_rows: outputs must be 16-byte aligned");
+  Cache4Rows a{rows, num_pages, heads, dim, page, io_dtype == FLARE_BF16, slots, {k_codes, v_codes}, {k_scales, v_scales},
+               {k_out, v_out}};
+  return hip_status(launch_cache_fp4_rows(a, (hipStream_t)stream), "cache_fp4_rows launch");
 }
 
 flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens, const int32_t *new_lens, int32_t *block_table,

@@ -210,6 +210,35 @@ flare_status check_rotary_blocks(const RotaryArgs &a) {
   return FLARE_OK;
 }
 
+flare_status check_qk_norm(const QkNormArgs &a, int64_t tokens) {
+  flare_status st = check_eps(a.eps);
+  if (st != FLARE_OK) return st;
+  if (a.r.k_heads == 0 && a.weight[1]) return fail(FLARE_ERR_SHAPE, "qk_norm_rotary: a k_weight, but no k heads");
+  if (a.r.slots) {
+    if (a.r.k_heads < 1) return fail(FLARE_ERR_SHAPE, "qk_norm_rotary_cache: no k heads");
+    if (a.r.v_stride < (int64_t)a.r.k_heads * a.r.dim)
+      return fail(FLARE_ERR_SHAPE, "qk_norm_rotary_cache: v_stride below a row");
+    if (tokens > 0 && !a.r.v) return fail(FLARE_ERR_NULL, "qk_norm_rotary_cache: v is NULL");
+  }
+  return check_rotary_blocks(a.r);
+}
+
+// Workgroups of the reverse mode at most, each of which writes a partial row a weight.
+int64_t qk_norm_bwd_blocks(int64_t tokens) { return tokens < 1024 ? tokens : 1024; }
+size_t qk_norm_bwd_workspace_bytes(int64_t tokens, int32_t dim) {
+  return (size_t)qk_norm_bwd_blocks(tokens) * dim * 2 * sizeof(float) + 256;
+}
+
+flare_status check_cache4(const char *what, int32_t dim, int64_t num_pages, int32_t page, const Cache4 &k, const Cache4 &v) {
+  if (dim < 1 || dim % 32 != 0) return fail(FLARE_ERR_UNSUPPORTED, "%s: %d channels, not groups of 32", what, dim);
+  if (page < 1 || num_pages < 0 || num_pages > INT32_MAX) return fail(FLARE_ERR_SHAPE, "%s: page or num_pages", what);
+  if (num_pages > 0 && (!k.codes || !k.scales || !v.codes || !v.scales))
+    return fail(FLARE_ERR_NULL, "%s: a cache pointer is NULL", what);
+  if ((((uintptr_t)k.codes | (uintptr_t)v.codes) & 15u) != 0)
+    return fail(FLARE_ERR_ALIGN, "%s: the codes must be 16-byte aligned", what);
+  return FLARE_OK;
+}
+
 flare_status check_step_tables(const StepTablesArgs &a) {
   if (a.num_req < 0 || a.max_pages < 0 || a.num_free < 0 || a.max_tokens < 0 || a.position_offset < 0)
     return fail(FLARE_ERR_SHAPE, "step_tables: a negative size");

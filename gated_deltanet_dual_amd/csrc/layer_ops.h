@@ -81,6 +81,35 @@ FLARE_HD RotaryItems rotary_items(const RotaryArgs &a, int vec) {
 constexpr int rotary_vec(bool bf16) { return bf16 ? 8 : 4; }  // 16 bytes
 int rotary_block_tokens(const RotaryArgs &a);                 // tokens a workgroup
 
+// ---------------------------------------------------------------- q/k norms with rotary positions
+// A cache in 4 bits: rows of dim / 2 bytes of codes, and for each group of 32
+// channels a page's bytes of scales.
+struct Cache4 {
+  uint8_t *codes;   // [num_pages, heads, page, dim / 2]
+  uint8_t *scales;  // [num_pages, heads, dim / 32, page]
+};
+
+struct QkNormArgs {
+  RotaryArgs r;  // sizes, positions, q, k, v, where they go; the reverse mode's sign is -1
+  float eps;
+  const float *weight[2];  // of q and k; NULL: turned, not normed
+  bool into4;              // k4, v4 in place of r.k_cache, r.v_cache
+  Cache4 k4, v4;
+  // reverse mode: the gradients of the outputs, then of the inputs
+  const void *dout[2];
+  int64_t dout_stride[2];
+  void *dx[2];
+  float *dweight[2], *part;  // part [2][blocks][dim]
+};
+
+struct Cache4Rows {
+  int64_t rows, num_pages;
+  int heads, dim, page, bf16;
+  const int64_t *slots;
+  const uint8_t *codes[2], *scales[2];  // of keys and values; out[1] NULL: keys alone
+  void *out[2];                         // [rows, heads, dim]
+};
+
 // ---------------------------------------------------------------- step tables
 constexpr int kTablesMaxReq = 8192;  // three int32 per request in LDS
 
@@ -130,6 +159,11 @@ flare_status check_rotary(int64_t tokens, const flare_rotary_shape *s, const int
                           const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_out);
 // the launch's limit, once the arguments are laid out
 flare_status check_rotary_blocks(const RotaryArgs &a);
+flare_status check_qk_norm(const QkNormArgs &a, int64_t tokens);
+int64_t qk_norm_bwd_blocks(int64_t tokens);
+size_t qk_norm_bwd_workspace_bytes(int64_t tokens, int32_t dim);
+// a cache's sizes and pointers; `what` names the call
+flare_status check_cache4(const char *what, int32_t dim, int64_t num_pages, int32_t page, const Cache4 &k, const Cache4 &v);
 flare_status check_step_tables(const StepTablesArgs &a);
 // shape alone (for the size query), then everything
 flare_status check_attention_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,

@@ -626,4 +626,9 @@ hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t st) {
   return a.bf16 ? residual_reverse<u16, float, 8>(a, st) : residual_reverse<float, float, 4>(a, st);
 }
 
+hipError_t launch_norm_partials(const float *part, int blocks, int dim, float *const (&out)[3], hipStream_t st) {
+  norm_partials_kernel<<<dim3((dim + 15) / 16, 3), 1024, 0, st>>>(part, blocks, dim, out[0], out[1], out[2]);
+  return hipGetLastError();
+}
+
 }  // namespace flare

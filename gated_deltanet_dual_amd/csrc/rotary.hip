@@ -12,18 +12,11 @@
 
 #include "fast_div.h"
 #include "layer_launch.h"
+#include "rotary_turn.h"
 #include "vec_io.h"
 
 namespace flare {
 namespace {
-
-// m cos and m sin of position * freq (sign: -1 for the reverse mode).
-__device__ __forceinline__ float2 turn(int32_t position, double freq, float m, float sign) {
-  const double turns = (double)position * (freq * 0.15915494309189533577);
-  float s, c;
-  sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-  return make_float2(m * c, m * sign * s);
-}
 
 struct RotaryPlan {
   int tb;                            // tokens a workgroup

@@ -17,7 +17,9 @@ const char *const kNames[K_COUNT] = {"gdn_dual_fwd_kernel", "gdn_bwd_scan_kernel
                                      "shortconv_dual_kernel", "gdn_tri_kernel", "gdn_bwd_pre_kernel",
                                      "gdn_fwd_pre_kernel", "gdn_fwd_scan_kernel", "shortconv_dual_bwd_kernel",
                                      "gdn_scatter_kernel", "gdn_fwd_prep_kernel", "norm_kernel", "norm_bwd_kernel",
-                                     "rotary_kernel", "step_tables_kernel", "block_attention_kernel"};
+                                     "rotary_kernel", "step_tables_kernel", "block_attention_kernel", "qk_norm_rotary_kernel",
+                                     "qk_norm_rotary_bwd_kernel", "cache_fp4_rows_kernel",
+                                     "block_attention_fp4_kernel"};
 std::atomic<int> g_on{0};
 std::mutex g_mu;
 std::vector<std::pair<hipEvent_t, hipEvent_t>> g_rec[K_COUNT];

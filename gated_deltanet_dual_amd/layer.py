@@ -59,12 +59,22 @@ def declare(L):
     L.flare_residual_norm_bwd.argtypes = [I64, I32, I32, I32, P, I64, P, P, I64, P, P, P, I32] + [P] * 9 + [P, SZ, P]
     L.flare_rotary.argtypes = [I64, RP, P, P, P, I64, P, I64, I32, P, P, P]
     L.flare_rotary_cache.argtypes = [I64, RP, P, P, P, I64, P, I64, P, I64, P, P, P, P, I64, I32, P]
+    QN = [I64, RP, P, P, P, I64, P, I64]
+    L.flare_qk_norm_rotary.argtypes = QN + [P, P, F, P, P, P]
+    L.flare_qk_norm_rotary_bwd_workspace_size.argtypes = [I64, I32]
+    L.flare_qk_norm_rotary_bwd_workspace_size.restype = SZ
+    L.flare_qk_norm_rotary_bwd.argtypes = QN + [P, P, F, P, I64, P, I64, P, P, P, P, P, SZ, P]
+    L.flare_qk_norm_rotary_cache.argtypes = QN + [P, I64, P, P, F, P, P, P, P, I64, I32, P]
+    L.flare_qk_norm_rotary_cache_fp4.argtypes = QN + [P, I64, P, P, F, P, P, P, P, P, P, I64, I32, P]
+    L.flare_cache_fp4_rows.argtypes = [I64, I32, I32, I32, P, P, P, P, P, I64, I32, P, P, P]
     L.flare_step_tables.argtypes = [I32, P, P, P, I32, P, I64, P, I32, I32, I64, P, P, P, P, P, P, P]
     L.flare_block_attention_workspace_size.argtypes = [I32, AP, I32, I32]
     L.flare_block_attention_workspace_size.restype = SZ
     L.flare_block_attention.argtypes = [I32, AP, P, P, P, I64, P, I32, P, I32, P, I32, P, P, P, SZ, P]
     for name in ("flare_gated_norm", "flare_gated_norm_bwd", "flare_residual_norm", "flare_residual_norm_bwd",
-                 "flare_rotary", "flare_rotary_cache", "flare_step_tables", "flare_block_attention"):
+                 "flare_rotary", "flare_rotary_cache", "flare_qk_norm_rotary", "flare_qk_norm_rotary_bwd",
+                 "flare_qk_norm_rotary_cache", "flare_qk_norm_rotary_cache_fp4", "flare_cache_fp4_rows",
+                 "flare_step_tables", "flare_block_attention"):
         getattr(L, name).restype = ctypes.c_int
 
 
@@ -389,14 +399,171 @@ def rotary_cache(positions, freqs, q, k, v, slots, k_cache, v_cache, interleaved
 
 def _chk_cache(k_cache, v_cache, heads, d, io, dev):
     """Key and value pages [num_pages, heads, page, d]; returns (num_pages, page)."""
-    if k_cache is None or k_cache.dim() != 4:
-        _fail("k_cache must be [num_pages, heads, page, d]")
+    if not isinstance(k_cache, _torch().Tensor) or not isinstance(v_cache, _module.Tensor) or k_cache.dim() != 4:
+        _fail("k_cache and v_cache must be tensors [num_pages, heads, page, d]")
     pages, page = k_cache.shape[0], k_cache.shape[2]
     if heads > 0x7FFFFFFF or page > 0x7FFFFFFF:
         _i32(heads, "cache heads"), _i32(page, "page")
     _chk(k_cache, "k_cache", (pages, heads, page, d), io, dev)
     _chk(v_cache, "v_cache", (pages, heads, page, d), io, dev)
     return pages, page
+
+
+# ---------------------------------------------------------------- q/k norms with rotary positions
+
+def _norm_weights(q_weight, k_weight, k, dim, dev):
+    if k is None and k_weight is not None:
+        _fail("k_weight without k")
+    _chk(q_weight, "q_weight", (dim,), _module.float32, dev, optional=True)
+    _chk(k_weight, "k_weight", (dim,), _module.float32, dev, optional=True)
+
+
+def qk_norm_rotary(positions, freqs, q, k=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, mscale=1.0,
+                   out=None):
+    """The norms of queries and keys for each head and their rotary positions in
+    one pass (flare_qk_norm_rotary): x / sqrt(mean x^2 + eps) * weight over the
+    last dimension, then rotary().  q_weight, k_weight fp32 [d], or None: that
+    side is turned, not normed.  The other arguments and the result are
+    rotary()'s."""
+    T, shp, io, dev, qs, ks = _rotary_inputs(positions, freqs, q, k, interleaved, mscale)
+    _norm_weights(q_weight, k_weight, k, shp.dim, dev)
+    qo, ko = out if out is not None else (None, None)
+    qo = _out_like(qo, "q out", q)
+    ko = _out_like(ko, "k out", k) if k is not None else None
+    _run(dev, lib().flare_qk_norm_rotary, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs, _ptr(k), ks,
+         _ptr(q_weight), _ptr(k_weight), eps, _ptr(qo), _ptr(ko))
+    return qo, ko
+
+
+def qk_norm_rotary_bwd_workspace_bytes(T, d) -> int:
+    """flare_qk_norm_rotary_bwd_workspace_size."""
+    return int(lib().flare_qk_norm_rotary_bwd_workspace_size(int(T), _i32(d, "d")))
+
+
+def qk_norm_rotary_bwd(positions, freqs, q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                       mscale=1.0, workspace=None, out=None):
+    """Reverse mode of qk_norm_rotary (flare_qk_norm_rotary_bwd): dq_out, dk_out
+    the gradients of its outputs (slices of wider rows allowed; k and dk_out
+    None without keys).  Returns a dict dq, dk, dq_weight, dk_weight (None for
+    what the forward did not have); `out` = such a dict reuses its buffers."""
+    T, shp, io, dev, qs, ks = _rotary_inputs(positions, freqs, q, k, interleaved, mscale)
+    _norm_weights(q_weight, k_weight, k, shp.dim, dev)
+    dqs = _token_rows(dq_out, "dq_out", q.shape, io, dev)
+    if k is None and dk_out is not None:
+        _fail("dk_out without k")
+    dks = 0 if k is None else _token_rows(dk_out, "dk_out", k.shape, io, dev)
+    out = out or {}
+    g = {"dq": _out_like(out.get("dq"), "dq", q),
+         "dk": _out_like(out.get("dk"), "dk", k) if k is not None else None,
+         "dq_weight": _out_like(out.get("dq_weight"), "dq_weight", q_weight) if q_weight is not None else None,
+         "dk_weight": _out_like(out.get("dk_weight"), "dk_weight", k_weight) if k_weight is not None else None}
+    if q_weight is not None or k_weight is not None:
+        workspace = _workspace(workspace, qk_norm_rotary_bwd_workspace_bytes(T, shp.dim), dev)
+    _run(dev, lib().flare_qk_norm_rotary_bwd, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs, _ptr(k), ks,
+         _ptr(q_weight), _ptr(k_weight), eps, _ptr(dq_out), dqs, _ptr(dk_out), dks, _ptr(g["dq"]), _ptr(g["dk"]),
+         _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return g
+
+
+def qk_norm_rotary_cache(positions, freqs, q, k, v, slots, k_cache, v_cache, q_weight=None, k_weight=None, eps=1e-6,
+                         interleaved=False, mscale=1.0, out=None):
+    """The serving form (flare_qk_norm_rotary_cache): returns q normed and
+    turned; k normed and turned and v are written to the cache as by
+    rotary_cache."""
+    if k is None or v is None:
+        _fail("k and v are required", 1)
+    T, shp, io, dev, qs, ks = _rotary_inputs(positions, freqs, q, k, interleaved, mscale)
+    _norm_weights(q_weight, k_weight, k, shp.dim, dev)
+    vs = _token_rows(v, "v", k.shape, io, dev)
+    _chk(slots, "slots", (T,), _module.int64, dev)
+    pages, page = _chk_cache(k_cache, v_cache, k.shape[1], k.shape[2], io, dev)
+    qo = _out_like(out, "out", q)
+    _run(dev, lib().flare_qk_norm_rotary_cache, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs, _ptr(k),
+         ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), eps, _ptr(slots), _ptr(qo), _ptr(k_cache), _ptr(v_cache), pages,
+         page)
+    return qo
+
+
+def cache_fp4(num_pages, heads, page, d, device="cuda"):
+    """(codes, scales) of an empty cache in 4 bits, all zeros: codes uint8
+    [num_pages, heads, page, d / 2], scales uint8 [num_pages, heads, d / 32,
+    page].  A value is its code (0, 1/2, 1, 3/2, 2, 3, 4, 6 and a sign) times
+    2^(scale - 127), the scale that of its 32 channels."""
+    torch = _torch()
+    if d < 32 or d % 32:
+        _fail("a cache in 4 bits has groups of 32 channels, not %d" % d, 4)
+    return (torch.zeros((num_pages, heads, page, d // 2), dtype=torch.uint8, device=device),
+            torch.zeros((num_pages, heads, d // 32, page), dtype=torch.uint8, device=device))
+
+
+def _chk_cache_fp4(cache, name, heads, d, dev):
+    """(codes, scales) of a cache in 4 bits; returns (num_pages, page)."""
+    if not isinstance(cache, (tuple, list)) or len(cache) != 2 or cache[0] is None or cache[0].dim() != 4:
+        _fail("%s must be (codes [num_pages, heads, page, d / 2], scales [num_pages, heads, d / 32, page])" % name)
+    codes, scales = cache
+    pages, page = codes.shape[0], codes.shape[2]
+    if d % 32:
+        _fail("a cache in 4 bits has groups of 32 channels, not %d" % d, 4)
+    if max(heads, page) > 0x7FFFFFFF:
+        _i32(heads, "cache heads"), _i32(page, "page")
+    _chk(codes, name + " codes", (pages, heads, page, d // 2), _module.uint8, dev)
+    _chk(scales, name + " scales", (pages, heads, d // 32, page), _module.uint8, dev)
+    return pages, page
+
+
+def _chk_caches_fp4(k_cache, v_cache, heads, d, dev):
+    pages, page = _chk_cache_fp4(k_cache, "k_cache", heads, d, dev)
+    if _chk_cache_fp4(v_cache, "v_cache", heads, d, dev) != (pages, page):
+        _fail("k_cache and v_cache have pages of different number or size")
+    return pages, page
+
+
+def qk_norm_rotary_cache_fp4(positions, freqs, q, k, v, slots, k_cache, v_cache, q_weight=None, k_weight=None, eps=1e-6,
+                             interleaved=False, mscale=1.0, out=None):
+    """qk_norm_rotary_cache into a cache in 4 bits
+    (flare_qk_norm_rotary_cache_fp4): k_cache and v_cache are (codes, scales) as
+    from cache_fp4().  Without weights it is rotary_cache into such a cache."""
+    if k is None or v is None:
+        _fail("k and v are required", 1)
+    T, shp, io, dev, qs, ks = _rotary_inputs(positions, freqs, q, k, interleaved, mscale)
+    _norm_weights(q_weight, k_weight, k, shp.dim, dev)
+    vs = _token_rows(v, "v", k.shape, io, dev)
+    _chk(slots, "slots", (T,), _module.int64, dev)
+    pages, page = _chk_caches_fp4(k_cache, v_cache, k.shape[1], k.shape[2], dev)
+    qo = _out_like(out, "out", q)
+    _run(dev, lib().flare_qk_norm_rotary_cache_fp4, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs,
+         _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), eps, _ptr(slots), _ptr(qo), _ptr(k_cache[0]),
+         _ptr(k_cache[1]), _ptr(v_cache[0]), _ptr(v_cache[1]), pages, page)
+    return qo
+
+
+def cache_fp4_rows(slots, k_cache, v_cache=None, dtype=None, out=None):
+    """Rows of a cache in 4 bits as bf16 (or dtype = float32) values
+    (flare_cache_fp4_rows): [T, heads, d], row t that at slots[t] (int64), zeros
+    for a slot of no page.  Returns (k, v), or k without v_cache; `out` likewise
+    reuses buffers."""
+    torch = _torch()
+    dev = _gpu_device(slots, "slots")
+    io = torch.bfloat16 if dtype is None else dtype
+    if io not in (torch.bfloat16, torch.float32):
+        _fail("cache_fp4_rows gives bfloat16 or float32, not %s" % io, 4)
+    if slots.dim() != 1:
+        _fail("slots must be int64 [T]")
+    T = slots.shape[0]
+    _chk(slots, "slots", (T,), torch.int64, dev)
+    if not isinstance(k_cache, (tuple, list)) or len(k_cache) != 2 or k_cache[0] is None or k_cache[0].dim() != 4:
+        _fail("k_cache must be (codes, scales)")
+    heads, d = k_cache[0].shape[1], 2 * k_cache[0].shape[3]
+    pages, page = _chk_cache_fp4(k_cache, "k_cache", heads, d, dev)
+    if v_cache is not None:
+        _chk_caches_fp4(k_cache, v_cache, heads, d, dev)
+    ko, vo = (None, None) if out is None else out if v_cache is not None else (out, None)
+    ko = _out(ko, "k out", (T, heads, d), io, dev)
+    vo = _out(vo, "v out", (T, heads, d), io, dev) if v_cache is not None else None
+    v_codes, v_scales = (None, None) if v_cache is None else v_cache
+    _run(dev, lib().flare_cache_fp4_rows, T, heads, d, _io(io), _ptr(slots), _ptr(k_cache[0]), _ptr(k_cache[1]),
+         _ptr(v_codes), _ptr(v_scales), pages, page, _ptr(ko), _ptr(vo))
+    return ko if v_cache is None else (ko, vo)
 
 
 # ---------------------------------------------------------------- serving-step tables
@@ -480,8 +647,8 @@ def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=Non
     if max(R, B, Hq, d) > 0x7FFFFFFF:
         _fail("q: shape %s" % (tuple(q.shape),), 4)
     _chk(q, "q", (R, B, Hq, d), torch.bfloat16, dev)
-    if k_cache is None or k_cache.dim() != 4:
-        _fail("k_cache must be [num_pages, Hk, page, d]")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _fail("k_cache must be a tensor [num_pages, Hk, page, d]")
     Hk = k_cache.shape[1]
     pages, page = _chk_cache(k_cache, v_cache, Hk, d, torch.bfloat16, dev)
     if block_table is None or block_table.dim() != 2:

@@ -679,6 +679,85 @@ flare_status flare_rotary_cache(int64_t tokens, const flare_rotary_shape *shape,
                                 void *q_out, void *k_cache, void *v_cache,
                                 int64_t num_pages, int32_t page, void *stream);
 
+/* The norms of queries and keys for each head and their rotary positions, in
+ * one pass:
+ *   n = x / sqrt(mean x^2 + eps) * weight        per (token, head) row
+ *   y = n, its first 2 * half channels turned as by flare_rotary
+ * arguments as flare_rotary's, and
+ *   q_weight, k_weight  fp32 [dim], the same for all heads; NULL: that side is
+ *              turned, not normed
+ * Requirements as flare_rotary's. */
+flare_status flare_qk_norm_rotary(int64_t tokens,
+                                  const flare_rotary_shape *shape,
+                                  const int32_t *positions, const double *freqs,
+                                  const void *q, int64_t q_stride,
+                                  const void *k, int64_t k_stride,
+                                  const float *q_weight, const float *k_weight,
+                                  float eps, void *q_out, void *k_out,
+                                  void *stream);
+
+/* Reverse mode: the forward's inputs, and dq_out, dk_out io [tokens, heads, dim]
+ * with token strides, the gradients of its outputs; writes dq, dk (io, packed)
+ * and dq_weight, dk_weight (fp32 [dim]) where the forward had weights (else
+ * NULL).  workspace: 256-byte aligned,
+ * flare_qk_norm_rotary_bwd_workspace_size bytes (partial weight sums, added in
+ * a fixed order: results are run-to-run identical); NULL without weights. */
+size_t flare_qk_norm_rotary_bwd_workspace_size(int64_t tokens, int32_t dim);
+flare_status flare_qk_norm_rotary_bwd(
+    int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+    const double *freqs, const void *q, int64_t q_stride, const void *k,
+    int64_t k_stride, const float *q_weight, const float *k_weight, float eps,
+    const void *dq_out, int64_t dq_out_stride, const void *dk_out,
+    int64_t dk_out_stride, void *dq, void *dk, float *dq_weight,
+    float *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The serving form: q normed and turned to q_out, k normed and turned and v
+ * copied into the pages of the cache, slots and caches as flare_rotary_cache's. */
+flare_status flare_qk_norm_rotary_cache(
+    int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+    const double *freqs, const void *q, int64_t q_stride, const void *k,
+    int64_t k_stride, const void *v, int64_t v_stride, const float *q_weight,
+    const float *k_weight, float eps, const int64_t *slots, void *q_out,
+    void *k_cache, void *v_cache, int64_t num_pages, int32_t page, void *stream);
+
+/* ---- a cache in 4 bits ----
+ * A row's channels lie in groups of 32 that share a scale.  A value is
+ *   c * 2^(byte - 127),  c one of 0, 1/2, 1, 3/2, 2, 3, 4, 6 with a sign
+ * (codes 0 to 7; 8 is the sign), which a bf16 holds exactly.
+ *   codes      uint8 [num_pages, heads, page, dim / 2]: the lower four bits of
+ *              a byte are the even channel's
+ *   scales     uint8 [num_pages, heads, dim / 32, page]; 255: the group is NaN
+ * Written values go to the nearest code, halfway to the even one.  The scale is
+ * the exponent of the group's largest magnitude less two, and one more where
+ * that magnitude is above 7 units: 7 is cut to 6, which is half a step there.
+ * Bytes written are 1 to 252 (larger magnitudes are cut to 6 * 2^125), or 255
+ * for a group with an infinity or NaN.  codes are 16-byte aligned.
+ *
+ * flare_qk_norm_rotary_cache into such a cache.  k is computed in 64 bits and
+ * rounded once.  dim must be a multiple of 32. */
+flare_status flare_qk_norm_rotary_cache_fp4(
+    int64_t tokens, const flare_rotary_shape *shape, const int32_t *positions,
+    const double *freqs, const void *q, int64_t q_stride, const void *k,
+    int64_t k_stride, const void *v, int64_t v_stride, const float *q_weight,
+    const float *k_weight, float eps, const int64_t *slots, void *q_out,
+    uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales,
+    int64_t num_pages, int32_t page, void *stream);
+
+/* Rows of such a cache as io values (a request that moves to a cache of another
+ * type; a prefix that is looked at): row t is that at slots[t]; zeros for a slot
+ * outside [0, num_pages * page).  The same slot may occur more than once.
+ *   k_out, v_out  io [rows, heads, dim], 16-byte aligned; v_out NULL: keys
+ *              alone, and the v pointers are ignored
+ * rows < 2^31; heads <= 65536; dim a multiple of 32, at most 1024. */
+flare_status flare_cache_fp4_rows(int64_t rows, int32_t heads, int32_t dim,
+                                  int32_t io_dtype, const int64_t *slots,
+                                  const uint8_t *k_codes,
+                                  const uint8_t *k_scales,
+                                  const uint8_t *v_codes,
+                                  const uint8_t *v_scales, int64_t num_pages,
+                                  int32_t page, void *k_out, void *v_out,
+                                  void *stream);
+
 /* The tables of a serving step, from lengths that stay on the device.  Request
  * r holds seq_lens[r] tokens in the cache and adds new_lens[r]; its pages are
  * block_table[r][0 .. ceil(seq_lens[r] / page)).  The pages it opens are taken,
@@ -789,6 +868,8 @@ int32_t flare_version(void);
  * then names the forward's output pass) and "gdn_bwd_scan_kernel" (the
  * reverse recurrence); "norm_kernel", "norm_bwd_kernel" (both launches),
  * "rotary_kernel", "step_tables_kernel", "block_attention_kernel" (all launches
+ * of a call), "qk_norm_rotary_kernel", "qk_norm_rotary_bwd_kernel" (both
+ * launches), "cache_fp4_rows_kernel", "block_attention_fp4_kernel" (all launches
  * of a call).
  * flare_timing_enable(1) turns it on (events are created lazily, host side
  * only; no device memory is allocated), (0) off.  Returns the previous state.
