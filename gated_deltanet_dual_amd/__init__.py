@@ -21,7 +21,7 @@ __all__ = ["Varlen", "GDNShape", "FlareError", "lib", "gdn_dual_fwd", "gdn_dual_
            "qkv_prologue_bwd", "qkv_prologue_bwd_workspace_bytes", "chunk_size", "ckpt_slots", "EVAL", "COMMIT",
            "QK_L2NORM", "F32", "BF16",
            "gated_norm", "gated_norm_bwd", "residual_norm", "residual_norm_bwd", "rotary_frequencies", "rotary",
-           "rotary_cache", "qk_norm_rotary", "qk_norm_rotary_bwd", "qk_norm_rotary_cache", "qk_norm_rotary_cache_fp4", "cache_fp4", "cache_fp4_rows", "step_tables", "block_attention", "LINEAR", "SILU", "SIGMOID"]
+           "rotary_cache", "qk_norm_rotary", "qk_norm_rotary_bwd", "qk_norm_rotary_cache", "qk_norm_rotary_cache_fp4", "cache_fp4", "cache_fp4_rows", "step_tables", "block_attention", "block_attention_fp4", "LINEAR", "SILU", "SIGMOID"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflare_gdn.so")
@@ -916,7 +916,8 @@ def timing_reset() -> None:
 
 # the operators around the GDN step
 from .layer import (LINEAR, SIGMOID, SILU, TABLES_BAD_LENGTH, TABLES_NO_PAGES, TABLES_OK,  # noqa: E402
-                    TABLES_TOO_LONG, TABLES_TOO_MANY_TOKENS, AttentionShape, RotaryShape, block_attention,
+                    TABLES_TOO_LONG, TABLES_TOO_MANY_TOKENS, AttentionShape, RotaryShape, block_attention, block_attention_fp4,
+                    block_attention_fp4_workspace_bytes,
                     block_attention_workspace_bytes, cache_fp4, cache_fp4_rows, gated_norm, gated_norm_bwd,
                     gated_norm_bwd_workspace_bytes, qk_norm_rotary, qk_norm_rotary_bwd,
                     qk_norm_rotary_bwd_workspace_bytes, qk_norm_rotary_cache, qk_norm_rotary_cache_fp4, residual_norm, residual_norm_bwd, residual_norm_bwd_workspace_bytes, rotary, rotary_cache,

@@ -353,6 +353,37 @@ flare_status flare_step_tables(int32_t num_req, const int32_t *seq_lens, const i
   return hip_status(launch_step_tables(a, (hipStream_t)stream), "step_tables launch");
 }
 
+// What both attentions check after the shape, but for the caches.
+static flare_status check_attention_call(int32_t num_req, const flare_attention_shape *shape, const void *q,
+                                         int64_t num_pages, const int32_t *block_table, int32_t max_pages,
+                                         const int32_t *seq_lens, int32_t max_seq_len, const int32_t *prefix_table,
+                                         int32_t prefix_len, const void *o) {
+  if (num_pages < 0 || num_pages > INT32_MAX || max_pages < 0)
+    return fail(FLARE_ERR_SHAPE, "block_attention: num_pages or max_pages");
+  if (max_seq_len > (int64_t)max_pages * shape->page)
+    return fail(FLARE_ERR_SHAPE, "block_attention: max_seq_len %d beyond the table's %d pages of %d", max_seq_len,
+                max_pages, shape->page);
+  if ((max_seq_len > 0 || prefix_len > 0) && num_pages == 0)
+    return fail(FLARE_ERR_SHAPE, "block_attention: keys, but a cache of no pages");
+  if (num_req > 0 && (!q || !o || !seq_lens || (max_seq_len > 0 && !block_table) || (prefix_len > 0 && !prefix_table)))
+    return fail(FLARE_ERR_NULL, "block_attention: a required pointer is NULL");
+  return FLARE_OK;
+}
+
+// The workspace and the launch's size for a plan.
+static flare_status check_attention_plan(const BlockAttnArgs &a, const AttnPlan &p, const void *workspace,
+                                         size_t workspace_bytes) {
+  const size_t need = block_attention_workspace_bytes(a, p);
+  if (need > 0) {
+    const flare_status st = check_workspace(workspace, workspace_bytes, need);
+    if (st != FLARE_OK) return st;
+  }
+  if (attn_launch_blocks(p) > kMaxBlocks)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: %lld workgroups, at most %lld", (long long)attn_launch_blocks(p),
+                (long long)kMaxBlocks);
+  return FLARE_OK;
+}
+
 size_t flare_block_attention_workspace_size(int32_t num_req, const flare_attention_shape *shape, int32_t max_seq_len,
                                             int32_t prefix_len) {
   if (check_attention_shape(num_req, shape, max_seq_len, prefix_len) != FLARE_OK) return 0;
@@ -367,30 +398,17 @@ flare_status flare_block_attention(int32_t num_req, const flare_attention_shape 
                                    float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   clear_error();
   flare_status st = check_attention_shape(num_req, shape, max_seq_len, prefix_len);
-  if (st != FLARE_OK) return st;
-  if (num_pages < 0 || num_pages > INT32_MAX || max_pages < 0)
-    return fail(FLARE_ERR_SHAPE, "block_attention: num_pages or max_pages");
-  if (max_seq_len > (int64_t)max_pages * shape->page)
-    return fail(FLARE_ERR_SHAPE, "block_attention: max_seq_len %d beyond the table's %d pages of %d", max_seq_len,
-                max_pages, shape->page);
-  if ((max_seq_len > 0 || prefix_len > 0) && num_pages == 0)
-    return fail(FLARE_ERR_SHAPE, "block_attention: keys, but a cache of no pages");
-  if (num_req == 0) return FLARE_OK;
-  if (!q || !o || !seq_lens || (max_seq_len > 0 && !block_table) || (prefix_len > 0 && !prefix_table) ||
-      (num_pages > 0 && (!k_cache || !v_cache)))
-    return fail(FLARE_ERR_NULL, "block_attention: a required pointer is NULL");
+  if (st == FLARE_OK)
+    st = check_attention_call(num_req, shape, q, num_pages, block_table, max_pages, seq_lens, max_seq_len, prefix_table,
+                              prefix_len, o);
+  if (st != FLARE_OK || num_req == 0) return st;
+  if (num_pages > 0 && (!k_cache || !v_cache)) return fail(FLARE_ERR_NULL, "block_attention: a required pointer is NULL");
   if ((((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)o) & 15u) != 0)
     return fail(FLARE_ERR_ALIGN, "block_attention: q, the caches and o must be 16-byte aligned");
   BlockAttnArgs a = attention_args(num_req, shape, max_seq_len, prefix_len);
   const AttnPlan p = attn_plan(a);
-  const size_t need = block_attention_workspace_bytes(a, p);
-  if (need > 0) {
-    st = check_workspace(workspace, workspace_bytes, need);
-    if (st != FLARE_OK) return st;
-  }
-  if (attn_launch_blocks(p) > kMaxBlocks)
-    return fail(FLARE_ERR_UNSUPPORTED, "block_attention: %lld workgroups, at most %lld", (long long)attn_launch_blocks(p),
-                (long long)kMaxBlocks);
+  st = check_attention_plan(a, p, workspace, workspace_bytes);
+  if (st != FLARE_OK) return st;
   a.num_pages = num_pages;
   a.max_pages = max_pages;
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
@@ -398,6 +416,45 @@ flare_status flare_block_attention(int32_t num_req, const flare_attention_shape 
   a.o = o; a.lse = lse;
   a.part = reinterpret_cast<float *>(workspace);
   return hip_status(launch_block_attention(a, p, (hipStream_t)stream), "block_attention launch");
+}
+
+size_t flare_block_attention_fp4_workspace_size(int32_t num_req, const flare_attention_shape *shape,
+                                                int32_t max_seq_len, int32_t prefix_len) {
+  if (check_attention_fp4_shape(num_req, shape, max_seq_len, prefix_len) != FLARE_OK) return 0;
+  const BlockAttnArgs a = attention_args(num_req, shape, max_seq_len, prefix_len);
+  return block_attention_workspace_bytes(a, attn_fp4_plan(a));
+}
+
+flare_status flare_block_attention_fp4(int32_t num_req, const flare_attention_shape *shape, const void *q,
+                                       const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                                       const uint8_t *v_scales, int64_t num_pages, const int32_t *block_table,
+                                       int32_t max_pages, const int32_t *seq_lens, int32_t max_seq_len,
+                                       const int32_t *prefix_table, int32_t prefix_len, void *o, float *lse,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+  clear_error();
+  flare_status st = check_attention_fp4_shape(num_req, shape, max_seq_len, prefix_len);
+  if (st == FLARE_OK)
+    st = check_attention_call(num_req, shape, q, num_pages, block_table, max_pages, seq_lens, max_seq_len, prefix_table,
+                              prefix_len, o);
+  if (st != FLARE_OK || num_req == 0) return st;
+  const Cache4 k4{const_cast<uint8_t *>(k_codes), const_cast<uint8_t *>(k_scales)};
+  const Cache4 v4{const_cast<uint8_t *>(v_codes), const_cast<uint8_t *>(v_scales)};
+  st = check_cache4("block_attention_fp4", shape->head_dim, num_pages, shape->page, k4, v4);
+  if (st != FLARE_OK) return st;
+  if ((((uintptr_t)q | (uintptr_t)o) & 15u) != 0 || (((uintptr_t)k_scales | (uintptr_t)v_scales) & 3u) != 0)
+    return fail(FLARE_ERR_ALIGN, "block_attention_fp4: q and o must be 16-byte, the scales 4-byte aligned");
+  BlockAttnFp4Args b{attention_args(num_req, shape, max_seq_len, prefix_len), k_scales, v_scales};
+  BlockAttnArgs &a = b.a;
+  const AttnPlan p = attn_fp4_plan(a);
+  st = check_attention_plan(a, p, workspace, workspace_bytes);
+  if (st != FLARE_OK) return st;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.q = q; a.k_cache = k_codes; a.v_cache = v_codes;
+  a.block_table = block_table; a.seq_lens = seq_lens; a.prefix_table = prefix_table;
+  a.o = o; a.lse = lse;
+  a.part = reinterpret_cast<float *>(workspace);
+  return hip_status(launch_block_attention_fp4(b, p, (hipStream_t)stream), "block_attention_fp4 launch");
 }
 
 }  // extern "C"

@@ -87,6 +87,69 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   return p;
 }
 
+AttnPlan attn_fp4_plan(const BlockAttnArgs &a) {
+  AttnPlan p{};
+  while ((1 << p.page_shift) < a.page) ++p.page_shift;
+  const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
+  const int64_t all_rows = rows * a.num_req;
+  const int most = a.dim == 256 ? 2 : 4;
+  auto tiles = [&](int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : most; };
+  p.own_tiles = tiles(rows);
+  p.prefix_tiles = a.prefix_len > 0 ? tiles(all_rows) : p.own_tiles;
+  p.own_groups = (int)ceil_div(rows, 16 * p.own_tiles);
+  p.prefix_groups = (int)ceil_div(all_rows, 16 * p.prefix_tiles);
+
+  // The lengths of the parts: the shortest time, in nanoseconds.
+  constexpr int64_t kSlots = 512, kStart = 2500, kLongest = 4096;
+  auto key_cost = [&](int t) { return (t == 1 ? 5 : t == 2 ? 8 : 13) * (int64_t)a.dim / 128 + 1; };
+  const int64_t own_key = key_cost(p.own_tiles), prefix_key = key_cost(p.prefix_tiles);
+  const int64_t join = all_rows * a.kv_heads * a.dim / 625 + 40;
+  const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
+  p.prefix_chunk = p.own_chunk = (int)kLongest;
+  int64_t best = INT64_MAX, own_top = kLongest;
+  while (own_top > 128 && own_top / 2 >= a.max_seq_len) own_top /= 2;
+  const int64_t least = ceil_div(a.prefix_len, kLongest), parts_most = ceil_div(a.prefix_len, 128);
+  for (int64_t n = least; n <= parts_most; n += 1 + n / 4) {
+    const int64_t chunk = n > 0 ? ceil_div(ceil_div(a.prefix_len, n), 128) * 128 : kLongest;
+    const int64_t parts = ceil_div(a.prefix_len, chunk), units8 = ceil_div(parts * a.kv_heads, 8) * p.prefix_groups;
+    const int64_t prefix_time = chunk * prefix_key + kStart, prefix_rounds = ceil_div(units8, kSlots / 8) * prefix_time;
+    for (int64_t c = own_top; c >= 128; c /= 2) {
+      const int64_t own_parts = ceil_div(a.max_seq_len, c);
+      const int64_t own_time = (c < a.max_seq_len ? c : a.max_seq_len) * own_key + kStart;
+      int64_t cost = (8 * units8 * prefix_time + units * own_parts * own_time) / kSlots;
+      const int64_t own_rounds = ceil_div(units * own_parts, kSlots) * own_time;
+      if (parts > 0 && cost < prefix_rounds) cost = prefix_rounds;
+      if (cost < own_rounds) cost = own_rounds;
+      if (parts + own_parts > 1) cost += (parts + own_parts) * join + kStart;
+      if (cost < best) {
+        best = cost;
+        p.prefix_chunk = (int)chunk;
+        p.prefix_parts = (int)parts;
+        p.own_chunk = (int)c;
+        p.own_parts = (int)own_parts;
+      }
+    }
+  }
+  p.prefix_blocks = ceil_div((int64_t)p.prefix_parts * a.kv_heads, 8) * 8 * p.prefix_groups;
+  // a short prefix is passed by every request before its own keys, in one part
+  if (a.prefix_len > 0 && ceil_div(a.prefix_len, 32) + ceil_div(a.max_seq_len, 32) <= kLongest / 32) {
+    const int64_t together = ceil_div(units, kSlots) * ((a.prefix_len + a.max_seq_len) * own_key + kStart);
+    if (together <= best) {
+      p.merged = 1;
+      p.prefix_tiles = p.own_tiles;
+      p.prefix_parts = 0;
+      p.prefix_blocks = 0;
+      p.own_parts = 1;
+      p.own_chunk = (int)kLongest;
+    }
+  }
+  if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
+  p.own_blocks = units * p.own_parts;
+  p.prefix_runs = (int)ceil_div(p.prefix_blocks, 8 * kOctets);
+  p.own_runs = (int)ceil_div(p.own_blocks, 8 * kOctets);
+  return p;
+}
+
 int64_t attn_launch_blocks(const AttnPlan &p) {
   const int64_t run = 8 * kOctets;
   return (ceil_div(p.prefix_blocks, run) + ceil_div(p.own_blocks, run)) * run;
@@ -278,6 +341,15 @@ flare_status check_attention_shape(int32_t num_req, const flare_attention_shape 
     return fail(FLARE_ERR_UNSUPPORTED, "block_attention: at most 2^31 - 8193 keys");
   if ((int64_t)num_req * s->block > INT32_MAX / 64 / s->q_heads)
     return fail(FLARE_ERR_UNSUPPORTED, "block_attention: num_req * block * q_heads beyond 2^25");
+  return FLARE_OK;
+}
+
+flare_status check_attention_fp4_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
+                                       int32_t prefix_len) {
+  const flare_status st = check_attention_shape(num_req, s, max_seq_len, prefix_len);
+  if (st != FLARE_OK) return st;
+  // a lane's place among a page's scales is kept in 32 bits
+  if (s->page > 1 << 24) return fail(FLARE_ERR_UNSUPPORTED, "block_attention_fp4: page %d, at most 2^24", s->page);
   return FLARE_OK;
 }
 

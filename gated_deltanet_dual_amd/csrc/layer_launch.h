@@ -20,6 +20,9 @@ hipError_t launch_qk_norm_rotary_bwd(const QkNormArgs &a, hipStream_t st);
 hipError_t launch_norm_partials(const float *part, int blocks, int dim, float *const (&out)[3], hipStream_t st);
 hipError_t launch_cache_fp4_rows(const Cache4Rows &a, hipStream_t st);
 hipError_t launch_step_tables(const StepTablesArgs &a, hipStream_t st);
+// joins a call's parts; nothing where it has only one
+hipError_t launch_attn_join(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st);
+hipError_t launch_block_attention_fp4(const BlockAttnFp4Args &a, const AttnPlan &p, hipStream_t st);
 hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st);
 
 }  // namespace flare

@@ -135,6 +135,11 @@ struct BlockAttnArgs {
   float *part;  // workspace
 };
 
+struct BlockAttnFp4Args {
+  BlockAttnArgs a;  // its caches are the codes
+  const uint8_t *k_scales, *v_scales;
+};
+
 // ---------------------------------------------------------------- host checks
 // A launch dimension holds fewer than 2^32 work items: so many workgroups of 256.
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 32) / 256 - 1;
@@ -168,6 +173,8 @@ flare_status check_step_tables(const StepTablesArgs &a);
 // shape alone (for the size query), then everything
 flare_status check_attention_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
                                    int32_t prefix_len);
+flare_status check_attention_fp4_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
+                                       int32_t prefix_len);
 BlockAttnArgs attention_args(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
                              int32_t prefix_len);
 

@@ -71,10 +71,13 @@ def declare(L):
     L.flare_block_attention_workspace_size.argtypes = [I32, AP, I32, I32]
     L.flare_block_attention_workspace_size.restype = SZ
     L.flare_block_attention.argtypes = [I32, AP, P, P, P, I64, P, I32, P, I32, P, I32, P, P, P, SZ, P]
+    L.flare_block_attention_fp4_workspace_size.argtypes = [I32, AP, I32, I32]
+    L.flare_block_attention_fp4_workspace_size.restype = SZ
+    L.flare_block_attention_fp4.argtypes = [I32, AP, P, P, P, P, P, I64, P, I32, P, I32, P, I32, P, P, P, SZ, P]
     for name in ("flare_gated_norm", "flare_gated_norm_bwd", "flare_residual_norm", "flare_residual_norm_bwd",
                  "flare_rotary", "flare_rotary_cache", "flare_qk_norm_rotary", "flare_qk_norm_rotary_bwd",
                  "flare_qk_norm_rotary_cache", "flare_qk_norm_rotary_cache_fp4", "flare_cache_fp4_rows",
-                 "flare_step_tables", "flare_block_attention"):
+                 "flare_step_tables", "flare_block_attention", "flare_block_attention_fp4"):
         getattr(L, name).restype = ctypes.c_int
 
 
@@ -617,40 +620,45 @@ def step_tables(seq_lens, new_lens, block_table, free_pages, pages_used, page, m
 
 # ---------------------------------------------------------------- block attention
 
-def block_attention_workspace_bytes(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len) -> int:
-    """flare_block_attention_workspace_size (bf16)."""
+def _attention_shape(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len):
     sizes = (("R", R), ("B", B), ("q_heads", q_heads), ("kv_heads", kv_heads), ("d", d), ("page", page),
              ("max_seq_len", max_seq_len), ("prefix_len", prefix_len))
     R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len = (_i32(n, name) for name, n in sizes)
-    shp = AttentionShape(B, q_heads, kv_heads, d, page, BF16, 0, 0.0)
-    return int(lib().flare_block_attention_workspace_size(R, ctypes.byref(shp), max_seq_len, prefix_len))
+    return R, ctypes.byref(AttentionShape(B, q_heads, kv_heads, d, page, BF16, 0, 0.0)), max_seq_len, prefix_len
 
 
-def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=None, prefix_len=0, causal=False,
-                    scale=0.0, max_seq_len=None, out=None, want_lse=False, lse=None, workspace=None):
-    """The block step of a softmax layer (flare_block_attention): q [R, B, Hq, d]
-    bf16 over a prefix of prefix_len keys shared by all requests (pages
-    prefix_table) and each request's own seq_lens[r] keys (pages block_table[r]),
-    the block's included.  causal=False: every query sees all of them;
-    causal=True: query b sees the prefix and the first seq_lens[r] - (B - 1 - b)
-    own keys.  Caches [num_pages, Hk, page, d] bf16.  max_seq_len bounds seq_lens
-    (default: what the table holds), and the work is cut by it: lengths beyond it
-    are cut.  Returns o, or
-    (o, lse) with want_lse or `lse` (fp32 [R, B, Hq])."""
+def block_attention_workspace_bytes(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len) -> int:
+    """flare_block_attention_workspace_size (bf16)."""
+    return int(lib().flare_block_attention_workspace_size(
+        *_attention_shape(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len)))
+
+
+def block_attention_fp4_workspace_bytes(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len) -> int:
+    """flare_block_attention_fp4_workspace_size."""
+    return int(lib().flare_block_attention_fp4_workspace_size(
+        *_attention_shape(R, B, q_heads, kv_heads, d, page, max_seq_len, prefix_len)))
+
+
+def _attention_inputs(q, what):
+    """(device, R, B, Hq, d) of an attention's queries."""
     torch = _torch()
     dev = _gpu_device(q, "q")
     if q.dim() != 4:
         _fail("q must be [R, B, Hq, d], got shape %s" % (tuple(q.shape),))
     if q.dtype != torch.bfloat16:
-        _fail("block_attention is built for bfloat16, got %s" % q.dtype, 4)
+        _fail("%s is built for bfloat16, got %s" % (what, q.dtype), 4)
     R, B, Hq, d = q.shape
     if max(R, B, Hq, d) > 0x7FFFFFFF:
         _fail("q: shape %s" % (tuple(q.shape),), 4)
     _chk(q, "q", (R, B, Hq, d), torch.bfloat16, dev)
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        _fail("k_cache must be a tensor [num_pages, Hk, page, d]")
-    Hk = k_cache.shape[1]
-    pages, page = _chk_cache(k_cache, v_cache, Hk, d, torch.bfloat16, dev)
+    return dev, R, B, Hq, d
+
+
+def _attend(size, attend, dev, q, caches, Hk, pages, page, block_table, seq_lens, prefix_table, prefix_len, causal, scale,
+            max_seq_len, out, want_lse, lse, workspace):
+    """The checks and the call that both attentions share."""
+    torch = _module
+    R, B, Hq, d = q.shape
     if block_table is None or block_table.dim() != 2:
         _fail("block_table must be int32 [R, max_pages]")
     wide = block_table.shape[1]
@@ -668,10 +676,50 @@ def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=Non
     o = _out_like(out, "out", q)
     if lse is not None or want_lse:
         lse = _out(lse, "lse", (R, B, Hq), torch.float32, dev)
-    need = int(lib().flare_block_attention_workspace_size(R, ctypes.byref(shp), most, n))
+    need = int(size(R, ctypes.byref(shp), most, n))
     if need > 0:
         workspace = _workspace(workspace, need, dev)
-    _run(dev, lib().flare_block_attention, R, ctypes.byref(shp), _ptr(q), _ptr(k_cache), _ptr(v_cache), pages,
-         _ptr(block_table), wide, _ptr(seq_lens), most, _ptr(prefix_table) if n > 0 else None, n, _ptr(o), _ptr(lse),
-         _ptr(workspace), 0 if workspace is None else workspace.numel())
+    _run(dev, attend, R, ctypes.byref(shp), _ptr(q), *caches, pages, _ptr(block_table), wide, _ptr(seq_lens), most,
+         _ptr(prefix_table) if n > 0 else None, n, _ptr(o), _ptr(lse), _ptr(workspace),
+         0 if workspace is None else workspace.numel())
     return o if lse is None else (o, lse)
+
+
+def block_attention(q, k_cache, v_cache, block_table, seq_lens, prefix_table=None, prefix_len=0, causal=False,
+                    scale=0.0, max_seq_len=None, out=None, want_lse=False, lse=None, workspace=None):
+    """The block step of a softmax layer (flare_block_attention): q [R, B, Hq, d]
+    bf16 over a prefix of prefix_len keys shared by all requests (pages
+    prefix_table) and each request's own seq_lens[r] keys (pages block_table[r]),
+    the block's included.  causal=False: every query sees all of them;
+    causal=True: query b sees the prefix and the first seq_lens[r] - (B - 1 - b)
+    own keys.  Caches [num_pages, Hk, page, d] bf16.  max_seq_len bounds seq_lens
+    (default: what the table holds), and the work is cut by it: lengths beyond it
+    are cut.  Returns o, or
+    (o, lse) with want_lse or `lse` (fp32 [R, B, Hq])."""
+    dev, R, B, Hq, d = _attention_inputs(q, "block_attention")
+    if not isinstance(k_cache, _module.Tensor) or k_cache.dim() != 4:
+        _fail("k_cache must be a tensor [num_pages, Hk, page, d]")
+    Hk = k_cache.shape[1]
+    pages, page = _chk_cache(k_cache, v_cache, Hk, d, _module.bfloat16, dev)
+    L = lib()
+    return _attend(L.flare_block_attention_workspace_size, L.flare_block_attention, dev, q, (_ptr(k_cache), _ptr(v_cache)),
+                   Hk, pages, page, block_table, seq_lens, prefix_table, prefix_len, causal, scale, max_seq_len, out,
+                   want_lse, lse, workspace)
+
+
+def block_attention_fp4(q, k_cache, v_cache, block_table, seq_lens, prefix_table=None, prefix_len=0, causal=False,
+                        scale=0.0, max_seq_len=None, out=None, want_lse=False, lse=None, workspace=None):
+    """block_attention over a cache in 4 bits (flare_block_attention_fp4): k_cache
+    and v_cache are (codes, scales) as from cache_fp4(), written by
+    qk_norm_rotary_cache_fp4; the other arguments and the result are
+    block_attention's."""
+    dev, R, B, Hq, d = _attention_inputs(q, "block_attention_fp4")
+    if not isinstance(k_cache, (tuple, list)) or len(k_cache) != 2 or k_cache[0] is None or k_cache[0].dim() != 4:
+        _fail("k_cache must be (codes, scales)")
+    Hk = k_cache[0].shape[1]
+    pages, page = _chk_caches_fp4(k_cache, v_cache, Hk, d, dev)
+    L = lib()
+    caches = (_ptr(k_cache[0]), _ptr(k_cache[1]), _ptr(v_cache[0]), _ptr(v_cache[1]))
+    return _attend(L.flare_block_attention_fp4_workspace_size, L.flare_block_attention_fp4, dev, q, caches, Hk, pages, page,
+                   block_table, seq_lens, prefix_table, prefix_len, causal, scale, max_seq_len, out, want_lse, lse,
+                   workspace)

@@ -841,6 +841,24 @@ flare_status flare_block_attention(
     int32_t max_seq_len, const int32_t *prefix_table, int32_t prefix_len,
     void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/* The block step over a cache in 4 bits: as flare_block_attention, with the caches
+ * as written by flare_qk_norm_rotary_cache_fp4 (head_dim and page are theirs).
+ * The scores are those of the values that the codes stand for.  Requirements as
+ * flare_block_attention's; page at most 2^24; codes 16-byte, scales 4-byte
+ * aligned.  Any byte may stand in codes and scales: values beyond fp32 are
+ * infinities, scales of 255 NaN, and both reach only queries that see them.
+ * workspace: flare_block_attention_fp4_workspace_size bytes. */
+size_t flare_block_attention_fp4_workspace_size(
+    int32_t num_req, const flare_attention_shape *shape, int32_t max_seq_len,
+    int32_t prefix_len);
+flare_status flare_block_attention_fp4(
+    int32_t num_req, const flare_attention_shape *shape, const void *q,
+    const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+    const uint8_t *v_scales, int64_t num_pages, const int32_t *block_table,
+    int32_t max_pages, const int32_t *seq_lens, int32_t max_seq_len,
+    const int32_t *prefix_table, int32_t prefix_len, void *o, float *lse,
+    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Thread-local message for the last non-OK status; "" if none. */
 const char *flare_last_error(void);
 

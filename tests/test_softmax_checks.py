@@ -133,3 +133,50 @@ def test_cache_shapes():
     big = (torch.empty((0, 1, 2 ** 32 + 16, 16), dtype=torch.uint8), torch.empty((0, 1, 1, 2 ** 32 + 16), dtype=torch.uint8))
     with pytest.raises(g.FlareError, match="beyond 32 bits"):
         layer._chk_cache_fp4(big, "k_cache", 1, 32, CPU)
+
+
+def attention4(L, R=2, block=4, qh=8, kh=2, d=128, page=64, io=g.BF16, causal=0, scale=0.0, q=FAKE, kc=FAKE, ks=FAKE, vc=FAKE,
+               vs=FAKE, pages=100, bt=FAKE, wide=8, lens=FAKE, most=512, pt=FAKE, n=5000, o=FAKE, ws=FAKE & ~255, nbytes=1 << 40):
+    s = g.AttentionShape(block, qh, kh, d, page, io, causal, scale)
+    return L.flare_block_attention_fp4(R, ctypes.byref(s), q, kc, ks, vc, vs, pages, bt, wide, lens, most, pt, n, o, None, ws,
+                                       nbytes, None)
+
+
+def test_attention(L):
+    for bad in (dict(R=-1), dict(block=0), dict(qh=0), dict(kh=0), dict(kh=3), dict(most=-1), dict(n=-1), dict(pages=-1),
+                dict(most=513), dict(pages=0), dict(scale=math.inf), dict(scale=math.nan), dict(pages=2 ** 31)):
+        assert attention4(L, **bad) == 2, bad
+    for bad in (dict(d=16), dict(d=96), dict(page=8), dict(page=48), dict(io=g.F32), dict(causal=2), dict(R=2 ** 24),
+                dict(n=2 ** 31 - 1), dict(page=2 ** 25)):
+        assert attention4(L, **bad) == 4, bad
+    for bad in ("q", "bt", "lens", "pt", "kc", "ks", "vc", "vs", "o"):
+        assert attention4(L, **{bad: None}) == 1, bad
+    assert attention4(L, q=FAKE + 8) == 3 and attention4(L, kc=FAKE + 8) == 3 and attention4(L, vs=FAKE + 2) == 3
+    need = g.block_attention_fp4_workspace_bytes(2, 4, 8, 2, 128, 64, 512, 5000)
+    assert need > 0 and attention4(L, nbytes=need - 1) == 5 and attention4(L, ws=None) == 5
+    assert attention4(L, ws=(FAKE & ~255) + 64) == 5
+    assert attention4(L, R=0, q=None, lens=None, bt=None, pt=None) == 0
+    assert g.block_attention_fp4_workspace_bytes(2, 4, 8, 2, 128, 64, 64, 0) == 0
+    assert g.block_attention_fp4_workspace_bytes(2, 4, 8, 2, 100, 64, 512, 100) == 0  # not instantiated
+    with pytest.raises(g.FlareError, match="beyond 32 bits"):
+        g.block_attention_fp4_workspace_bytes(2, 4, 8, 2, 128, 64, 512, 2 ** 32 + 5)
+    # more workgroups than a launch holds
+    assert attention4(L, R=2 ** 20, block=1, qh=8, kh=8, most=2 ** 30, wide=2 ** 10, page=2 ** 20, n=0, pt=None, nbytes=2 ** 62) == 4
+
+
+@pytest.mark.parametrize("R,B,Hq,Hk,d,own,prefix", [(1, 1, 1, 1, 64, 1, 0), (256, 4, 16, 4, 128, 1024, 8192), (3, 7, 16, 2, 256, 777, 2500),
+                                                    (1, 1, 16, 4, 128, 1 << 20, 0), (64, 1, 8, 8, 64, 0, 1 << 22), (5, 32, 8, 1, 128, 40, 40)])
+def test_attention_workspace_is_rows_times_parts(L, R, B, Hq, Hk, d, own, prefix):
+    """d + 2 floats a row and part, plus the alignment; parts of at most 4096 keys."""
+    n = g.block_attention_fp4_workspace_bytes(R, B, Hq, Hk, d, 16, own, prefix)
+    if n == 0:
+        assert own + prefix <= 4096
+        return
+    parts, rest = divmod(n - 256, R * B * Hq * (d + 2) * 4)
+    assert rest == 0 and parts >= -(-own // 4096) + -(-prefix // 4096) and parts >= 2
+
+
+def test_attention_refuses_host_tensors():
+    c4 = g.cache_fp4(1, 1, 16, 64, device="cpu")
+    with pytest.raises(g.FlareError, match="GPU tensor"):
+        g.block_attention_fp4(torch.zeros(2, 1, 1, 64, dtype=torch.bfloat16), c4, c4, None, None)
