@@ -422,7 +422,8 @@ size_t flare_block_attention_fp4_workspace_size(int32_t num_req, const flare_att
                                                 int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_fp4_shape(num_req, shape, max_seq_len, prefix_len) != FLARE_OK) return 0;
   const BlockAttnArgs a = attention_args(num_req, shape, max_seq_len, prefix_len);
-  return block_attention_workspace_bytes(a, attn_fp4_plan(a));
+  AttnForms forms;
+  return block_attention_workspace_bytes(a, attn_fp4_plan(a, forms));
 }
 
 flare_status flare_block_attention_fp4(int32_t num_req, const flare_attention_shape *shape, const void *q,
@@ -445,7 +446,10 @@ flare_status flare_block_attention_fp4(int32_t num_req, const flare_attention_sh
     return fail(FLARE_ERR_ALIGN, "block_attention_fp4: q and o must be 16-byte, the scales 4-byte aligned");
   BlockAttnFp4Args b{attention_args(num_req, shape, max_seq_len, prefix_len), k_scales, v_scales};
   BlockAttnArgs &a = b.a;
-  const AttnPlan p = attn_fp4_plan(a);
+  st = check_attention_fp4_cache(a, num_pages);
+  if (st != FLARE_OK) return st;
+  AttnForms forms;
+  const AttnPlan p = attn_fp4_plan(a, forms);
   st = check_attention_plan(a, p, workspace, workspace_bytes);
   if (st != FLARE_OK) return st;
   a.num_pages = num_pages;
@@ -454,7 +458,7 @@ flare_status flare_block_attention_fp4(int32_t num_req, const flare_attention_sh
   a.block_table = block_table; a.seq_lens = seq_lens; a.prefix_table = prefix_table;
   a.o = o; a.lse = lse;
   a.part = reinterpret_cast<float *>(workspace);
-  return hip_status(launch_block_attention_fp4(b, p, (hipStream_t)stream), "block_attention_fp4 launch");
+  return hip_status(launch_block_attention_fp4(b, p, forms, (hipStream_t)stream), "block_attention_fp4 launch");
 }
 
 }  // extern "C"

@@ -29,6 +29,31 @@ struct Part {
   const int32_t *table;
 };
 
+// The id-th workgroup of the requests' own keys.
+template <int OWN_ROWS>
+__device__ __forceinline__ bool own_part(const BlockAttnArgs &a, const AttnPlan &p, uint32_t id, Part &w) {
+  const uint32_t BG = a.block * (a.q_heads / a.kv_heads);
+  if (id >= p.own_blocks) return false;
+  w.head = (int)(id % (uint32_t)a.kv_heads);
+  id /= (uint32_t)a.kv_heads;
+  const uint32_t rg = id % (uint32_t)p.own_groups;
+  id /= (uint32_t)p.own_groups;
+  // all requests' first parts before their second: the longest requests' last ones start last
+  w.req = (int)(id % (uint32_t)a.num_req);
+  const int part = (int)(id / (uint32_t)a.num_req);
+  w.len = attn_own_len(a, a.seq_lens[w.req]);
+  w.row0 = w.req * BG + rg * OWN_ROWS;
+  w.row_end = (w.req + 1) * BG;
+  w.k0 = part * p.own_chunk;
+  w.k1 = w.len - w.k0 < p.own_chunk ? w.len : w.k0 + p.own_chunk;
+  w.out = p.prefix_parts + part;
+  w.pre = p.merged ? a.prefix_len : 0;
+  w.table = a.block_table + (int64_t)w.req * a.max_pages;
+  // a part behind the request's length is not read by the joining launch; the
+  // only part is written in any case
+  return w.k0 < w.k1 || p.prefix_parts + p.own_parts == 1;
+}
+
 // Workgroups of the prefix and of the requests' own keys alternate in runs of one
 // workgroup for each CU, in proportion and the prefix first: the prefix is bound by
 // its products, the own keys by memory, so a CU holds both kinds at a time (256
@@ -58,26 +83,7 @@ __device__ __forceinline__ bool find_part(const BlockAttnArgs &a, const AttnPlan
     w.table = a.prefix_table;
     return true;
   }
-  uint32_t id = ((run - before) * kOctets + in) * 8 + blockIdx.x % 8;
-  if (id >= p.own_blocks) return false;
-  w.head = (int)(id % (uint32_t)a.kv_heads);
-  id /= (uint32_t)a.kv_heads;
-  const uint32_t rg = id % (uint32_t)p.own_groups;
-  id /= (uint32_t)p.own_groups;
-  // all requests' first parts before their second: the longest requests' last ones start last
-  w.req = (int)(id % (uint32_t)a.num_req);
-  const int part = (int)(id / (uint32_t)a.num_req);
-  w.len = attn_own_len(a, a.seq_lens[w.req]);
-  w.row0 = w.req * BG + rg * OWN_ROWS;
-  w.row_end = (w.req + 1) * BG;
-  w.k0 = part * p.own_chunk;
-  w.k1 = w.len - w.k0 < p.own_chunk ? w.len : w.k0 + p.own_chunk;
-  w.out = p.prefix_parts + part;
-  w.pre = p.merged ? a.prefix_len : 0;
-  w.table = a.block_table + (int64_t)w.req * a.max_pages;
-  // a part behind the request's length is not read by the joining launch; the
-  // only part is written in any case
-  return w.k0 < w.k1 || p.prefix_parts + p.own_parts == 1;
+  return own_part<OWN_ROWS>(a, p, ((run - before) * kOctets + in) * 8 + blockIdx.x % 8, w);
 }
 
 }  // namespace flare

@@ -28,9 +28,14 @@ FLARE_HD int attn_own_len(const BlockAttnArgs &a, int32_t len) {
 
 // a.max_seq_len <= max_pages * page
 AttnPlan attn_plan(const BlockAttnArgs &a);
-// Over a cache in 4 bits, where a workgroup has 16 rows a tile and its four waves a
-// quarter of its keys each.
-AttnPlan attn_fp4_plan(const BlockAttnArgs &a);
+// Over a cache in 4 bits, where the prefix and the own keys each take one of two forms: a
+// workgroup's waves share its tiles of keys and have 16 rows a tile each (prefix_tiles,
+// own_tiles of 64 rows), or they share the rows, 16 a tile, and have a quarter of the keys
+// each.  The own keys are shared only where the prefix is.
+struct AttnForms {
+  bool prefix_shared, own_shared;
+};
+AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f);
 // The workgroups that a plan launches: those of the prefix and of the own keys, each
 // filled up to whole runs.
 int64_t attn_launch_blocks(const AttnPlan &p);

@@ -26,7 +26,7 @@
 #include <type_traits>
 #include <utility>
 
-#include "attn_parts.h"
+#include "attn_tiles.h"
 #include "fp4.h"
 #include "layer_launch.h"
 
@@ -75,13 +75,17 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
     const int j = (T < pre_tiles ? 32 * T : k0 + 32 * (T - pre_tiles)) + 16 * sb, last = (end - 1) & ~15;
     return j < last ? j : last;
   };
-  // lane i holds the page of this wave's subtile i
-  int page_id = 0;
+  // lane i holds where this wave's subtile i lies: its codes in units of 16 rows, its scales
+  // in units of 16 bytes
+  uint32_t codes_at = 0, scales_at = 0;
   if (mine > 0) {
-    const int t = (lane >> 1) < mine ? lane >> 1 : mine - 1, T = wave + 4 * t;
-    page_id = (T < pre_tiles ? a.prefix_table : w.table)[subtile(T, lane & 1) >> p.page_shift];
-    if (page_id < 0) page_id = 0;
-    if (page_id >= a.num_pages) page_id = (int)a.num_pages - 1;
+    const int t = (lane >> 1) < mine ? lane >> 1 : mine - 1, T = wave + 4 * t, j = subtile(T, lane & 1);
+    int pg = (T < pre_tiles ? a.prefix_table : w.table)[j >> p.page_shift];
+    if (pg < 0) pg = 0;
+    if (pg >= a.num_pages) pg = (int)a.num_pages - 1;
+    const uint32_t ph = (uint32_t)pg * a.kv_heads + head, off = (j & (a.page - 1)) >> 4;
+    codes_at = (ph << (p.page_shift - 4)) + off;
+    scales_at = (ph * (D / 32) << (p.page_shift - 4)) + off;
   }
   // this lane's places in a subtile
   const uint32_t k_at = col * (D / 2) + grp * (D == 64 ? 8 : 16);
@@ -91,10 +95,8 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
   auto load = [&](Tile<D> &x, int t) {
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
-      const int j = subtile(wave + 4 * t, sb), pg = __builtin_amdgcn_readlane(page_id, 2 * t + sb);
-      const int64_t ph = (int64_t)pg * a.kv_heads + head;
-      const int off = j & (a.page - 1);
-      const int64_t at = ((ph << p.page_shift) + off) * (D / 2), s_at = ((ph * (D / 32)) << p.page_shift) + off;
+      const int64_t at = (int64_t)(uint32_t)__builtin_amdgcn_readlane(codes_at, 2 * t + sb) * (8 * D);
+      const int64_t s_at = (int64_t)(uint32_t)__builtin_amdgcn_readlane(scales_at, 2 * t + sb) * 16;
       const uint8_t *kc = (const uint8_t *)a.k_cache + at, *vc = (const uint8_t *)a.v_cache + at;
       const uint8_t *ks = b.k_scales + s_at, *vs = b.v_scales + s_at;
       if constexpr (D == 64) {
@@ -130,7 +132,6 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
     return z;
   };
   u32x4v *const q_lds = reinterpret_cast<u32x4v *>(lds);
-  char *const join = lds + kQueryBytes<D, NQ>;
   bf16x8 q[kQueriesInLds<D, NQ> ? 1 : NQ][kQueriesInLds<D, NQ> ? 1 : KS];
   if constexpr (kQueriesInLds<D, NQ>) {
     for (int i = wave; i < NQ * KS; i += 4) q_lds[i * 64 + lane] = query(i / KS, i % KS);
@@ -251,27 +252,24 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
         }
       }
       if (__any(odd)) {
-        uint32_t *const pl = reinterpret_cast<uint32_t *>(join) + wave * NQ * 16 * 16;  // [NQ][16][32 weights]
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pl[(n * 16 + col) * 16 + 8 * (e >> 1) + 2 * grp + (e & 1)] = pb[n][e];
-        __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
         for (int key = all > kt ? all : kt; key < end && key < kt + 32; ++key) {
-          const int pg = __builtin_amdgcn_readlane(page_id, 2 * t + ((key - kt) >> 4)), off = key & (a.page - 1);
-          const int64_t ph = (int64_t)pg * a.kv_heads + head;
+          const int from = 2 * t + ((key - kt) >> 4);
+          const int64_t at = (int64_t)(uint32_t)__builtin_amdgcn_readlane(codes_at, from) * 16 + (key & 15);
+          const int64_t s_at = (int64_t)(uint32_t)__builtin_amdgcn_readlane(scales_at, from) * 16 + (key & 15);
           float f[NQ];
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
-            const uint32_t two = pl[(n * 16 + col) * 16 + ((key - kt) >> 1)];
+            const int j = key - kt;
+            const uint32_t lo = j & 2 ? pb[n][1] : pb[n][0], hi = j & 2 ? pb[n][3] : pb[n][2];
+            const uint32_t two = __shfl(j & 16 ? hi : lo, 4 * (j & 12) + col);
             f[n] = __uint_as_float(key & 1 ? two & 0xffff0000u : two << 16);
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int ch = DT * (4 * grp + r);
-            const uint32_t byte = b.v_scales[((ph * (D / 32) + ch / kFp4Group) << p.page_shift) + off];
-            const uint8_t *row = (const uint8_t *)a.v_cache + ((ph << p.page_shift) + off) * (D / 2) + ch / 2;
+            const uint32_t byte = b.v_scales[s_at + ((int64_t)(ch / kFp4Group) << p.page_shift)];
+            const uint8_t *row = (const uint8_t *)a.v_cache + at * (D / 2) + ch / 2;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               const uint32_t two = fp4_pair<0>(row[c], byte << 23);
@@ -286,10 +284,11 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
         }
       }
     }
-    // the values: 8 keys a lane, their scales as a float's exponent
+    // the values: 8 keys a lane, their scales as a float's exponent (what stands in the other
+    // bits is not looked at)
     uint32_t scale[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) scale[i] = ((x.vs[i >> 2] >> 8 * (i & 3)) & 255u) << 23;
+    for (int i = 0; i < 8; ++i) scale[i] = (i & 3) < 3 ? x.vs[i >> 2] << (23 - 8 * (i & 3)) : x.vs[i >> 2] >> 1;
     each<D / 32>([&](auto c) {
       constexpr int C = decltype(c)::value;
       uint32_t y[8];
@@ -308,15 +307,17 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
     });
   };
 #pragma unroll 1
-  for (int t = 0; t < mine; ++t) {
+  for (int t = 0; t < mine; t += 2) {
     if (t + 1 < mine) load(tb, t + 1);
     compute(ta, t);
-    ta = tb;
+    if (t + 1 >= mine) break;
+    if (t + 2 < mine) load(ta, t + 2);
+    compute(tb, t + 1);
   }
 
   // The four waves' maxima and sums, then their outputs: wave r joins the channels DT (4 grp
   // + r) .. of every row, which lie together.
-  __syncthreads();
+  char *const join = lds + kQueryBytes<D, NQ>;
   float2 *const stat = reinterpret_cast<float2 *>(join);           // [4][NQ][16]
   float *const piece = reinterpret_cast<float *>(stat + 4 * NQ * 16);  // [wave][its 3 pieces][64][DT]
 #pragma unroll
@@ -394,42 +395,158 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
   }
 }
 
+// The tiles of the form that block_attn.hip describes, whose waves share them: a wave
+// loads its 16 rows of codes into registers two tiles ahead and converts them into LDS one
+// ahead.  Four lanes a row: a lane has D / 4 channels of it.  TK = 64: a wave
+// has one subtile of K and of V; TK = 32: waves 0, 1 K, 2, 3 V.
+template <int D, int TK> struct CodesToLds {
+  static constexpr int SUBS = TK / 16, W = D / 32;  // words of codes of a lane's row, pieces in LDS
+  static constexpr bool kLands = true;
+  const BlockAttnFp4Args &b;
+  u16 *kt, *vt;
+  int shift, lane, wave, sub;
+  struct Codes {
+    uint32_t c[W], s[D == 256 ? 2 : 1];
+  } k, v;  // SUBS = 2: k alone, of whichever is this wave's
+  __device__ __forceinline__ CodesToLds(const BlockAttnFp4Args &b, int shift, int lane, int wave, int sub, u16 (&kt_lds)[2][TK * D],
+                                        u16 (&vt_lds)[2][TK * D])
+      : b(b), kt(kt_lds[0]), vt(vt_lds[0]), shift(shift), lane(lane), wave(wave), sub(sub) {}
+  __device__ __forceinline__ void fetch(Codes &x, const void *codes, const uint8_t *scales, int64_t ph, int row) const {
+    const uint8_t *c = (const uint8_t *)codes + ((ph << shift) + row) * (D / 2);
+    const uint8_t *s = scales + ((ph * (D / 32)) << shift) + row;
+    const uint32_t at = lane >> 2, q = lane & 3, page = 1u << shift;
+    if constexpr (D == 64) {
+      *reinterpret_cast<uint2 *>(x.c) = *reinterpret_cast<const uint2 *>(c + (at * (D / 2) + q * 8));
+      x.s[0] = s[(q >> 1) * page + at];
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 128; ++h) {
+        *reinterpret_cast<uint4 *>(x.c + 4 * h) = *reinterpret_cast<const uint4 *>(c + (at * (D / 2) + q * (D / 8) + 16 * h));
+        x.s[h] = s[(q * (D / 128) + h) * page + at];
+      }
+    }
+  }
+  __device__ __forceinline__ void load(int pg, int head, int row, int) {
+    const int64_t ph = (int64_t)pg * b.a.kv_heads + head;
+    if constexpr (SUBS == 4) {
+      fetch(k, b.a.k_cache, b.k_scales, ph, row);
+      fetch(v, b.a.v_cache, b.v_scales, ph, row);
+    } else {
+      fetch(k, wave < 2 ? b.a.k_cache : b.a.v_cache, wave < 2 ? b.k_scales : b.v_scales, ph, row);
+    }
+  }
+  __device__ __forceinline__ void put(const Codes &x, u16 *tile, bool value) const {
+    const int row = lane >> 2, q = lane & 3;
+    u16 *to = tile + (sub * 16 + row) * D;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t c = x.c[i], s = x.s[i / 4] << 23;
+      const int piece = value ? v_piece<D>(row, W * q + i) : k_piece<D>(row, W * q + i);
+      *reinterpret_cast<uint4 *>(to + piece * 8) = make_uint4(fp4_pair<0>(c, s), fp4_pair<1>(c, s), fp4_pair<2>(c, s), fp4_pair<3>(c, s));
+    }
+  }
+  __device__ __forceinline__ void land(int buf) const {
+    if constexpr (SUBS == 4) {
+      put(k, kt + buf * (TK * D), false);
+      put(v, vt + buf * (TK * D), true);
+    } else {
+      put(k, (wave < 2 ? kt : vt) + buf * (TK * D), wave >= 2);
+    }
+  }
+};
+
+// What this workgroup works on.  As find_part, but the row groups of a unit (kv head, part)
+// of the prefix go round the XCDs: its codes are few enough for each XCD's L2 to have them
+// all, and units that are no multiple of eight leave no XCD more than others.
+template <int PREFIX_ROWS, int OWN_ROWS>
+__device__ __forceinline__ bool find_part_fp4(const BlockAttnArgs &a, const AttnPlan &p, Part &w) {
+  const uint32_t G = a.q_heads / a.kv_heads, BG = a.block * G;
+  const uint32_t run = blockIdx.x / 8 / kOctets, in = blockIdx.x % (8 * kOctets), all = p.prefix_runs + p.own_runs;
+  const uint32_t before = ((uint64_t)run * p.prefix_runs + all - 1) / all;  // runs of the prefix before this one
+  if (((uint64_t)(run + 1) * p.prefix_runs + all - 1) / all > before) {
+    const uint32_t pi = before * (8 * kOctets) + in;
+    if (pi >= p.prefix_blocks) return false;
+    const uint32_t unit = pi / p.prefix_groups, rg = pi % p.prefix_groups;
+    const int part = (int)(unit / a.kv_heads);
+    w.head = (int)(unit % a.kv_heads);
+    w.row0 = rg * PREFIX_ROWS;
+    w.row_end = a.num_req * BG;
+    w.len = a.prefix_len;
+    w.k0 = part * p.prefix_chunk;
+    w.k1 = w.len - w.k0 < p.prefix_chunk ? w.len : w.k0 + p.prefix_chunk;
+    w.out = part;
+    w.pre = 0;
+    w.req = -1;
+    w.table = a.prefix_table;
+    return true;
+  }
+  return own_part<OWN_ROWS>(a, p, (run - before) * (8 * kOctets) + in, w);
+}
+
+// What takes 16 rows a tile: a workgroup whose waves divide the keys among them (OWN = false),
+// or each wave, over tiles of keys that they share (true).
+template <int D> constexpr int kTileKeys = D == 256 ? 32 : 64;
+template <int D, bool SHARED, int NQ> constexpr int kRows = SHARED ? 64 * NQ : 16 * NQ;
+
 constexpr int larger(int a, int b) { return a > b ? a : b; }
-template <int D, int NQ> constexpr int kLdsBytes = kQueryBytes<D, NQ> + larger(4 * NQ * 16 * 8 + 12 * 64 * (D / 16) * 4, 4 * NQ * 1024);
+template <int D, bool SHARED, int NQ>
+constexpr int kLdsBytes = SHARED ? 4 * kTileKeys<D> * D * 2
+                                 : kQueryBytes<D, NQ> + 4 * NQ * 16 * 8 + 12 * 64 * (D / 16) * 4;
 
-// NQP, NQO: row tiles of 16 for the prefix (rows of all requests) and for a request's own
-// keys; WPS: waves a SIMD.
-template <int D, int NQP, int NQO, int WPS>
+template <int D, bool SHARED, int NQ>
+__device__ __forceinline__ void part_of(const BlockAttnFp4Args &b, const AttnPlan &p, const Part &w, char *lds) {
+  if constexpr (SHARED) {
+    constexpr int TK = kTileKeys<D>;
+    using Tiles = u16[2][TK * D];
+    const uint32_t oct = blockIdx.x / 8;
+    attn_part<D, NQ, TK, CodesToLds<D, TK>>(b, p, w, w.req < 0 ? 0 : (oct + oct / 32) & 3, *reinterpret_cast<Tiles *>(lds),
+                                            *reinterpret_cast<Tiles *>(lds + sizeof(Tiles)));
+  } else {
+    part_fp4<D, NQ>(b, p, w, lds);
+  }
+}
+
+// The prefix's and the own keys' form and row tiles; WPS: waves a SIMD.
+template <int D, bool PS, int NQP, bool OS, int NQO, int WPS>
 __global__ __launch_bounds__(256, WPS) void attend_fp4_kernel(BlockAttnFp4Args b, AttnPlan p) {
-  __shared__ __align__(16) char lds[larger(kLdsBytes<D, NQP>, kLdsBytes<D, NQO>)];
+  __shared__ __align__(16) char lds[larger(kLdsBytes<D, PS, NQP>, kLdsBytes<D, OS, NQO>)];
   Part w;
-  if (!find_part<16 * NQP, 16 * NQO>(b.a, p, w)) return;
-  if (NQP == NQO || w.req >= 0) part_fp4<D, NQO>(b, p, w, lds);
-  else part_fp4<D, NQP>(b, p, w, lds);
+  if (!find_part_fp4<kRows<D, PS, NQP>, kRows<D, OS, NQO>>(b.a, p, w)) return;
+  if ((PS == OS && NQP == NQO) || w.req >= 0) part_of<D, OS, NQO>(b, p, w, lds);
+  else part_of<D, PS, NQP>(b, p, w, lds);
 }
 
-template <int D, int NQP, int NQO, int WPS> void launch(const BlockAttnFp4Args &b, const AttnPlan &p, hipStream_t st) {
-  attend_fp4_kernel<D, NQP, NQO, WPS><<<(unsigned)attn_launch_blocks(p), 256, 0, st>>>(b, p);
+template <int D, bool PS, int NQP, bool OS, int NQO, int WPS>
+void launch(const BlockAttnFp4Args &b, const AttnPlan &p, hipStream_t st) {
+  attend_fp4_kernel<D, PS, NQP, OS, NQO, WPS><<<(unsigned)attn_launch_blocks(p), 256, 0, st>>>(b, p);
 }
 
-template <int D> void launch_d(const BlockAttnFp4Args &b, const AttnPlan &p, hipStream_t st) {
-  if (p.prefix_tiles == 1) launch<D, 1, 1, D == 256 ? 2 : 3>(b, p, st);
-  else if (p.prefix_tiles == 2 && p.own_tiles == 1) launch<D, 2, 1, 2>(b, p, st);
-  else if (p.prefix_tiles == 2) launch<D, 2, 2, 2>(b, p, st);
-  else if constexpr (D <= 128) {
-    if (p.own_tiles == 1) launch<D, 4, 1, 2>(b, p, st);
-    else if (p.own_tiles == 2) launch<D, 4, 2, 2>(b, p, st);
-    else launch<D, 4, 4, 2>(b, p, st);
+template <int D> void launch_d(const BlockAttnFp4Args &b, const AttnPlan &p, const AttnForms &f, hipStream_t st) {
+  constexpr int TWO = D == 256 ? 1 : 2, S = D == 64 ? 3 : 2;
+  if (!f.prefix_shared) {  // nor the own keys'
+    if (p.prefix_tiles == 1) {
+      launch<D, false, 1, false, 1, D == 64 ? 4 : D == 128 ? 3 : 2>(b, p, st);
+    } else if constexpr (D <= 128) {
+      if (p.own_tiles == 1) launch<D, false, 2, false, 1, D == 64 ? 3 : 2>(b, p, st);
+      else launch<D, false, 2, false, 2, D == 64 ? 3 : 2>(b, p, st);
+    }
+  } else if (!f.own_shared) {
+    if (p.own_tiles == 1) launch<D, true, TWO, false, 1, S>(b, p, st);
+    else if constexpr (D <= 128) launch<D, true, TWO, false, 2, S>(b, p, st);
+  } else if (p.own_tiles == 2) {
+    launch<D, true, TWO, true, TWO, S>(b, p, st);
+  } else {
+    launch<D, true, TWO, true, 1, S>(b, p, st);
   }
 }
 
 }  // namespace
 
-hipError_t launch_block_attention_fp4(const BlockAttnFp4Args &b, const AttnPlan &p, hipStream_t st) {
+hipError_t launch_block_attention_fp4(const BlockAttnFp4Args &b, const AttnPlan &p, const AttnForms &f, hipStream_t st) {
   TimedLaunch tl(K_BLOCK_ATTN_FP4, st);
-  if (b.a.dim == 64) launch_d<64>(b, p, st);
-  else if (b.a.dim == 128) launch_d<128>(b, p, st);
-  else launch_d<256>(b, p, st);
+  if (b.a.dim == 64) launch_d<64>(b, p, f, st);
+  else if (b.a.dim == 128) launch_d<128>(b, p, f, st);
+  else launch_d<256>(b, p, f, st);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : launch_attn_join(b.a, p, st);
 }

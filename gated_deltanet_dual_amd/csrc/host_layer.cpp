@@ -87,39 +87,79 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
   return p;
 }
 
-AttnPlan attn_fp4_plan(const BlockAttnArgs &a) {
+namespace {
+// What a key costs a workgroup, in tenths of a nanosecond: alone on its CU, its share of a
+// CU's instructions that several keep busy, and its share of memory's time where no other
+// row group reads it.  Measured: the shared form of two row tiles at d = 128, 4096 keys 106 us
+// alone, 4 x 2048 keys 80 us two a CU; d = 256, one: 2 x 2048 133 us; d = 64, two: 4 x 1024 60
+// us four a CU.  The other form, one row tile at d = 128, 4096 keys 29 us where every CU has
+// one, 2 x 2048 24 us.
+struct KeyCost {
+  int alone, busy, memory;
+};
+KeyCost key_cost(bool shared, int tiles, int dim) {
+  const int memory = dim / 2 - dim / 64;  // 17 / 16 of a byte a channel, at 4.4 TB/s over 256 CUs
+  if (shared) {
+    if (dim == 256) return {450, 325, memory};
+    if (dim == 64) return tiles == 2 ? KeyCost{180, 146, memory} : KeyCost{120, 90, memory};
+    return tiles == 2 ? KeyCost{260, 195, memory} : KeyCost{176, 120, memory};
+  }
+  if (dim == 256) return {140, 70, memory};
+  if (dim == 64) return tiles == 2 ? KeyCost{65, 40, memory} : KeyCost{50, 25, memory};
+  return tiles == 2 ? KeyCost{98, 55, memory} : KeyCost{70, 35, memory};
+}
+constexpr int64_t kCus = 256, kStart = 45000;  // a launch's start and end
+}  // namespace
+
+AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   AttnPlan p{};
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
   const int64_t all_rows = rows * a.num_req;
-  const int most = a.dim == 256 ? 2 : 4;
-  auto tiles = [&](int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : most; };
-  p.own_tiles = tiles(rows);
-  p.prefix_tiles = a.prefix_len > 0 ? tiles(all_rows) : p.own_tiles;
-  p.own_groups = (int)ceil_div(rows, 16 * p.own_tiles);
-  p.prefix_groups = (int)ceil_div(all_rows, 16 * p.prefix_tiles);
-
-  // The lengths of the parts: the shortest time, in nanoseconds.
-  constexpr int64_t kSlots = 512, kStart = 2500, kLongest = 4096;
-  auto key_cost = [&](int t) { return (t == 1 ? 5 : t == 2 ? 8 : 13) * (int64_t)a.dim / 128 + 1; };
-  const int64_t own_key = key_cost(p.own_tiles), prefix_key = key_cost(p.prefix_tiles);
-  const int64_t join = all_rows * a.kv_heads * a.dim / 625 + 40;
+  const int two = a.dim == 256 ? 1 : 2;
+  f.own_shared = rows > 16 * two;
+  // as over bf16: two row tiles a wave where that leaves a workgroup for every CU
+  p.own_tiles = f.own_shared ? (rows > 64 && ceil_div(rows, 128) * a.kv_heads * a.num_req >= 256 ? two : 1) : rows > 16 ? 2 : 1;
+  p.own_groups = (int)ceil_div(rows, (f.own_shared ? 64 : 16) * p.own_tiles);
   const int64_t units = (int64_t)p.own_groups * a.kv_heads * a.num_req;
-  p.prefix_chunk = p.own_chunk = (int)kLongest;
-  int64_t best = INT64_MAX, own_top = kLongest;
+  const KeyCost own = key_cost(f.own_shared, p.own_tiles, a.dim);
+  // the time of n workgroups of so many keys: of the prefix, which the row groups read from
+  // the caches, and of the own keys
+  auto passes = [](int64_t n, int64_t keys, int64_t alone, int64_t each) {
+    const int64_t busy = ceil_div(n, kCus) * keys * each;
+    return keys * alone > busy ? keys * alone : busy;
+  };
+  const int own_each = own.busy > own.memory ? own.busy : own.memory;
+
+  // A short prefix is passed by every request before its own keys, in one part, where that
+  // takes no longer than its sharing; a wave keeps where its tiles lie in its 64 lanes: 64
+  // tiles that are shared, 32 tiles of 32 keys that are a quarter of the part's.
+  const int64_t tile = f.own_shared && a.dim != 256 ? 64 : 32, part_tiles = f.own_shared ? 64 : 128;
+  const int64_t all_tiles = ceil_div(a.prefix_len, tile) + ceil_div(a.max_seq_len, tile);
+  const int64_t together = a.prefix_len > 0 && all_tiles <= part_tiles ? passes(units, a.prefix_len + a.max_seq_len, own.alone, own_each) : INT64_MAX;
+
+  f.prefix_shared = f.own_shared || (a.prefix_len > 0 && all_rows > 64);
+  p.prefix_tiles = a.prefix_len == 0 ? p.own_tiles : f.prefix_shared ? two : all_rows > 16 ? two : 1;
+  if (!f.prefix_shared && p.prefix_tiles < p.own_tiles) p.prefix_tiles = p.own_tiles;
+  p.prefix_groups = (int)ceil_div(all_rows, (f.prefix_shared ? 64 : 16) * p.prefix_tiles);
+  const KeyCost prefix = key_cost(f.prefix_shared, p.prefix_tiles, a.dim);
+  const int64_t longest = a.dim == 256 ? 2048 : 4096, prefix_units = (int64_t)p.prefix_groups * a.kv_heads;
+  // every part is written, and read again by the joining launch
+  const int64_t join = all_rows * a.kv_heads * a.dim / 140 + 200;
+  p.prefix_chunk = p.own_chunk = (int)longest;
+  int64_t best = INT64_MAX, own_top = longest;
   while (own_top > 128 && own_top / 2 >= a.max_seq_len) own_top /= 2;
-  const int64_t least = ceil_div(a.prefix_len, kLongest), parts_most = ceil_div(a.prefix_len, 128);
+  const int64_t least = ceil_div(a.prefix_len, longest), parts_most = ceil_div(a.prefix_len, 128);
   for (int64_t n = least; n <= parts_most; n += 1 + n / 4) {
-    const int64_t chunk = n > 0 ? ceil_div(ceil_div(a.prefix_len, n), 128) * 128 : kLongest;
-    const int64_t parts = ceil_div(a.prefix_len, chunk), units8 = ceil_div(parts * a.kv_heads, 8) * p.prefix_groups;
-    const int64_t prefix_time = chunk * prefix_key + kStart, prefix_rounds = ceil_div(units8, kSlots / 8) * prefix_time;
+    const int64_t chunk = n > 0 ? ceil_div(ceil_div(a.prefix_len, n), 128) * 128 : longest;
+    const int64_t parts = ceil_div(a.prefix_len, chunk);
+    const int64_t prefix_time = parts > 0 ? passes(parts * prefix_units, chunk, prefix.alone, prefix.busy) : 0;
     for (int64_t c = own_top; c >= 128; c /= 2) {
-      const int64_t own_parts = ceil_div(a.max_seq_len, c);
-      const int64_t own_time = (c < a.max_seq_len ? c : a.max_seq_len) * own_key + kStart;
-      int64_t cost = (8 * units8 * prefix_time + units * own_parts * own_time) / kSlots;
-      const int64_t own_rounds = ceil_div(units * own_parts, kSlots) * own_time;
-      if (parts > 0 && cost < prefix_rounds) cost = prefix_rounds;
-      if (cost < own_rounds) cost = own_rounds;
+      const int64_t own_parts = ceil_div(a.max_seq_len, c), keys = c < a.max_seq_len ? c : a.max_seq_len;
+      const int64_t own_time = own_parts > 0 ? passes(units * own_parts, keys, own.alone, own_each) : 0;
+      int64_t cost = (parts * prefix_units * chunk * prefix.busy + units * own_parts * keys * own.busy) / kCus;
+      if (cost < prefix_time) cost = prefix_time;
+      if (cost < own_time) cost = own_time;
       if (parts + own_parts > 1) cost += (parts + own_parts) * join + kStart;
       if (cost < best) {
         best = cost;
@@ -130,19 +170,15 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a) {
       }
     }
   }
-  p.prefix_blocks = ceil_div((int64_t)p.prefix_parts * a.kv_heads, 8) * 8 * p.prefix_groups;
-  // a short prefix is passed by every request before its own keys, in one part
-  if (a.prefix_len > 0 && ceil_div(a.prefix_len, 32) + ceil_div(a.max_seq_len, 32) <= kLongest / 32) {
-    const int64_t together = ceil_div(units, kSlots) * ((a.prefix_len + a.max_seq_len) * own_key + kStart);
-    if (together <= best) {
-      p.merged = 1;
-      p.prefix_tiles = p.own_tiles;
-      p.prefix_parts = 0;
-      p.prefix_blocks = 0;
-      p.own_parts = 1;
-      p.own_chunk = (int)kLongest;
-    }
+  if (together <= best) {
+    p.merged = 1;
+    f.prefix_shared = f.own_shared;
+    p.prefix_tiles = p.own_tiles;
+    p.prefix_parts = 0;
+    p.own_parts = 1;
+    p.own_chunk = (int)(part_tiles * tile);
   }
+  p.prefix_blocks = p.prefix_parts * prefix_units;
   if (p.prefix_parts + p.own_parts == 0) p.own_parts = 1;  // no keys at all: zeros are written
   p.own_blocks = units * p.own_parts;
   p.prefix_runs = (int)ceil_div(p.prefix_blocks, 8 * kOctets);
@@ -350,6 +386,13 @@ flare_status check_attention_fp4_shape(int32_t num_req, const flare_attention_sh
   if (st != FLARE_OK) return st;
   // a lane's place among a page's scales is kept in 32 bits
   if (s->page > 1 << 24) return fail(FLARE_ERR_UNSUPPORTED, "block_attention_fp4: page %d, at most 2^24", s->page);
+  return FLARE_OK;
+}
+
+flare_status check_attention_fp4_cache(const BlockAttnArgs &a, int64_t num_pages) {
+  // the kernel counts a cache's rows and scales in units of 16
+  if (num_pages > (((int64_t)1 << 36) - 1) / a.kv_heads / (a.dim / 32) / a.page)
+    return fail(FLARE_ERR_UNSUPPORTED, "block_attention_fp4: caches of up to 2^41 values");
   return FLARE_OK;
 }
 

@@ -22,7 +22,7 @@ hipError_t launch_cache_fp4_rows(const Cache4Rows &a, hipStream_t st);
 hipError_t launch_step_tables(const StepTablesArgs &a, hipStream_t st);
 // joins a call's parts; nothing where it has only one
 hipError_t launch_attn_join(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st);
-hipError_t launch_block_attention_fp4(const BlockAttnFp4Args &a, const AttnPlan &p, hipStream_t st);
+hipError_t launch_block_attention_fp4(const BlockAttnFp4Args &a, const AttnPlan &p, const AttnForms &f, hipStream_t st);
 hipError_t launch_block_attention(const BlockAttnArgs &a, const AttnPlan &p, hipStream_t st);
 
 }  // namespace flare

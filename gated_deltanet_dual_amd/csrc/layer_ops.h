@@ -175,6 +175,7 @@ flare_status check_attention_shape(int32_t num_req, const flare_attention_shape 
                                    int32_t prefix_len);
 flare_status check_attention_fp4_shape(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
                                        int32_t prefix_len);
+flare_status check_attention_fp4_cache(const BlockAttnArgs &a, int64_t num_pages);
 BlockAttnArgs attention_args(int32_t num_req, const flare_attention_shape *s, int32_t max_seq_len,
                              int32_t prefix_len);
 

@@ -121,6 +121,11 @@ CASES = [
     (2, 20, 1, 8, 128, 32, [20, 131], 5000),
     (3, 9, 1, 3, 64, 32, [20, 0, 131], 4500),
     (1, 1, 1, 1, 64, 16, [1], 4097),
+    # a short prefix before more own keys than a part of shared tiles holds
+    (40, 1, 1, 2, 256, 64, [2500] + [40] * 39, 100),
+    (40, 1, 1, 2, 128, 64, [3900] + [40] * 39, 100),
+    (3, 40, 1, 1, 128, 64, [3900, 40, 41], 150),
+    (3, 40, 1, 1, 256, 64, [1900, 40, 41], 100),
 ]
 
 
