@@ -102,6 +102,18 @@ struct QkNormArgs {
   float *dweight[2], *part;  // part [2][blocks][dim]
 };
 
+// How the work is dealt.  A row goes to a team of 1 << shift lanes, its items of two vectors
+// one a lane, and a workgroup has some tokens' rows at a time.
+struct QkNormTiles {
+  int vec;     // channels of a vector
+  bool tails;  // short vectors occur
+  int per;     // work items of a head
+  int shift;
+  int tokens[2];      // of a workgroup; into 4 bits those of queries and of keys
+  int64_t blocks[3];  // workgroups; into 4 bits those of queries, keys and values follow each other
+};
+QkNormTiles qk_norm_tiles(const QkNormArgs &a, bool reverse);
+
 struct Cache4Rows {
   int64_t rows, num_pages;
   int heads, dim, page, bf16;

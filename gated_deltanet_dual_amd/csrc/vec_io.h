@@ -27,6 +27,20 @@ template <> struct Vec<u16, 8> {
     __builtin_memcpy(p, &v, 16);
   }
 };
+template <> struct Vec<u16, 4> {
+  static __device__ __forceinline__ void load(const u16 *p, float *f) {
+    uint2 v;
+    __builtin_memcpy(&v, p, 8);
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(u16 *p, const float *f) {
+    const uint2 v = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    __builtin_memcpy(p, &v, 8);
+  }
+};
 template <> struct Vec<float, 4> {
   static __device__ __forceinline__ void load(const float *p, float *f) { __builtin_memcpy(f, p, 16); }
   static __device__ __forceinline__ void store(float *p, const float *f) { __builtin_memcpy(p, f, 16); }

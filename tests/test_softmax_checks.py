@@ -57,7 +57,7 @@ def test_forward(L):
     for bad in (dict(tokens=-1), dict(qh=0), dict(kh=-1), dict(dim=0), dict(half=33), dict(half=2 ** 30), dict(qs=127),
                 dict(ks=63), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(kh=0)):
         assert forward(L, **bad) == 2, bad  # kh = 0: a k_weight, but no k heads
-    for bad in (dict(dim=2048, qs=4096, ks=2048), dict(io=7), dict(inter=2), dict(tokens=2 ** 31), dict(tokens=2 ** 24, qh=64, qs=4096)):
+    for bad in (dict(dim=2048, qs=4096, ks=2048), dict(io=7), dict(inter=2), dict(tokens=2 ** 31), dict(tokens=2 ** 24, qh=256, qs=16384)):
         assert forward(L, **bad) == 4, bad
     for bad in ("pos", "freqs", "qo", "ko"):
         assert forward(L, **{bad: None}) == 1, bad
