@@ -127,13 +127,18 @@ def _token_rows(t, name, shape, dtype, dev):
     the elements between tokens (a slice of a wider row has more than its own)."""
     if t is None:
         _fail("%s is required" % name, 1)
+    strides = t.stride()
+    if len(strides) == 3 and t.dtype == dtype and t.shape == shape and t.device == dev:  # the usual case, in short
+        token, head, channel = strides
+        tokens, heads, d = shape
+        if channel == 1 and head == d and (tokens <= 1 or token >= heads * d):
+            return token if tokens > 1 else heads * d
     if t.dtype != dtype:
         _fail("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         _fail("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.device != dev:
         _fail("%s is on %s, expected %s" % (name, t.device, dev))
-    strides = t.stride()
     if shape[0] > 1 and t.is_contiguous():
         return strides[0]
     row = 1
@@ -417,8 +422,10 @@ def _chk_cache(k_cache, v_cache, heads, d, io, dev):
 def _norm_weights(q_weight, k_weight, k, dim, dev):
     if k is None and k_weight is not None:
         _fail("k_weight without k")
-    _chk(q_weight, "q_weight", (dim,), _module.float32, dev, optional=True)
-    _chk(k_weight, "k_weight", (dim,), _module.float32, dev, optional=True)
+    if q_weight is not None:
+        _chk(q_weight, "q_weight", (dim,), _module.float32, dev)
+    if k_weight is not None:
+        _chk(k_weight, "k_weight", (dim,), _module.float32, dev)
 
 
 def qk_norm_rotary(positions, freqs, q, k=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, mscale=1.0,
@@ -515,10 +522,10 @@ def _chk_cache_fp4(cache, name, heads, d, dev):
 
 
 def _chk_caches_fp4(k_cache, v_cache, heads, d, dev):
-    pages, page = _chk_cache_fp4(k_cache, "k_cache", heads, d, dev)
-    if _chk_cache_fp4(v_cache, "v_cache", heads, d, dev) != (pages, page):
+    sizes = _chk_cache_fp4(k_cache, "k_cache", heads, d, dev)
+    if _chk_cache_fp4(v_cache, "v_cache", heads, d, dev) != sizes:
         _fail("k_cache and v_cache have pages of different number or size")
-    return pages, page
+    return sizes
 
 
 def qk_norm_rotary_cache_fp4(positions, freqs, q, k, v, slots, k_cache, v_cache, q_weight=None, k_weight=None, eps=1e-6,
