@@ -77,6 +77,35 @@ def test_forward(g, T, Hq, Hk, d, rot, inter, io, norm):
     same(alone, y.cpu().double())
 
 
+# heads that 64 lanes do not hold at a time, in whole vectors and short ones; vectors of 4 and of 8; heads narrower than a
+# vector; workgroups of many tokens, the last one's fewer
+FORMS = [(6, 2, 1, 1020, 600, False, "bf16", "qk"), (6, 2, 1, 1021, 14, False, "bf16", "qk"), (6, 1, 2, 1024, 1024, True, "bf16", "qk"),
+         (6, 1, 2, 1020, 600, True, "f32", "qk"), (11, 3, 2, 132, 64, True, "bf16", "qk"), (11, 3, 2, 132, 132, False, "bf16", "k"),
+         (9, 5, 3, 3, 2, True, "bf16", "qk"), (9, 5, 3, 3, 2, False, "f32", "qk"), (9, 2, 2, 2, 2, True, "bf16", "qk"),
+         (70001, 1, 1, 16, 16, False, "bf16", "qk"), (3083, 2, 3, 20, 10, True, "bf16", "qk")]
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,rot,inter,io,norm", FORMS)
+def test_forms(g, T, Hq, Hk, d, rot, inter, io, norm):
+    import torch
+    io = types(io)
+    q, k, v, pos, freqs, qw, kw, rnd = make(T + d, T, Hq, Hk, d, rot, io, norm)
+    y, z = g.qk_norm_rotary(pos, freqs, q, k, qw, kw, eps=EPS, interleaved=inter)
+    check_forward(y, q, qw, pos, freqs, inter, 1.0, io, "q")
+    check_forward(z, k, kw, pos, freqs, inter, 1.0, io, "k")
+    dq, dk = rnd(T, Hq, d).to(io), rnd(T, Hk, d).to(io)
+    out = g.qk_norm_rotary_bwd(pos, freqs, q, k, dq, dk, qw, kw, eps=EPS, interleaved=inter)
+    chain = 256 + 64 + max(Hq, Hk) * (1 + T // 256)
+    check_reverse(out, "q", q, qw, dq, pos, freqs, inter, 1.0, io, chain)
+    check_reverse(out, "k", k, kw, dk, pos, freqs, inter, 1.0, io, chain)
+    pages = -(-T // 16) + 1
+    kc, vc = rnd(pages, Hk, 16, d).to(io), rnd(pages, Hk, 16, d).to(io)
+    slots = torch.randperm(pages * 16, device="cuda")[:T]
+    y2 = g.qk_norm_rotary_cache(pos, freqs, q, k, v, slots, kc, vc, qw, kw, eps=EPS, interleaved=inter)
+    flat = lambda c: c.transpose(1, 2).flatten(0, 1)[slots]  # noqa: E731
+    assert y2.equal(y) and flat(kc).equal(z) and flat(vc).equal(v)
+
+
 def gradients64(x, w, dy, pos, freqs, inter, mscale):
     """(dx, dw) and the size of the terms that each is formed of."""
     import torch
@@ -190,7 +219,10 @@ def test_cache(g, T, Hq, Hk, d, rot, inter, io, norm, page):
 # d and Hk of one round of keys through the workgroup's buffer and of several
 FP4_SIZES = [(1, 16, 4, 128, 128, False, "bf16", "qk", 64), (70, 3, 2, 96, 34, True, "f32", "qk", 1), (300, 4, 2, 64, 16, False, "bf16", "k", 16),
              (40, 1, 9, 256, 256, True, "bf16", "qk", 32), (33, 2, 3, 1024, 100, False, "f32", "qk", 16), (9, 2, 40, 32, 0, False, "bf16", "", 7),
-             (2300, 2, 1, 64, 64, False, "bf16", "q", 128), (2100, 1, 8, 160, 160, False, "f32", "qk", 64)]
+             (2300, 2, 1, 64, 64, False, "bf16", "q", 128), (2100, 1, 8, 160, 160, False, "f32", "qk", 64),
+             # heads that 64 lanes do not hold at a time; workgroups of many tokens of one key head
+             (5, 1, 2, 1024, 1024, False, "bf16", "qk", 16), (5, 1, 2, 992, 50, True, "f32", "qk", 16),
+             (66000, 1, 1, 32, 32, True, "bf16", "qk", 64)]
 
 
 def fill(g, pages, heads, page, d, seed):
