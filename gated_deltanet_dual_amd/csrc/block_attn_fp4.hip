@@ -411,18 +411,27 @@ template <int D, int TK> struct CodesToLds {
   __device__ __forceinline__ CodesToLds(const BlockAttnFp4Args &b, int shift, int lane, int wave, int sub, u16 (&kt_lds)[2][TK * D],
                                         u16 (&vt_lds)[2][TK * D])
       : b(b), kt(kt_lds[0]), vt(vt_lds[0]), shift(shift), lane(lane), wave(wave), sub(sub) {}
+  // A lane's row and its quarter.  Eight neighbouring lanes write 16 bytes each to LDS at a
+  // time and want eight places of 128 bytes.  Two rows' four quarters in order meet four of
+  // them (d = 64, 128) or two; so the eight lanes are half quarters of four rows, every other
+  // lane has its halves the other way round (d = 256) and of values, where only even places
+  // change with the row, each two words.  37 requests x 7 x 16 heads of 256 over 2500 + 777
+  // keys: 43 us with those conflicts, half of the LDS' cycles, 37 without.
+  __device__ __forceinline__ static int row_of(int lane) { return D == 64 ? lane >> 2 : (lane >> 1 & 3) | (lane >> 4 << 2); }
+  __device__ __forceinline__ static int quarter_of(int lane) { return D == 64 ? lane & 3 : (lane & 1) | (lane >> 2 & 2); }
   __device__ __forceinline__ void fetch(Codes &x, const void *codes, const uint8_t *scales, int64_t ph, int row) const {
     const uint8_t *c = (const uint8_t *)codes + ((ph << shift) + row) * (D / 2);
     const uint8_t *s = scales + ((ph * (D / 32)) << shift) + row;
-    const uint32_t at = lane >> 2, q = lane & 3, page = 1u << shift;
+    const uint32_t at = row_of(lane), q = quarter_of(lane), page = 1u << shift;
     if constexpr (D == 64) {
       *reinterpret_cast<uint2 *>(x.c) = *reinterpret_cast<const uint2 *>(c + (at * (D / 2) + q * 8));
       x.s[0] = s[(q >> 1) * page + at];
     } else {
 #pragma unroll
       for (int h = 0; h < D / 128; ++h) {
-        *reinterpret_cast<uint4 *>(x.c + 4 * h) = *reinterpret_cast<const uint4 *>(c + (at * (D / 2) + q * (D / 8) + 16 * h));
-        x.s[h] = s[(q * (D / 128) + h) * page + at];
+        const uint32_t half = D == 256 ? h ^ (q & 1) : h;
+        *reinterpret_cast<uint4 *>(x.c + 4 * h) = *reinterpret_cast<const uint4 *>(c + (at * (D / 2) + q * (D / 8) + 16 * half));
+        x.s[h] = s[(q * (D / 128) + half) * page + at];
       }
     }
   }
@@ -436,13 +445,15 @@ template <int D, int TK> struct CodesToLds {
     }
   }
   __device__ __forceinline__ void put(const Codes &x, u16 *tile, bool value) const {
-    const int row = lane >> 2, q = lane & 3;
+    const int row = row_of(lane), q = quarter_of(lane);
     u16 *to = tile + (sub * 16 + row) * D;
+    const bool turn = D == 64 ? row & 1 : value && (q & 1);
+    const int piece = (value ? v_piece<D>(row, W * q) : k_piece<D>(row, W * q)) ^ (D == 256 ? 4 * (q & 1) : 0) ^ (turn ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const uint32_t c = x.c[i], s = x.s[i / 4] << 23;
-      const int piece = value ? v_piece<D>(row, W * q + i) : k_piece<D>(row, W * q + i);
-      *reinterpret_cast<uint4 *>(to + piece * 8) = make_uint4(fp4_pair<0>(c, s), fp4_pair<1>(c, s), fp4_pair<2>(c, s), fp4_pair<3>(c, s));
+      const uint32_t mine = x.c[i], other = x.c[i ^ 1], c = turn ? other : mine, s = x.s[i / 4] << 23;
+      *reinterpret_cast<uint4 *>(to + (piece ^ i) * 8) =
+          make_uint4(fp4_pair<0>(c, s), fp4_pair<1>(c, s), fp4_pair<2>(c, s), fp4_pair<3>(c, s));
     }
   }
   __device__ __forceinline__ void land(int buf) const {

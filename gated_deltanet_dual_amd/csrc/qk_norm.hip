@@ -31,7 +31,7 @@ namespace {
 
 struct QkNormPlan {
   QkNormTiles t;
-  int wave_keys;  // into 4 bits: channels of the rows that a wave has at a time
+  int wave_keys;  // into 4 bits: LDS values of the rows that a wave has at a time
   float inv_dim;
   FastDiv half, q_heads, k_heads;
   FastDiv chunks, v_items;  // into 4 bits: a row's pieces of 8 channels, a token's values' pieces
@@ -440,6 +440,10 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
   items_of<VEC>(p, r, lane, it);
   double *const mine = keys + (threadIdx.x >> 6) * p.wave_keys;
   const int chunks = r.dim / 8, pieces = wave_teams * chunks;
+  // A row lies as [8][chunks + 2], a channel's place in its piece first: lanes that read or
+  // write one channel each of neighbouring pieces, or vectors, meet neighbouring banks.
+  const int wave_row = 8 * (chunks + 2);
+  auto place_in = [&](int c) { return (c & 7) * (chunks + 2) + (c >> 3); };
   using Raws = Raw<IO, VEC>[NI][2];
   auto load = [&](int row, Raws &to) {
     if (row >= rows) row = rows - 1;
@@ -464,7 +468,7 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
 #pragma unroll
             for (int e = 0; e < VEC; ++e) y[i][h][e] = x[i][h][e];
       }
-      double *const to = mine + wave_team * r.dim;
+      double *const to = mine + wave_team * wave_row;
       const double2 *const cf = coef + fast_div(row, p.k_heads) * (r.half + kCoefMore);
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -472,8 +476,8 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
           turn_item<VEC, TAIL>(it[i], r.interleaved, cf, y[i]);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            if (!TAIL || e < it[i].n0) to[it[i].c0 + e] = y[i][0][e];
-            if (e < it[i].n1) to[it[i].c1 + e] = y[i][1][e];
+            if (!TAIL || e < it[i].n0) to[place_in(it[i].c0 + e)] = y[i][0][e];
+            if (e < it[i].n1) to[place_in(it[i].c1 + e)] = y[i][1][e];
           }
         }
     }
@@ -485,7 +489,7 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
         const int t = fast_div(row0 + j, p.k_heads), head = row0 + j - t * r.k_heads;
         double x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = mine[j * r.dim + 8 * chunk + e];
+        for (int e = 0; e < 8; ++e) x[e] = mine[j * wave_row + e * (chunks + 2) + chunk];
         store_fp4(a.k4, r, place[t], head, chunk, x);
       }
     }
@@ -699,7 +703,7 @@ QkNormPlan plan_of(const QkNormArgs &a, const QkNormTiles &t) {
   const RotaryArgs &r = a.r;
   QkNormPlan p{};
   p.t = t;
-  p.wave_keys = (64 >> t.shift) * r.dim;
+  p.wave_keys = (64 >> t.shift) * (r.dim + 16);
   p.inv_dim = 1.0f / (float)r.dim;
   p.half = make_fast_div(r.half > 0 ? r.half : 1);
   p.q_heads = make_fast_div(r.q_heads);
