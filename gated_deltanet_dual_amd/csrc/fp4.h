@@ -8,36 +8,39 @@ namespace flare {
 
 constexpr int kFp4Group = 32;  // channels that share a scale
 
+// What of a double decides its code and its group's scale, borders of few bits: the upper
+// half, its last bit set where the lower one is not zero.
+struct Upper {
+  uint32_t w;
+};
+__device__ __forceinline__ Upper upper(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  return {(uint32_t)(b >> 32) | ((uint32_t)b != 0 ? 1u : 0u)};
+}
+
 // The magnitude's bits, ordered as the magnitudes are, NaN above all.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-__device__ __forceinline__ uint64_t abs_bits(double x) { return (uint64_t)__double_as_longlong(x) & 0x7fffffffffffffffull; }
+__device__ __forceinline__ uint32_t abs_bits(Upper x) { return x.w & 0x7fffffffu; }
 
 // The scale of a group whose largest magnitude has these bits: its exponent less two
 // (the largest code is 6 = 1.5 2^2), and one more where the largest value is above 7
 // units: 7 is cut to 6, as far as half a step there, and more would be cut further.  1 to
 // 252, so that every value is a normal finite bf16 or the subnormal it would be; 255: the
 // group holds an infinity or NaN, and is NaN.
-__device__ __forceinline__ int fp4_scale(uint32_t top) {
-  if (top >= 0x7f800000u) return 255;
-  const int e = (int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x600000u);
-  return e < 1 ? 1 : e > 252 ? 252 : e;
-}
-__device__ __forceinline__ int fp4_scale(uint64_t top) {
-  if (top >= 0x7ff0000000000000ull) return 255;
-  const int e = (int)(top >> 52) - 1023 + 127 - 2 + ((top & 0xfffffffffffffull) > 0xc000000000000ull);
+template <typename T> __device__ __forceinline__ int fp4_scale(uint32_t top) {
+  constexpr int kMantissa = __is_same(T, Upper) ? 20 : 23, kBias = __is_same(T, Upper) ? 1023 : 127;
+  if (top >= (uint32_t)(2 * kBias + 1) << kMantissa) return 255;
+  const int e = (int)(top >> kMantissa) - kBias + 127 - 2 + ((top & ((1u << kMantissa) - 1)) > 3u << (kMantissa - 2));
   return e < 1 ? 1 : e > 252 ? 252 : e;
 }
 
-// x / 2^(byte - 127) as a float whose rounding to a code is x's: a double goes to the odd
-// one of its two neighbours, so that what is halfway between codes in 32 bits is so in 64.
+// x / 2^(byte - 127) as a float whose rounding to a code is x's: exact, or with as many bits
+// as a border's and a last one that keeps it off the border.
 __device__ __forceinline__ float fp4_units(float x, int byte) { return x * __uint_as_float((uint32_t)(254 - byte) << 23); }
-__device__ __forceinline__ float fp4_units(double x, int byte) {
-  const double z = x * (double)__uint_as_float((uint32_t)(254 - byte) << 23);
-  const float f = (float)z;
-  const double back = (double)f;
-  uint32_t b = __float_as_uint(f);
-  if (back != z) b = (b - (fabs(back) > fabs(z) ? 1u : 0u)) | 1u;
-  return __uint_as_float(b);
+__device__ __forceinline__ float fp4_units(Upper x, int byte) {
+  // the exponent's bias changed, below 2^-127 to 0 and beyond 2^80 to that
+  const int v = (int)(x.w & 0x7fffffffu) - ((1023 - 254 + byte) << 20), top = 207 << 20;
+  return __uint_as_float((uint32_t)(v < 0 ? 0 : v > top ? top : v) << 3 | (x.w & 0x80000000u));
 }
 
 // The codes of eight channels, halfway to the even code, beyond 6 to 6.

@@ -209,9 +209,6 @@ template <typename T> __device__ __forceinline__ T team_sum(T x, int shift) {
   return x;
 }
 
-__device__ __forceinline__ uint32_t xor_lane(uint32_t x, int o) { return __shfl_xor(x, o); }
-__device__ __forceinline__ uint64_t xor_lane(uint64_t x, int o) { return __shfl_xor((unsigned long long)x, o); }
-
 // A token's page and row in it; page < 0: nowhere.
 __device__ __forceinline__ int2 place_of(const RotaryArgs &r, int64_t tok) {
   const int64_t slot = r.slots[tok], all = r.num_pages * r.page;
@@ -223,18 +220,18 @@ __device__ __forceinline__ int2 place_of(const RotaryArgs &r, int64_t tok) {
 // Eight channels of a row into 4 bits: four neighbouring lanes hold a group of 32.
 template <typename T>
 __device__ __forceinline__ void store_fp4(const Cache4 &to, const RotaryArgs &r, int2 at, int head, int chunk, const T (&x)[8]) {
-  auto top = abs_bits(x[0]);
+  uint32_t top = abs_bits(x[0]);
 #pragma unroll
   for (int e = 1; e < 8; ++e) {
-    const auto b = abs_bits(x[e]);
+    const uint32_t b = abs_bits(x[e]);
     top = b > top ? b : top;
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    const auto b = xor_lane(top, o);
+    const uint32_t b = __shfl_xor(top, o);
     top = b > top ? b : top;
   }
-  const int byte = fp4_scale(top);
+  const int byte = fp4_scale<T>(top);
   const uint32_t codes = fp4_codes(x, byte);
   if (at.x < 0) return;
   const int64_t ph = (int64_t)at.x * r.k_heads + head;
@@ -430,7 +427,7 @@ __device__ __forceinline__ void wave_lds_ready() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 template <typename IO, int VEC, bool TAIL, int NI>
-__device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPlan &p, int block, float *weights, double2 *coef, int2 *place, double *keys) {
+__device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPlan &p, int block, float *weights, double2 *coef, int2 *place, Upper *keys) {
   const RotaryArgs &r = a.r;
   const int64_t t0 = (int64_t)block * p.t.tokens[1];
   const int n = (int)(r.tokens - t0 < p.t.tokens[1] ? r.tokens - t0 : p.t.tokens[1]);
@@ -438,7 +435,7 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
   const int in_wave = threadIdx.x & 63, wave_team = in_wave >> shift, wave_teams = 64 >> shift, rows = n * r.k_heads;
   Item it[NI];
   items_of<VEC>(p, r, lane, it);
-  double *const mine = keys + (threadIdx.x >> 6) * p.wave_keys;
+  Upper *const mine = keys + (threadIdx.x >> 6) * p.wave_keys;
   const int chunks = r.dim / 8, pieces = wave_teams * chunks;
   // A row lies as [8][chunks + 2], a channel's place in its piece first: lanes that read or
   // write one channel each of neighbouring pieces, or vectors, meet neighbouring banks.
@@ -468,7 +465,7 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
 #pragma unroll
             for (int e = 0; e < VEC; ++e) y[i][h][e] = x[i][h][e];
       }
-      double *const to = mine + wave_team * wave_row;
+      Upper *const to = mine + wave_team * wave_row;
       const double2 *const cf = coef + fast_div(row, p.k_heads) * (r.half + kCoefMore);
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -476,8 +473,8 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
           turn_item<VEC, TAIL>(it[i], r.interleaved, cf, y[i]);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            if (!TAIL || e < it[i].n0) to[place_in(it[i].c0 + e)] = y[i][0][e];
-            if (e < it[i].n1) to[place_in(it[i].c1 + e)] = y[i][1][e];
+            if (!TAIL || e < it[i].n0) to[place_in(it[i].c0 + e)] = upper(y[i][0][e]);
+            if (e < it[i].n1) to[place_in(it[i].c1 + e)] = upper(y[i][1][e]);
           }
         }
     }
@@ -487,7 +484,7 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
       const int j = fast_div(i, p.chunks), chunk = i - j * chunks;
       if (row0 + j < rows) {
         const int t = fast_div(row0 + j, p.k_heads), head = row0 + j - t * r.k_heads;
-        double x[8];
+        Upper x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = mine[j * wave_row + e * (chunks + 2) + chunk];
         store_fp4(a.k4, r, place[t], head, chunk, x);
@@ -528,7 +525,7 @@ __device__ __forceinline__ void values_to_fp4(const QkNormArgs &a, const QkNormP
 
 template <typename IO, int VEC, bool TAIL, int NI, int OUT>
 __global__ __launch_bounds__(256) void qk_norm_rotary_kernel(QkNormArgs a, QkNormPlan p) {
-  extern __shared__ __align__(16) char lds[];  // weights, coefficients, places, keys in 64 bits
+  extern __shared__ __align__(16) char lds[];  // weights, coefficients, places, keys on their way to codes
   float *const weights = reinterpret_cast<float *>(lds);
   char *const rest = lds + 2 * weight_floats(a.r.dim) * sizeof(float);
   float2 *const coef = reinterpret_cast<float2 *>(rest);
@@ -541,7 +538,7 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_kernel(QkNormArgs a, QkNor
     } else if ((block -= p.t.blocks[0]) < p.t.blocks[1]) {
       double2 *const coef64 = reinterpret_cast<double2 *>(rest);
       int2 *const place = reinterpret_cast<int2 *>(coef64 + p.t.tokens[1] * (a.r.half + kCoefMore));
-      keys_to_fp4<IO, VEC, TAIL, NI>(a, p, block, weights, coef64, place, reinterpret_cast<double *>(place + p.t.tokens[1]));
+      keys_to_fp4<IO, VEC, TAIL, NI>(a, p, block, weights, coef64, place, reinterpret_cast<Upper *>(place + p.t.tokens[1]));
     } else {
       values_to_fp4<IO>(a, p, block - p.t.blocks[1]);
     }
@@ -720,7 +717,7 @@ template <typename IO, int VEC, bool TAIL, int OUT> void forward(const QkNormArg
   size_t lds = weights + (size_t)t.tokens[0] * (sizeof(float2) * (r.half + kCoefMore) + sizeof(int2));
   if (OUT == PAGES4) {
     const size_t keys = weights + (size_t)t.tokens[1] * (sizeof(double2) * (r.half + kCoefMore) + sizeof(int2)) +
-                        4 * p.wave_keys * sizeof(double);
+                        4 * p.wave_keys * sizeof(Upper);
     if (lds < keys) lds = keys;
   }
   const int grid = (int)(t.blocks[0] + t.blocks[1] + t.blocks[2]);
