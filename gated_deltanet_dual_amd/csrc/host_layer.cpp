@@ -330,8 +330,8 @@ flare_status check_qk_norm(const QkNormArgs &a, int64_t tokens) {
 
 // Tokens a workgroup: `rounds` rows a team, while enough workgroups are left and the
 // coefficients stay few.
-static int qk_norm_block_tokens(const QkNormTiles &t, const RotaryArgs &r, int heads, int rounds, int64_t blocks) {
-  const int teams = 256 >> t.shift;
+static int qk_norm_block_tokens(int shift, const RotaryArgs &r, int heads, int rounds, int64_t blocks) {
+  const int teams = 256 >> shift;
   int n = 1;
   while (n < 64 && n * heads < rounds * teams && r.tokens / (n + 1) >= blocks && (n + 1) * r.half <= 1024) ++n;
   return n;
@@ -342,27 +342,32 @@ QkNormTiles qk_norm_tiles(const QkNormArgs &a, bool reverse) {
   // Short vectors where a head's parts are no whole ones.  Of 2-byte rows the forward takes
   // 16 bytes a vector, which has fewer instructions a row; 64-bit keys and the weights'
   // gradients' sums fill the registers, and 8 bytes leave room for twice the waves: 32768
-  // tokens of 20 heads of 128 forward 61 us and 67, reverse 145 and 136 (16 and 8 bytes).
+  // tokens of 20 heads of 128 forward 61 us and 67, reverse 145 and 136 (16 and 8 bytes);
+  // 16384 tokens into 4 bits with the queries' rows by 16 or by 8 bytes 53 us and 58.
   const int parts = (r.interleaved ? 2 * r.half : r.half) | (r.dim - 2 * r.half) | r.dim;
   QkNormTiles t{};
-  t.vec = r.bf16 && !reverse && !a.into4 && parts % 8 == 0 ? 8 : 4;
+  t.vec = r.bf16 && !reverse && parts % 8 == 0 ? 8 : 4;
   t.tails = parts % t.vec != 0;
-  t.per = rotary_turned_items(r, t.vec) + rotary_copy_items(r.dim - 2 * r.half, t.vec);
-  while (t.shift < 6 && 1 << t.shift < t.per) ++t.shift;
-  // Rows a team, same case: 1, 2, 4, 8 of them forward 66, 61, 62, 64 us, reverse 163, 136,
-  // 119, 120.  Keys into 4 bits, whose angles in 64 bits are dear, 16384 tokens, queries'
-  // rows 4 each: 4 of them 73, 8 70; and fewer workgroups of queries, which share the CUs with
-  // the keys' and values': 1024 tokens, at least 1024 12.0, 512 11.  Fewer workgroups in the reverse mode, for each writes
-  // a row of either weight's sums: 1531 tokens of 9 heads of 80, 1024 of them 29, 512 20, 256 22.
+  auto lanes = [&r](int vec, int &per, int &shift) {
+    per = rotary_turned_items(r, vec) + rotary_copy_items(r.dim - 2 * r.half, vec);
+    while (shift < 6 && 1 << shift < per) ++shift;
+  };
+  lanes(t.vec, t.per, t.shift);
+  lanes(4, t.key_per, t.key_shift);
+  // Rows a team, 32768 tokens: 1, 2, 4, 8 of them forward 66, 61, 62, 64 us, reverse 163, 136,
+  // 119, 120.  At least as many workgroups as keep the CUs busy, fewer where queries', keys'
+  // and values' go side by side (1024 tokens into 4 bits, 1024 of the queries' and of the
+  // keys' 12.0, 512 10.2 us) and in the reverse mode, where each writes a row of either
+  // weight's sums (1531 tokens of 9 heads of 80, 1024 29, 512 20, 256 22 us).
   if (reverse) {
-    t.tokens[0] = qk_norm_block_tokens(t, r, r.q_heads + r.k_heads, 4, 512);
+    t.tokens[0] = qk_norm_block_tokens(t.shift, r, r.q_heads + r.k_heads, 4, 512);
     t.blocks[0] = std::min(ceil_div(r.tokens, t.tokens[0]), qk_norm_bwd_blocks(r.tokens));
   } else {
-    t.tokens[0] = qk_norm_block_tokens(t, r, r.q_heads + (a.into4 ? 0 : r.k_heads * (r.slots ? 2 : 1)), 4, a.into4 ? 512 : 1024);
+    t.tokens[0] = qk_norm_block_tokens(t.shift, r, r.q_heads + (a.into4 ? 0 : r.k_heads * (r.slots ? 2 : 1)), 4, a.into4 ? 512 : 1024);
     t.blocks[0] = ceil_div(r.tokens, t.tokens[0]);
   }
   if (a.into4) {
-    t.tokens[1] = qk_norm_block_tokens(t, r, r.k_heads, 8, 1024);
+    t.tokens[1] = qk_norm_block_tokens(t.key_shift, r, r.k_heads, 4, 512);
     t.blocks[1] = ceil_div(r.tokens, t.tokens[1]);
     t.blocks[2] = std::min<int64_t>(ceil_div(r.tokens * r.k_heads * (r.dim / 8), 256), 1 << 20);
   }

@@ -109,6 +109,7 @@ struct QkNormTiles {
   bool tails;  // short vectors occur
   int per;     // work items of a head
   int shift;
+  int key_per, key_shift;  // of keys into 4 bits, whose vectors have 4 channels
   int tokens[2];      // of a workgroup; into 4 bits those of queries and of keys
   int64_t blocks[3];  // workgroups; into 4 bits those of queries, keys and values follow each other
 };

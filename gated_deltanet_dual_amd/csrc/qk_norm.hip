@@ -281,11 +281,11 @@ __device__ __forceinline__ void unpack_row(const Raw<IO, VEC> (&from)[NI][2], co
   }
 }
 // This lane's items of a head; one that it does not have has no channels.
-template <int VEC, int NI> __device__ __forceinline__ void items_of(const QkNormPlan &p, const RotaryArgs &r, int lane, Item (&it)[NI]) {
+template <int VEC, int NI> __device__ __forceinline__ void items_of(int per, int shift, const RotaryArgs &r, int lane, Item (&it)[NI]) {
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    it[i] = item_of<VEC>(r, lane + (i << p.t.shift));
-    if (lane + (i << p.t.shift) >= p.t.per) it[i] = Item{0, 0, 0, 0, false};
+    it[i] = item_of<VEC>(r, lane + (i << shift));
+    if (lane + (i << shift) >= per) it[i] = Item{0, 0, 0, 0, false};
   }
 }
 // Both weights to LDS, each in its own weight_floats(dim) with zeros at their end.
@@ -329,7 +329,7 @@ __device__ __forceinline__ void forward_rows(const QkNormArgs &a, const QkNormPl
   const int shift = p.t.shift, lane = threadIdx.x & ((1 << shift) - 1), team = threadIdx.x >> shift, teams = 256 >> shift;
   const int nq = n * r.q_heads, nk = keys ? n * r.k_heads : 0, rows = nq + nk + (OUT == PAGES ? nk : 0);
   Item turned[NI], copied[NI];
-  items_of<VEC>(p, r, lane, turned);
+  items_of<VEC>(p.t.per, p.t.shift, r, lane, turned);
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     copied[i] = copy_of<VEC>(r, lane + (i << shift));
@@ -416,11 +416,12 @@ __device__ __forceinline__ void forward_rows(const QkNormArgs &a, const QkNormPl
 
 // Keys into 4 bits: computed in 64 bits from their norm's sum to the rounding, so that a
 // value next to the border of two codes, half a step apart, goes to the right one, which 32
-// bits would miss once in some 10^7 values.  They pass through LDS, a wave's own part of it,
+// bits would miss once in some 10^5 values.  They pass through LDS, a wave's own part of it,
 // where groups of 32 channels lie together whatever pairs were turned.  16384 tokens of 16
-// query, 4 key and 4 value heads of 128: 60 to 64 us (2.5 TB/s); the keys' arithmetic in 64
-// bits, at half the rate and with twice the registers, bounds it: without the queries' rows it
-// is no shorter.  As fp32 throughout it was 20 us less.
+// query, 4 key and 4 value heads of 128: 50 to 53 us (2.9 TB/s), bound by instructions: the
+// queries and values alone are 38, the keys and values 25, and waves of both share the SIMDs.
+// (fp32 first, its errors bounded, and 64 bits for the waves that have a value near a border,
+// one in 50: 66 us, for most workgroups have such a wave and wait for it.)
 __device__ __forceinline__ void wave_lds_ready() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -431,10 +432,10 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
   const RotaryArgs &r = a.r;
   const int64_t t0 = (int64_t)block * p.t.tokens[1];
   const int n = (int)(r.tokens - t0 < p.t.tokens[1] ? r.tokens - t0 : p.t.tokens[1]);
-  const int shift = p.t.shift, lane = threadIdx.x & ((1 << shift) - 1), teams = 256 >> shift;
+  const int shift = p.t.key_shift, lane = threadIdx.x & ((1 << shift) - 1), teams = 256 >> shift;
   const int in_wave = threadIdx.x & 63, wave_team = in_wave >> shift, wave_teams = 64 >> shift, rows = n * r.k_heads;
   Item it[NI];
-  items_of<VEC>(p, r, lane, it);
+  items_of<VEC>(p.t.key_per, shift, r, lane, it);
   Upper *const mine = keys + (threadIdx.x >> 6) * p.wave_keys;
   const int chunks = r.dim / 8, pieces = wave_teams * chunks;
   // A row lies as [8][chunks + 2], a channel's place in its piece first: lanes that read or
@@ -534,11 +535,11 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_kernel(QkNormArgs a, QkNor
   } else {
     int block = blockIdx.x;
     if (block < p.t.blocks[0]) {
-      forward_rows<IO, VEC, TAIL, NI, PACKED>(a, p, block, false, weights, coef, nullptr);
+      forward_rows<IO, VEC, TAIL, VEC == 8 ? 1 : NI, PACKED>(a, p, block, false, weights, coef, nullptr);
     } else if ((block -= p.t.blocks[0]) < p.t.blocks[1]) {
       double2 *const coef64 = reinterpret_cast<double2 *>(rest);
       int2 *const place = reinterpret_cast<int2 *>(coef64 + p.t.tokens[1] * (a.r.half + kCoefMore));
-      keys_to_fp4<IO, VEC, TAIL, NI>(a, p, block, weights, coef64, place, reinterpret_cast<Upper *>(place + p.t.tokens[1]));
+      keys_to_fp4<IO, 4, TAIL, NI>(a, p, block, weights, coef64, place, reinterpret_cast<Upper *>(place + p.t.tokens[1]));
     } else {
       values_to_fp4<IO>(a, p, block - p.t.blocks[1]);
     }
@@ -558,7 +559,7 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
   const RotaryArgs &r = a.r;
   const int shift = p.t.shift, lane = threadIdx.x & ((1 << shift) - 1), team = threadIdx.x >> shift, teams = 256 >> shift;
   Item it[NI];
-  items_of<VEC>(p, r, lane, it);
+  items_of<VEC>(p.t.per, shift, r, lane, it);
   float dw[2][NI][2][VEC] = {};
   const int step = p.t.tokens[0], each = step * (r.half + kCoefMore);
   auto count = [&](int64_t t0) { return t0 >= r.tokens ? 0 : (int)(r.tokens - t0 < step ? r.tokens - t0 : step); };
@@ -665,7 +666,9 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
   }
 }
 
-// Rows of a cache in 4 bits as bf16 or fp32: 8 channels a thread.
+// Rows of a cache in 4 bits as bf16 or fp32: 8 channels a thread.  16576 rows of 4 heads of
+// 128, keys and values: 12.6 us, 3.5 TB/s, of which a launch's start and end are a third; 1152
+// rows 3.3 us.
 template <typename IO>
 __global__ __launch_bounds__(256) void cache_fp4_rows_kernel(Cache4Rows a, FastDiv chunks, FastDiv row_items) {
   const int per_row = a.heads * (a.dim / 8);
@@ -700,7 +703,7 @@ QkNormPlan plan_of(const QkNormArgs &a, const QkNormTiles &t) {
   const RotaryArgs &r = a.r;
   QkNormPlan p{};
   p.t = t;
-  p.wave_keys = (64 >> t.shift) * (r.dim + 16);
+  p.wave_keys = (64 >> t.key_shift) * (r.dim + 16);
   p.inv_dim = 1.0f / (float)r.dim;
   p.half = make_fast_div(r.half > 0 ? r.half : 1);
   p.q_heads = make_fast_div(r.q_heads);
@@ -721,22 +724,16 @@ template <typename IO, int VEC, bool TAIL, int OUT> void forward(const QkNormArg
     if (lds < keys) lds = keys;
   }
   const int grid = (int)(t.blocks[0] + t.blocks[1] + t.blocks[2]);
-  // vectors of 8 channels: 64 lanes have a whole head of 1024
-  if (VEC == 8 || t.per <= 1 << t.shift) qk_norm_rotary_kernel<IO, VEC, TAIL, 1, OUT><<<grid, 256, lds, st>>>(a, p);
-  else if constexpr (VEC == 4) qk_norm_rotary_kernel<IO, VEC, TAIL, 3, OUT><<<grid, 256, lds, st>>>(a, p);
+  // of vectors of 8 channels 64 lanes have a whole head of 1024, but not of its keys into 4 bits
+  if (OUT == PAGES4 ? t.key_per <= 1 << t.key_shift : t.per <= 1 << t.shift)
+    qk_norm_rotary_kernel<IO, VEC, TAIL, 1, OUT><<<grid, 256, lds, st>>>(a, p);
+  else if constexpr (VEC == 4 || OUT == PAGES4) qk_norm_rotary_kernel<IO, VEC, TAIL, 3, OUT><<<grid, 256, lds, st>>>(a, p);
 }
 template <int OUT> void forward_form(const QkNormArgs &a, hipStream_t st) {
   const QkNormTiles t = qk_norm_tiles(a, false);
-  if (!a.r.bf16) {
-    if (t.tails) forward<float, 4, true, OUT>(a, t, st);
-    else forward<float, 4, false, OUT>(a, t, st);
-  } else if (t.tails) {
-    forward<u16, 4, true, OUT>(a, t, st);
-  } else if (t.vec == 4) {
-    forward<u16, 4, false, OUT>(a, t, st);
-  } else if constexpr (OUT != PAGES4) {
-    forward<u16, 8, false, OUT>(a, t, st);
-  }
+  if (!a.r.bf16) t.tails ? forward<float, 4, true, OUT>(a, t, st) : forward<float, 4, false, OUT>(a, t, st);
+  else if (t.tails) forward<u16, 4, true, OUT>(a, t, st);
+  else t.vec == 8 ? forward<u16, 8, false, OUT>(a, t, st) : forward<u16, 4, false, OUT>(a, t, st);
 }
 
 template <typename IO, bool TAIL> void reverse(const QkNormArgs &a, const QkNormTiles &t, hipStream_t st) {

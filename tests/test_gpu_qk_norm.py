@@ -222,7 +222,7 @@ FP4_SIZES = [(1, 16, 4, 128, 128, False, "bf16", "qk", 64), (70, 3, 2, 96, 34, T
              (2300, 2, 1, 64, 64, False, "bf16", "q", 128), (2100, 1, 8, 160, 160, False, "f32", "qk", 64),
              # heads that 64 lanes do not hold at a time; workgroups of many tokens of one key head
              (5, 1, 2, 1024, 1024, False, "bf16", "qk", 16), (5, 1, 2, 992, 50, True, "f32", "qk", 16),
-             (66000, 1, 1, 32, 32, True, "bf16", "qk", 64)]
+             (66000, 1, 1, 32, 32, True, "bf16", "qk", 64), (50, 3, 2, 128, 120, False, "bf16", "qk", 16)]
 
 
 def fill(g, pages, heads, page, d, seed):

@@ -94,7 +94,7 @@ def test_every_form_is_launched(calls):
             for d, half in ((128, 64), (132, 64), (80, 25), (1024, 512), (1020, 300), (1021, 7)):
                 todo.append(call(op, tokens=100, d=d, half=half, io=io))
     for io in (g.BF16, g.F32):
-        for d, half in ((128, 64), (128, 25), (1024, 512), (1024, 25)):
+        for d, half in ((128, 64), (128, 60), (128, 25), (1024, 512), (1024, 508), (1024, 25)):
             todo.append(call("cache4", tokens=100, d=d, half=half, io=io))
         todo.append(call("rows", tokens=100, io=io))
     for d in (64, 128, 256):
