@@ -93,7 +93,7 @@ namespace {
 // What a key costs a workgroup, in tenths of a nanosecond: alone on its CU, its share of a
 // CU's instructions that several keep busy, and its share of memory's time where no other
 // row group reads it.  Measured: the shared form of two row tiles at d = 128, 4096 keys 106 us
-// alone, 4 x 2048 keys 80 us two a CU; d = 256, one: 2 x 2048 133 us; d = 64, two: 4 x 1024 60
+// alone, 4 x 2048 keys 80 us two a CU; d = 256, one: 2 x 2048 111 us; d = 64, two: 4 x 1024 60
 // us four a CU.  The other form, one row tile at d = 128, 4096 keys 29 us where every CU has
 // one, 2 x 2048 24 us.
 struct KeyCost {
@@ -102,7 +102,7 @@ struct KeyCost {
 KeyCost key_cost(bool shared, int tiles, int dim) {
   const int memory = dim / 2 - dim / 64;  // 17 / 16 of a byte a channel, at 4.4 TB/s over 256 CUs
   if (shared) {
-    if (dim == 256) return {450, 325, memory};
+    if (dim == 256) return {390, 275, memory};
     if (dim == 64) return tiles == 2 ? KeyCost{180, 146, memory} : KeyCost{120, 90, memory};
     return tiles == 2 ? KeyCost{260, 195, memory} : KeyCost{176, 120, memory};
   }
