@@ -16,8 +16,8 @@
 // waits for all before it as well.  32768 tokens of 16 query and 4 key heads of 128 in
 // bf16: forward 62 us (5.4 TB/s; 92 with loads and weights in turn), reverse 119 us
 // (4.2 TB/s; 167), where its instructions, some 35 a channel, weigh as much.  Short
-// vectors cost: heads of 80, 50 channels turned as halves, 71 and 181 us.  Below some
-// 2000 tokens the chain of a workgroup's loads bounds it: 1024 tokens 7.4 and 16 us.
+// vectors cost: heads of 80, 50 channels turned as halves, 71 and 115 us.  Below some
+// 2000 tokens the chain of a workgroup's loads bounds it: 1024 tokens 7.3 and 14.6 us.
 #include <hip/hip_runtime.h>
 
 #include "fast_div.h"
@@ -555,7 +555,7 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
   extern __shared__ __align__(16) char lds[];
   float *const weights = reinterpret_cast<float *>(lds);
   float2 *const coefs = reinterpret_cast<float2 *>(weights + 2 * weight_floats(a.r.dim));  // [2][tokens][half]
-  __shared__ float cols[256 * VEC];
+  __shared__ float cols[2][2][256 * VEC];
   const RotaryArgs &r = a.r;
   const int shift = p.t.shift, lane = threadIdx.x & ((1 << shift) - 1), team = threadIdx.x >> shift, teams = 256 >> shift;
   Item it[NI];
@@ -642,26 +642,25 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
     pass(std::integral_constant<int, 1>(), t0, count(t0), coef, [] {});
     __syncthreads();
   }
-  // the teams' sums, a vector of every thread at a time
+  // the teams' sums, an item of every thread at a time: of both kinds, both vectors
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    if (!a.weight[kind]) continue;
-    float *out = a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * r.dim;
+  for (int i = 0; i < NI; ++i) {
+    if (i > 0) __syncthreads();
 #pragma unroll
-    for (int v = 0; v < 2 * NI; ++v) {
-      __syncthreads();
+    for (int kv = 0; kv < 4; ++kv)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) cols[threadIdx.x * VEC + e] = dw[kind][v / 2][v % 2][e];
-      __syncthreads();
-      for (int j = threadIdx.x; j < VEC << shift; j += 256) {
-        const int item = j / VEC + (v / 2 << shift), e = j % VEC;
-        if (item >= p.t.per) continue;
-        const Item at = item_of<VEC>(r, item);
-        if (e >= (v % 2 ? at.n1 : at.n0)) continue;
-        float s = 0.0f;
-        for (int k = 0; k < teams; ++k) s += cols[(k << shift) * VEC + j];
-        out[(v % 2 ? at.c1 : at.c0) + e] = s;
-      }
+      for (int e = 0; e < VEC; ++e) cols[kv / 2][kv % 2][threadIdx.x * VEC + e] = dw[kv / 2][i][kv % 2][e];
+    __syncthreads();
+    const int width = VEC << shift;
+    for (int j = threadIdx.x; j < 4 * width; j += 256) {
+      static_assert(VEC == 4);
+      const int kv = j >> shift >> 2, kind = kv >> 1, h = kv & 1, at = j & (width - 1), item = at / VEC + (i << shift), e = at % VEC;
+      if (!(kind ? a.weight[1] : a.weight[0]) || item >= p.t.per) continue;
+      const Item part = item_of<VEC>(r, item);
+      if (e >= (h ? part.n1 : part.n0)) continue;
+      float s = 0.0f;
+      for (int k = 0; k < teams; ++k) s += cols[kind][h][(k << shift) * VEC + at];
+      a.part[((int64_t)kind * gridDim.x + blockIdx.x) * r.dim + (h ? part.c1 : part.c0) + e] = s;
     }
   }
 }

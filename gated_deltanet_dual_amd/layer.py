@@ -564,9 +564,8 @@ def cache_fp4_rows(slots, k_cache, v_cache=None, dtype=None, out=None):
     if not isinstance(k_cache, (tuple, list)) or len(k_cache) != 2 or k_cache[0] is None or k_cache[0].dim() != 4:
         _fail("k_cache must be (codes, scales)")
     heads, d = k_cache[0].shape[1], 2 * k_cache[0].shape[3]
-    pages, page = _chk_cache_fp4(k_cache, "k_cache", heads, d, dev)
-    if v_cache is not None:
-        _chk_caches_fp4(k_cache, v_cache, heads, d, dev)
+    pages, page = (_chk_cache_fp4(k_cache, "k_cache", heads, d, dev) if v_cache is None
+                   else _chk_caches_fp4(k_cache, v_cache, heads, d, dev))
     ko, vo = (None, None) if out is None else out if v_cache is not None else (out, None)
     ko = _out(ko, "k out", (T, heads, d), io, dev)
     vo = _out(vo, "v out", (T, heads, d), io, dev) if v_cache is not None else None
