@@ -16,8 +16,8 @@
 // waits for all before it as well.  32768 tokens of 16 query and 4 key heads of 128 in
 // bf16: forward 62 us (5.4 TB/s; 92 with loads and weights in turn), reverse 119 us
 // (4.2 TB/s; 167), where its instructions, some 35 a channel, weigh as much.  Short
-// vectors cost: heads of 80, 50 channels turned as halves, 71 and 115 us.  Below some
-// 2000 tokens the chain of a workgroup's loads bounds it: 1024 tokens 7.3 and 14.6 us.
+// vectors cost: heads of 80, 50 channels turned as halves, 71 and 106 us.  Below some
+// 2000 tokens the chain of a workgroup's loads bounds it: 1024 tokens 7.1 and 15 us.
 #include <hip/hip_runtime.h>
 
 #include "fast_div.h"
@@ -403,6 +403,10 @@ __device__ __forceinline__ void forward_rows(const QkNormArgs &a, const QkNormPl
   form_coefficients(coef, r, p.half, t0, n);
   if (OUT != PACKED && (int)threadIdx.x < n) place[threadIdx.x] = place_of(r, t0 + threadIdx.x);
   __syncthreads();
+  if (rows <= teams) {  // nothing to have under way
+    if (team < rows) finish(w0, x0);
+    return;
+  }
   for (int row = team; row < rows; row += 2 * teams) {
     w1 = row_at(row + teams < rows ? row + teams : row);
     load(w1, x1);
@@ -622,6 +626,10 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
     Raws x0, d0, x1, d1;
     if (rows > 0) load(team < rows ? team : 0, x0, d0);
     between();
+    if (rows <= teams) {
+      if (team < rows) finish(team, x0, d0);
+      return;
+    }
     for (int row = team; row < rows; row += 2 * teams) {
       load(row + teams < rows ? row + teams : row, x1, d1);
       finish(row, x0, d0);
