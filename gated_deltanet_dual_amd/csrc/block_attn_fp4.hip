@@ -13,14 +13,24 @@
 // their products to 2^-14 of the largest only: scores off by 5e-6 of themselves where bf16
 // products are off by 1e-8.)
 //
-// 4 bits make the operands small enough to need no LDS: a lane loads 32 codes of one key
-// as 16 bytes, which are its share of the first product's operand (each lane group takes
-// the channels that its bytes hold, the queries' are laid out alike); and for the second
-// product it loads, of each of its 8 keys, the codes of D / 16 neighbouring channels,
-// converts them and exchanges halves of registers in pairs, so that it holds 8 keys of one
-// channel for each of D / 16 products, whose rows are every (D / 16)-th channel.  So the
-// waves of a workgroup share nothing while they pass the keys: each takes every fourth
-// tile of 32 keys, one tile loaded ahead in registers, and the four join at the end.
+// Few rows (part_fp4): 4 bits make the operands small enough to need no LDS.  A lane loads
+// 32 codes of one key as 16 bytes, which are its share of the first product's operand (each
+// lane group takes the channels that its bytes hold, the queries' are laid out alike); and
+// for the second product it loads, of each of its 8 keys, the codes of D / 16 neighbouring
+// channels, converts them and exchanges halves of registers in pairs, so that it holds 8
+// keys of one channel for each of D / 16 products, whose rows are every (D / 16)-th channel.
+// So the waves of a workgroup share nothing while they pass the keys: each takes every
+// fourth tile of 32 keys, one tile in registers while the next one is under way, and the
+// four join at the end.  Memory bounds it: 256 requests x 4 tokens, 4 heads of 128, up to
+// 1024 keys 28.3 us, 4.2 TB/s, of which the loads alone take 26.8; one token over 131072
+// keys 15.9 us, 4.6 TB/s, and 5.4 to join.
+//
+// Many rows (CodesToLds): what a wave converts there would be converted again by every other
+// wave with rows of the same keys; so four waves convert a tile once, into LDS, and each passes
+// it with 16 or 32 rows of its own, by the loop of attn_tiles.h.  256 requests x 4 over a
+// prefix of 8192: 103 us with the requests' own keys beside it, 740 TFLOP/s; LDS, vector and
+// matrix instructions each take some 2000 cycles of a tile of 64 keys and 128 rows.  As few
+// rows it took 142.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

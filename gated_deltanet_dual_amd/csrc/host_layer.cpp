@@ -119,6 +119,8 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
   const int64_t all_rows = rows * a.num_req;
   const int two = a.dim == 256 ? 1 : 2;
+  // Many rows share their tiles.  256 requests x 1024 own keys, 4 heads of 128: 32 rows 38 us
+  // apart and 53 shared, 48 rows 59 and 54; 128 requests, 64 rows of 64: 24 and 21.
   f.own_shared = rows > 16 * two;
   // as over bf16: two row tiles a wave where that leaves a workgroup for every CU
   p.own_tiles = f.own_shared ? (rows > 64 && ceil_div(rows, 128) * a.kv_heads * a.num_req >= 256 ? two : 1) : rows > 16 ? 2 : 1;
@@ -140,7 +142,11 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   const int64_t all_tiles = ceil_div(a.prefix_len, tile) + ceil_div(a.max_seq_len, tile);
   const int64_t together = a.prefix_len > 0 && all_tiles <= part_tiles ? passes(units, a.prefix_len + a.max_seq_len, own.alone, own_each) : INT64_MAX;
 
-  f.prefix_shared = f.own_shared || (a.prefix_len > 0 && all_rows > 64);
+  // The prefix's too, where the rows of all kv heads are many; 4 of them over 32000 keys: at d =
+  // 128 512 rows 56 us apart and 59 shared, 1024 97 and 95, 2048 176 and 156; at d = 64 256 rows 28
+  // and 29, 512 43 and 41, 1024 72 and 63; at d = 256 128 rows 53 and 45, one head 256 rows 33 and 35.
+  const int64_t many = a.dim == 128 ? 4096 : a.dim == 64 ? 1536 : 384;
+  f.prefix_shared = f.own_shared || (a.prefix_len > 0 && all_rows * a.kv_heads > many);
   p.prefix_tiles = a.prefix_len == 0 ? p.own_tiles : f.prefix_shared ? two : all_rows > 16 ? two : 1;
   if (!f.prefix_shared && p.prefix_tiles < p.own_tiles) p.prefix_tiles = p.own_tiles;
   p.prefix_groups = (int)ceil_div(all_rows, (f.prefix_shared ? 64 : 16) * p.prefix_tiles);

@@ -673,8 +673,8 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
   }
 }
 
-// Rows of a cache in 4 bits as bf16 or fp32: 8 channels a thread.  16576 rows of 4 heads of
-// 128, keys and values: 12.6 us, 3.5 TB/s, of which a launch's start and end are a third; 1152
+// Rows of a cache in 4 bits as bf16 or fp32: 8 channels a thread.  16512 rows of 4 heads of
+// 128, keys and values: 12.4 us, 3.8 TB/s, of which a launch's start and end are a third; 1152
 // rows 3.3 us.
 template <typename IO>
 __global__ __launch_bounds__(256) void cache_fp4_rows_kernel(Cache4Rows a, FastDiv chunks, FastDiv row_items) {

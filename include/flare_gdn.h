@@ -686,7 +686,8 @@ flare_status flare_rotary_cache(int64_t tokens, const flare_rotary_shape *shape,
  * arguments as flare_rotary's, and
  *   q_weight, k_weight  fp32 [dim], the same for all heads; NULL: that side is
  *              turned, not normed
- * Requirements as flare_rotary's. */
+ * Requirements as flare_rotary's, but for the tokens: 2^22 whatever the heads,
+ * more of few heads. */
 flare_status flare_qk_norm_rotary(int64_t tokens,
                                   const flare_rotary_shape *shape,
                                   const int32_t *positions, const double *freqs,

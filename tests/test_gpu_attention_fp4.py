@@ -143,6 +143,14 @@ def test_many_requests_with_many_rows(g, d, Hk, prefix, causal):
     check(g, make(11, R, B, Hk, G, d, 16, [(i * 29) % 150 for i in range(R)], prefix), prefix, causal)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("R,B,Hk,G,d,prefix", [(210, 2, 2, 4, 64, 4500), (70, 4, 2, 5, 64, 4500), (260, 4, 2, 2, 128, 4300),
+                                               (140, 4, 2, 5, 128, 4300), (50, 2, 1, 8, 256, 4200)])
+def test_prefix_of_many_requests_with_few_rows(g, R, B, Hk, G, d, prefix, causal):
+    """Tiles of the prefix shared by the rows of many requests, their own keys' by none."""
+    check(g, make(12, R, B, Hk, G, d, 16, [(i * 29) % 70 for i in range(R)], prefix), prefix, causal)
+
+
 def test_sharp_scores_and_scale(g):
     """Scores far apart (the running maximum moves, weights vanish) and a scale of the
     caller's own."""

@@ -98,7 +98,7 @@ def test_every_form_is_launched(calls):
             todo.append(call("cache4", tokens=100, d=d, half=half, io=io))
         todo.append(call("rows", tokens=100, io=io))
     for d in (64, 128, 256):
-        for R in (1, 5, 300):
+        for R in (1, 5, 300, 2000):
             for block in (1, 3, 4, 8, 16, 40):
                 for group in (1, 8):
                     for n in (0, 200, 20000):
