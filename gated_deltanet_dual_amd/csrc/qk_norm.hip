@@ -432,7 +432,8 @@ __device__ __forceinline__ void wave_lds_ready() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 template <typename IO, int VEC, bool TAIL, int NI>
-__device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPlan &p, int block, float *weights, double2 *coef, int2 *place, Upper *keys) {
+__device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPlan &p, int block, float *weights, double2 *coef,
+                                            int2 *place, Upper *keys) {
   const RotaryArgs &r = a.r;
   const int64_t t0 = (int64_t)block * p.t.tokens[1];
   const int n = (int)(r.tokens - t0 < p.t.tokens[1] ? r.tokens - t0 : p.t.tokens[1]);
@@ -535,7 +536,8 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_kernel(QkNormArgs a, QkNor
   char *const rest = lds + 2 * weight_floats(a.r.dim) * sizeof(float);
   float2 *const coef = reinterpret_cast<float2 *>(rest);
   if constexpr (OUT != PAGES4) {
-    forward_rows<IO, VEC, TAIL, NI, OUT>(a, p, blockIdx.x, true, weights, coef, reinterpret_cast<int2 *>(coef + p.t.tokens[0] * (a.r.half + kCoefMore)));
+    int2 *const place = reinterpret_cast<int2 *>(coef + p.t.tokens[0] * (a.r.half + kCoefMore));
+    forward_rows<IO, VEC, TAIL, NI, OUT>(a, p, blockIdx.x, true, weights, coef, place);
   } else {
     int block = blockIdx.x;
     if (block < p.t.blocks[0]) {
@@ -686,7 +688,8 @@ __global__ __launch_bounds__(256) void cache_fp4_rows_kernel(Cache4Rows a, FastD
     const int64_t slot = a.slots[row];
     uint32_t v[4] = {0, 0, 0, 0};
     if (slot >= 0 && slot < a.num_pages * a.page) {
-      const int64_t pg = a.num_pages * a.page <= INT32_MAX ? (int64_t)((uint32_t)slot / (uint32_t)a.page) : slot / a.page, ph = pg * a.heads + head, at = slot - pg * a.page;
+      const int64_t pg = a.num_pages * a.page <= INT32_MAX ? (int64_t)((uint32_t)slot / (uint32_t)a.page) : slot / a.page;
+      const int64_t ph = pg * a.heads + head, at = slot - pg * a.page;
       const uint32_t w = *reinterpret_cast<const uint32_t *>(a.codes[side] + ((ph * a.page + at) * a.dim >> 1) + 4 * c);
       const uint32_t s = (uint32_t)a.scales[side][(ph * (a.dim / kFp4Group) + (c >> 2)) * a.page + at] << 23;
       v[0] = fp4_pair<0>(w, s);
