@@ -468,7 +468,7 @@ def qk_norm_rotary_bwd(positions, freqs, q, k, dq_out, dk_out, q_weight=None, k_
          "dq_weight": _out_like(out.get("dq_weight"), "dq_weight", q_weight) if q_weight is not None else None,
          "dk_weight": _out_like(out.get("dk_weight"), "dk_weight", k_weight) if k_weight is not None else None}
     if q_weight is not None or k_weight is not None:
-        workspace = _workspace(workspace, qk_norm_rotary_bwd_workspace_bytes(T, shp.dim), dev)
+        workspace = _workspace(workspace, lib().flare_qk_norm_rotary_bwd_workspace_size(T, shp.dim), dev)
     _run(dev, lib().flare_qk_norm_rotary_bwd, T, ctypes.byref(shp), _ptr(positions), _ptr(freqs), _ptr(q), qs, _ptr(k), ks,
          _ptr(q_weight), _ptr(k_weight), eps, _ptr(dq_out), dqs, _ptr(dk_out), dks, _ptr(g["dq"]), _ptr(g["dk"]),
          _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), _ptr(workspace), 0 if workspace is None else workspace.numel())
@@ -522,6 +522,17 @@ def _chk_cache_fp4(cache, name, heads, d, dev):
 
 
 def _chk_caches_fp4(k_cache, v_cache, heads, d, dev):
+    if isinstance(k_cache, (tuple, list)) and isinstance(v_cache, (tuple, list)) and len(k_cache) == len(v_cache) == 2:
+        kc, ks = k_cache
+        vc, vs = v_cache
+        if kc is not None and ks is not None and vc is not None and vs is not None:  # all as they should be, in short
+            codes, scales, u8 = kc.shape, ks.shape, _module.uint8
+            if (len(codes) == len(scales) == 4 and vc.shape == codes and vs.shape == scales and d % 32 == 0
+                    and codes[1] == scales[1] == heads <= 0x7FFFFFFF and 2 * codes[3] == 32 * scales[2] == d
+                    and codes[0] == scales[0] and codes[2] == scales[3] <= 0x7FFFFFFF
+                    and kc.dtype == ks.dtype == vc.dtype == vs.dtype == u8 and kc.device == ks.device == vc.device == vs.device == dev
+                    and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+                return codes[0], codes[2]
     sizes = _chk_cache_fp4(k_cache, "k_cache", heads, d, dev)
     if _chk_cache_fp4(v_cache, "v_cache", heads, d, dev) != sizes:
         _fail("k_cache and v_cache have pages of different number or size")
