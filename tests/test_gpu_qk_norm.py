@@ -469,3 +469,32 @@ def test_refusals(g):
                 lambda: g.cache_fp4_rows(slots, c, g.cache_fp4(2, 2, 32, 64)), lambda: g.cache_fp4_rows(slots[None], c)):
         with pytest.raises(g.FlareError):
             bad()
+
+
+def test_two_streams_at_once(g):
+    """Calls under way together, each with its own workspace and cache, give the bits of one
+    after the other."""
+    import torch
+    sets = []
+    for seed, T, Hq, Hk, d, rot, io in ((7, 3000, 8, 2, 128, 64, torch.bfloat16), (8, 700, 3, 2, 96, 34, torch.float32)):
+        q, k, v, pos, freqs, qw, kw, rnd = make(seed, T, Hq, Hk, d, rot, io)
+        sets.append((pos, freqs, q, k, v, qw, kw, rnd(T, Hq, d).to(io), rnd(T, Hk, d).to(io), torch.randperm(4096, device="cuda")[:T]))
+
+    def calls(i):
+        pos, freqs, q, k, v, qw, kw, dq, dk, slots = sets[i]
+        kc, vc = g.cache_fp4(64, k.shape[1], 64, k.shape[2]), g.cache_fp4(64, k.shape[1], 64, k.shape[2])
+        grads = g.qk_norm_rotary_bwd(pos, freqs, q, k, dq, dk, qw, kw)
+        return [*g.qk_norm_rotary(pos, freqs, q, k, qw, kw), *grads.values(),
+                g.qk_norm_rotary_cache_fp4(pos, freqs, q, k, v, slots, kc, vc, qw, kw), *kc, *vc, *g.cache_fp4_rows(slots, kc, vc)]
+
+    want = [calls(0), calls(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        got = [[], []]
+        for _ in range(4):
+            for i, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    got[i].append(calls(i))
+        torch.cuda.synchronize()
+        assert all(a.equal(b) for i in range(2) for one in got[i] for a, b in zip(one, want[i]))
