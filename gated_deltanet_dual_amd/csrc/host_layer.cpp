@@ -353,12 +353,19 @@ QkNormTiles qk_norm_tiles(const QkNormArgs &a, bool reverse) {
   const int parts = (r.interleaved ? 2 * r.half : r.half) | (r.dim - 2 * r.half) | r.dim;
   QkNormTiles t{};
   t.vec = r.bf16 && !reverse && parts % 8 == 0 ? 8 : 4;
-  t.tails = parts % t.vec != 0;
   auto lanes = [&r](int vec, int &per, int &shift) {
     per = rotary_turned_items(r, vec) + rotary_copy_items(r.dim - 2 * r.half, vec);
+    shift = 0;
     while (shift < 6 && 1 << shift < per) ++shift;
   };
   lanes(t.vec, t.per, t.shift);
+  // The forms of vectors of 8 have one item a lane.  64 lanes have all of a head of 1024, but
+  // for one interleaved whose turned part and whose rest both end in half an item: 65.
+  if (t.vec == 8 && t.per > 1 << t.shift) {
+    t.vec = 4;
+    lanes(t.vec, t.per, t.shift);
+  }
+  t.tails = parts % t.vec != 0;
   lanes(4, t.key_per, t.key_shift);
   // Rows a team, 32768 tokens: 1, 2, 4, 8 of them forward 66, 61, 62, 64 us, reverse 163, 136,
   // 119, 120.  At least as many workgroups as keep the CUs busy, fewer where queries', keys'

@@ -723,7 +723,10 @@ QkNormPlan plan_of(const QkNormArgs &a, const QkNormTiles &t) {
   return p;
 }
 
-template <typename IO, int VEC, bool TAIL, int OUT> void forward(const QkNormArgs &a, const QkNormTiles &t, hipStream_t st) {
+// Whether `items` of each of a team's lanes are all of a head.
+bool in_lanes(int items, int per, int shift) { return per <= items << shift; }
+
+template <typename IO, int VEC, bool TAIL, int OUT> hipError_t forward(const QkNormArgs &a, const QkNormTiles &t, hipStream_t st) {
   const RotaryArgs &r = a.r;
   const QkNormPlan p = plan_of(a, t);
   const size_t weights = 2 * sizeof(float) * weight_floats(r.dim);
@@ -734,23 +737,28 @@ template <typename IO, int VEC, bool TAIL, int OUT> void forward(const QkNormArg
     if (lds < keys) lds = keys;
   }
   const int grid = (int)(t.blocks[0] + t.blocks[1] + t.blocks[2]);
-  // of vectors of 8 channels 64 lanes have a whole head of 1024, but not of its keys into 4 bits
-  if (OUT == PAGES4 ? t.key_per <= 1 << t.key_shift : t.per <= 1 << t.shift)
+  // rows of vectors of 8 have one item a lane in every form; three are those of vectors of 4,
+  // of the keys into 4 bits among them
+  if (!in_lanes(VEC == 8 ? 1 : 3, t.per, t.shift) || !in_lanes(3, t.key_per, t.key_shift)) return hipErrorInvalidConfiguration;
+  if (OUT == PAGES4 ? in_lanes(1, t.key_per, t.key_shift) : in_lanes(1, t.per, t.shift))
     qk_norm_rotary_kernel<IO, VEC, TAIL, 1, OUT><<<grid, 256, lds, st>>>(a, p);
   else if constexpr (VEC == 4 || OUT == PAGES4) qk_norm_rotary_kernel<IO, VEC, TAIL, 3, OUT><<<grid, 256, lds, st>>>(a, p);
+  return hipGetLastError();
 }
-template <int OUT> void forward_form(const QkNormArgs &a, hipStream_t st) {
+template <int OUT> hipError_t forward_form(const QkNormArgs &a, hipStream_t st) {
   const QkNormTiles t = qk_norm_tiles(a, false);
-  if (!a.r.bf16) t.tails ? forward<float, 4, true, OUT>(a, t, st) : forward<float, 4, false, OUT>(a, t, st);
-  else if (t.tails) forward<u16, 4, true, OUT>(a, t, st);
-  else t.vec == 8 ? forward<u16, 8, false, OUT>(a, t, st) : forward<u16, 4, false, OUT>(a, t, st);
+  if (!a.r.bf16) return t.tails ? forward<float, 4, true, OUT>(a, t, st) : forward<float, 4, false, OUT>(a, t, st);
+  if (t.tails) return forward<u16, 4, true, OUT>(a, t, st);
+  return t.vec == 8 ? forward<u16, 8, false, OUT>(a, t, st) : forward<u16, 4, false, OUT>(a, t, st);
 }
 
-template <typename IO, bool TAIL> void reverse(const QkNormArgs &a, const QkNormTiles &t, hipStream_t st) {
+template <typename IO, bool TAIL> hipError_t reverse(const QkNormArgs &a, const QkNormTiles &t, hipStream_t st) {
   const QkNormPlan p = plan_of(a, t);
   const size_t lds = 2 * sizeof(float) * weight_floats(a.r.dim) + 2 * sizeof(float2) * (size_t)t.tokens[0] * (a.r.half + kCoefMore);
-  if (t.per <= 1 << t.shift) qk_norm_rotary_bwd_kernel<IO, 4, TAIL, 1><<<(int)t.blocks[0], 256, lds, st>>>(a, p);
+  if (!in_lanes(3, t.per, t.shift)) return hipErrorInvalidConfiguration;
+  if (in_lanes(1, t.per, t.shift)) qk_norm_rotary_bwd_kernel<IO, 4, TAIL, 1><<<(int)t.blocks[0], 256, lds, st>>>(a, p);
   else qk_norm_rotary_bwd_kernel<IO, 4, TAIL, 3><<<(int)t.blocks[0], 256, lds, st>>>(a, p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -758,19 +766,16 @@ template <typename IO, bool TAIL> void reverse(const QkNormArgs &a, const QkNorm
 hipError_t launch_qk_norm_rotary(const QkNormArgs &a, hipStream_t st) {
   if (a.r.tokens == 0) return hipSuccess;
   TimedLaunch tl(K_QK_NORM, st);
-  if (a.into4) forward_form<PAGES4>(a, st);
-  else if (a.r.slots) forward_form<PAGES>(a, st);
-  else forward_form<PACKED>(a, st);
-  return hipGetLastError();
+  if (a.into4) return forward_form<PAGES4>(a, st);
+  return a.r.slots ? forward_form<PAGES>(a, st) : forward_form<PACKED>(a, st);
 }
 
 hipError_t launch_qk_norm_rotary_bwd(const QkNormArgs &a, hipStream_t st) {
   TimedLaunch tl(K_QK_NORM_BWD, st);
   const QkNormTiles t = qk_norm_tiles(a, true);
   if (a.r.tokens > 0) {
-    if (a.r.bf16) t.tails ? reverse<u16, true>(a, t, st) : reverse<u16, false>(a, t, st);
-    else t.tails ? reverse<float, true>(a, t, st) : reverse<float, false>(a, t, st);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = a.r.bf16 ? (t.tails ? reverse<u16, true>(a, t, st) : reverse<u16, false>(a, t, st))
+                                  : t.tails ? reverse<float, true>(a, t, st) : reverse<float, false>(a, t, st);
     if (e != hipSuccess) return e;
   }
   if (!a.weight[0] && !a.weight[1]) return hipSuccess;

@@ -498,3 +498,11 @@ def test_two_streams_at_once(g):
                     got[i].append(calls(i))
         torch.cuda.synchronize()
         assert all(a.equal(b) for i in range(2) for one in got[i] for a, b in zip(one, want[i]))
+
+
+@pytest.mark.parametrize("half", [4, 36, 252, 508])
+def test_interleaved_heads_of_an_item_more_than_lanes(g, half):
+    """bf16 heads of 1024 whose turned part and whose rest both end in half an item of two
+    vectors of 8: 65 items for 64 lanes."""
+    test_forms(g, 6, 2, 1, 1024, 2 * half, True, "bf16", "qk")
+    test_cache_fp4(g, 9, 3, 2, 1024, 2 * half, True, "bf16", "qk", 16)
