@@ -135,3 +135,28 @@ def test_more_workgroups_than_a_launch_holds(calls):
         assert s == 0 and all(0 < n < 2 ** 32 for n in items)
     (s, items, _), = calls(call("attention", R=2 ** 23, qh=1, kh=1, most=2 ** 20))
     assert s == 4 and items == []
+
+
+def test_every_call_enqueues_its_launches(calls):
+    """One of the norms and of the rows, two of the reverse mode with its weights' sums, and of an
+    attention two where its workspace holds parts: a call that enqueues nothing is no success."""
+    todo, want = [], []
+    for inter in (0, 1):
+        for io in (g.BF16, g.F32):
+            for d, half in ((1, 0), (3, 1), (64, 32), (80, 25), (128, 12), (1016, 4), (1024, 0), (1024, 4), (1024, 300), (1024, 508), (1024, 512)):
+                for op in ("forward", "reverse", "cache") + (("cache4",) if d % 32 == 0 else ()):
+                    for tokens in (1, 3000):
+                        todo.append(call(op, tokens=tokens, d=d, half=half, io=io, inter=inter))
+                        want.append(2 if op == "reverse" else 1)
+    for values in (False, True):
+        todo.append(call("rows", tokens=1, values=values))
+        want.append(1)
+    for d in (64, 128, 256):
+        for R in (1, 40, 300):
+            for block, group in ((1, 1), (1, 17), (4, 8), (33, 1), (16, 16)):
+                for n, most in ((0, 0), (0, 1), (50, 700), (0, 9000), (20000, 700), (20000, 0)):
+                    todo.append(call("attention", R=R, block=block, d=d, qh=2 * group, kh=2, n=n, most=most))
+                    want.append(2 if g.block_attention_fp4_workspace_bytes(R, block, 2 * group, 2, d, 64, most, n) else 1)
+    got = [r for i in range(0, len(todo), 200) for r in calls(*todo[i:i + 200])]
+    for (status, items, _), n, c in zip(got, want, todo):
+        assert status == 0 and len(items) == n and all(0 < i < 2 ** 32 for i in items), (c, status, items)
