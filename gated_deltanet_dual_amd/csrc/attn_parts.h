@@ -19,6 +19,17 @@ __device__ __forceinline__ float xmax32(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// Two weights of at least 0 in two bf16 halves each, the first ones in x: cut, so that up to
+// 2^-7 of a weight is left, and that rounded, off by 2^-15 of the weight at most.  2^-20 of it
+// are added, so that the second half of a weight that is not 0 is not 0 either: a value of
+// infinity times both halves stays one.
+__device__ __forceinline__ uint2 two_halves(float x, float y) {
+  const uint32_t first = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+  constexpr float kMore = 1.0f + 0x1p-20f;
+  return make_uint2(first, pack_bf16x2(__builtin_fmaf(x, kMore, -__uint_as_float(first << 16)),
+                                       __builtin_fmaf(y, kMore, -__uint_as_float(first & 0xffff0000u))));
+}
+
 // What a workgroup works on: rows [row0, row_end) (token * G + query of the
 // group) of one kv head against keys [k0, k1) of the prefix or of one request.
 struct Part {

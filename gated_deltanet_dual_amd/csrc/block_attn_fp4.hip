@@ -13,6 +13,14 @@
 // their products to 2^-14 of the largest only: scores off by 5e-6 of themselves where bf16
 // products are off by 1e-8.)
 //
+// Beside bf16 values the second product takes its weights in bf16.  Few rows give them in two
+// halves (two_halves) and a product for each: outputs are off by their own rounding, 1.66e-3 of
+// themselves in the mean, where weights rounded once make 2.29e-3, for a little time: 256
+// requests over their own keys 28.6 and 29.8 us, one token over 131072 keys 21.3 and 22.0, 5
+// rows of narrow heads 24.1 and 26.5.  Many rows give them rounded once, half a step or 2^-8 of
+// a weight at most, as over bf16: two halves took 138 us for 103 over a shared prefix, 45 for 42
+// at d = 256.  The sum l takes the weights as they are in both forms.
+//
 // Few rows (part_fp4): 4 bits make the operands small enough to need no LDS.  A lane loads
 // 32 codes of one key as 16 bytes, which are its share of the first product's operand (each
 // lane group takes the channels that its bytes hold, the queries' are laid out alike); and
@@ -231,7 +239,7 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
         for (int d = 0; d < DT; ++d) o[n][d] *= al;
       }
     }
-    u32x4v pb[NQ];
+    u32x4v pb[NQ], rest[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const float base = m[n] == -INFINITY ? 0.0f : m[n] * sc;  // a row that sees nothing yet
@@ -242,7 +250,11 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
         sum += y[e];
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pb[n][e] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
+      for (int e = 0; e < 4; ++e) {
+        const uint2 w = two_halves(y[2 * e], y[2 * e + 1]);
+        pb[n][e] = w.x;
+        rest[n][e] = w.y;
+      }
       l[n] += sum;
     }
     if (ragged) {
@@ -271,9 +283,12 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
             const int j = key - kt;
-            const uint32_t lo = j & 2 ? pb[n][1] : pb[n][0], hi = j & 2 ? pb[n][3] : pb[n][2];
-            const uint32_t two = __shfl(j & 16 ? hi : lo, 4 * (j & 12) + col);
-            f[n] = __uint_as_float(key & 1 ? two & 0xffff0000u : two << 16);
+            auto weight = [&](const u32x4v &w) {
+              const uint32_t lo = j & 2 ? w[1] : w[0], hi = j & 2 ? w[3] : w[2];
+              const uint32_t two = __shfl(j & 16 ? hi : lo, 4 * (j & 12) + col);
+              return __uint_as_float(key & 1 ? two & 0xffff0000u : two << 16);
+            };
+            f[n] = weight(pb[n]) + weight(rest[n]);
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -314,6 +329,10 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
       for (int n = 0; n < NQ; ++n) mma_bf16(o[n][2 * C], __builtin_bit_cast(bf16x8, even), __builtin_bit_cast(bf16x8, pb[n]));
 #pragma unroll
       for (int n = 0; n < NQ; ++n) mma_bf16(o[n][2 * C + 1], __builtin_bit_cast(bf16x8, next), __builtin_bit_cast(bf16x8, pb[n]));
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) mma_bf16(o[n][2 * C], __builtin_bit_cast(bf16x8, even), __builtin_bit_cast(bf16x8, rest[n]));
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) mma_bf16(o[n][2 * C + 1], __builtin_bit_cast(bf16x8, next), __builtin_bit_cast(bf16x8, rest[n]));
     });
   };
 #pragma unroll 1

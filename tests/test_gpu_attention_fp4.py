@@ -470,3 +470,41 @@ def test_refusals(g):
     odd = torch.empty(vc[0].numel() + 8, dtype=torch.uint8, device="cuda")[8:].reshape(vc[0].shape)
     with pytest.raises(g.FlareError):
         ok(v_cache=(odd, vc[1]))
+
+
+FEW_ROWS = [(1, 1, 4, 4, 128, 64, [700], 0), (3, 4, 2, 4, 128, 16, [1, 33, 130], 77), (4, 1, 1, 8, 256, 32, [15, 16, 31, 32], 1),
+            (2, 16, 1, 2, 64, 32, [16, 47], 40), (5, 3, 1, 5, 64, 128, [3, 64, 127, 128, 129], 129), (1, 1, 1, 2, 64, 16, [4500], 0),
+            (1, 1, 1, 4, 128, 16, [70], 4200), (3, 2, 2, 2, 128, 16, [0, 33, 70], 4100), (2, 8, 1, 4, 128, 16, [8, 90], 20)]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("i", range(len(FEW_ROWS)))
+def test_weights_of_few_rows_keep_16_bits(g, i, causal):
+    """Up to 16 (d = 256) or 32 rows a kv head and request, and not thousands over a prefix: the weights
+    go into the second product in two bf16 halves.  The first is cut, so that up to 2^-7 of a weight
+    is left, the second rounds that by 2^-8 of itself, and 2^-20 are added: 2^-15 + 2^-20 of sum
+    p |v| / sum p in place of 2^-8.  Scores, exponentials and sums as above."""
+    import torch
+    R, B, Hk, G, d, page, lens, prefix = FEW_ROWS[i]
+    q, kc, vc, bt, sl, pt = make(50 + i, R, B, Hk, G, d, page, lens, prefix)
+    o = g.block_attention_fp4(q, kc, vc, bt, sl, prefix_table=pt, prefix_len=prefix, causal=causal)
+    ro, _, size = attention64(q, cache_values(*kc), cache_values(*vc), bt, sl, pt, prefix, causal)
+    close(o, ro, torch.bfloat16, (2.0 ** -15 + 2.0 ** -20 + 4e-4) * size, "o")
+
+
+@pytest.mark.parametrize("d,B,G,R", [(64, 5, 2, 2), (128, 1, 4, 2), (128, 8, 4, 2), (256, 4, 1, 2), (128, 20, 8, 2), (256, 9, 2, 2)])
+def test_infinite_values_that_every_row_sees(g, d, B, G, R):
+    """A value that no float holds times a weight above 0 is infinite, of the value's sign,
+    whatever the weight's bits: also where one key has all the weight, which is then 1 exactly."""
+    import torch
+    for own, prefix in ((1, 0), (40, 0), (90, 70)):
+        q, kc, vc, bt, lens, pt = make(60, R, B, 1, G, d, 16, [own] * R, prefix, kscale=0.5)
+        clean = g.block_attention_fp4(q, kc, vc, bt, lens, prefix_table=pt, prefix_len=prefix)
+        codes, scales = (t.clone() for t in vc)
+        for r in range(R):
+            page = int(bt[r, 0])
+            scales[page, 0, 1, 0] = 254
+            codes[page, 0, 0, 16:32] = 0xF7
+        o = g.block_attention_fp4(q, kc, (codes, scales), bt, lens, prefix_table=pt, prefix_len=prefix)
+        assert (o[..., 32:64:2] == math.inf).all() and (o[..., 33:64:2] == -math.inf).all()
+        assert torch.equal(o[..., :32], clean[..., :32]) and torch.equal(o[..., 64:], clean[..., 64:])
