@@ -64,10 +64,6 @@ template <int D> struct Tile {
   uint32_t k[2][D / 32], ks[2][VW], v[8][VW], vs[2];
 };
 
-// Queries of a workgroup's rows stay in registers up to 32 of them a lane, else in LDS.
-template <int D, int NQ> constexpr bool kQueriesInLds = NQ * (D / 32) > 8;
-template <int D, int NQ> constexpr int kQueryBytes = kQueriesInLds<D, NQ> ? NQ * (D / 32) * 1024 : 0;
-
 // One part: 16 NQ rows of a kv head against its keys, by four waves.
 template <int D, int NQ>
 __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPlan &p, const Part &w, char *lds) {
@@ -149,17 +145,12 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
       z = *reinterpret_cast<const u32x4v *>((const u16 *)a.q + ((int64_t)tok * a.q_heads + head * G + (m - tok * G)) * D + channel(s));
     return z;
   };
-  u32x4v *const q_lds = reinterpret_cast<u32x4v *>(lds);
-  bf16x8 q[kQueriesInLds<D, NQ> ? 1 : NQ][kQueriesInLds<D, NQ> ? 1 : KS];
-  if constexpr (kQueriesInLds<D, NQ>) {
-    for (int i = wave; i < NQ * KS; i += 4) q_lds[i * 64 + lane] = query(i / KS, i % KS);
-    __syncthreads();
-  } else {
+  static_assert(NQ * KS <= 8);  // 32 registers
+  bf16x8 q[NQ][KS];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+  for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int s = 0; s < KS; ++s) q[n][s] = __builtin_bit_cast(bf16x8, query(n, s));
-  }
+    for (int s = 0; s < KS; ++s) q[n][s] = __builtin_bit_cast(bf16x8, query(n, s));
   int lim[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -197,22 +188,15 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
 #pragma unroll
       for (int sb = 0; sb < 2; ++sb) s[n][sb] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < KS; ++e) {
-      bf16x8 qe[NQ];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        if constexpr (kQueriesInLds<D, NQ>) qe[n] = __builtin_bit_cast(bf16x8, q_lds[(n * KS + e) * 64 + lane]);
-        else qe[n] = q[n][e];
-      }
+    for (int e = 0; e < KS; ++e)
 #pragma unroll
       for (int sb = 0; sb < 2; ++sb) {
         const uint32_t c = x.k[sb][e], scale = x.ks[sb][e / 4] << 23;
         const bf16x8 kf = __builtin_bit_cast(
             bf16x8, make_uint4(fp4_pair<0>(c, scale), fp4_pair<1>(c, scale), fp4_pair<2>(c, scale), fp4_pair<3>(c, scale)));
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_bf16(s[n][sb], kf, qe[n]);
+        for (int n = 0; n < NQ; ++n) mma_bf16(s[n][sb], kf, q[n][e]);
       }
-    }
     if (ragged) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
@@ -346,8 +330,7 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
 
   // The four waves' maxima and sums, then their outputs: wave r joins the channels DT (4 grp
   // + r) .. of every row, which lie together.
-  char *const join = lds + kQueryBytes<D, NQ>;
-  float2 *const stat = reinterpret_cast<float2 *>(join);           // [4][NQ][16]
+  float2 *const stat = reinterpret_cast<float2 *>(lds);            // [4][NQ][16]
   float *const piece = reinterpret_cast<float *>(stat + 4 * NQ * 16);  // [wave][its 3 pieces][64][DT]
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -531,7 +514,7 @@ template <int D, bool SHARED, int NQ> constexpr int kRows = SHARED ? 64 * NQ : 1
 constexpr int larger(int a, int b) { return a > b ? a : b; }
 template <int D, bool SHARED, int NQ>
 constexpr int kLdsBytes = SHARED ? 4 * kTileKeys<D> * D * 2
-                                 : kQueryBytes<D, NQ> + 4 * NQ * 16 * 8 + 12 * 64 * (D / 16) * 4;
+                                 : 4 * NQ * 16 * 8 + 12 * 64 * (D / 16) * 4;
 
 template <int D, bool SHARED, int NQ>
 __device__ __forceinline__ void part_of(const BlockAttnFp4Args &b, const AttnPlan &p, const Part &w, char *lds) {
