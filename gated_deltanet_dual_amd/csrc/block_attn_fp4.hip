@@ -540,37 +540,35 @@ __global__ __launch_bounds__(256, WPS) void attend_fp4_kernel(BlockAttnFp4Args b
 }
 
 template <int D, bool PS, int NQP, bool OS, int NQO, int WPS>
-void launch(const BlockAttnFp4Args &b, const AttnPlan &p, hipStream_t st) {
+hipError_t launch(const BlockAttnFp4Args &b, const AttnPlan &p, hipStream_t st) {
   attend_fp4_kernel<D, PS, NQP, OS, NQO, WPS><<<(unsigned)attn_launch_blocks(p), 256, 0, st>>>(b, p);
+  return hipGetLastError();
 }
 
-template <int D> void launch_d(const BlockAttnFp4Args &b, const AttnPlan &p, const AttnForms &f, hipStream_t st) {
+template <int D> hipError_t launch_d(const BlockAttnFp4Args &b, const AttnPlan &p, const AttnForms &f, hipStream_t st) {
   constexpr int TWO = D == 256 ? 1 : 2, S = D == 64 ? 3 : 2;
   if (!f.prefix_shared) {  // nor the own keys'
-    if (p.prefix_tiles == 1) {
-      launch<D, false, 1, false, 1, D == 64 ? 4 : D == 128 ? 3 : 2>(b, p, st);
-    } else if constexpr (D <= 128) {
-      if (p.own_tiles == 1) launch<D, false, 2, false, 1, D == 64 ? 3 : 2>(b, p, st);
-      else launch<D, false, 2, false, 2, D == 64 ? 3 : 2>(b, p, st);
+    if (p.prefix_tiles == 1) return launch<D, false, 1, false, 1, D == 64 ? 4 : D == 128 ? 3 : 2>(b, p, st);
+    if constexpr (D <= 128) {
+      if (p.own_tiles == 1) return launch<D, false, 2, false, 1, D == 64 ? 3 : 2>(b, p, st);
+      return launch<D, false, 2, false, 2, D == 64 ? 3 : 2>(b, p, st);
     }
   } else if (!f.own_shared) {
-    if (p.own_tiles == 1) launch<D, true, TWO, false, 1, S>(b, p, st);
-    else if constexpr (D <= 128) launch<D, true, TWO, false, 2, S>(b, p, st);
+    if (p.own_tiles == 1) return launch<D, true, TWO, false, 1, S>(b, p, st);
+    if constexpr (D <= 128) return launch<D, true, TWO, false, 2, S>(b, p, st);
   } else if (p.own_tiles == 2) {
-    launch<D, true, TWO, true, TWO, S>(b, p, st);
+    return launch<D, true, TWO, true, TWO, S>(b, p, st);
   } else {
-    launch<D, true, TWO, true, 1, S>(b, p, st);
+    return launch<D, true, TWO, true, 1, S>(b, p, st);
   }
+  return hipErrorInvalidConfiguration;  // no plan's
 }
 
 }  // namespace
 
 hipError_t launch_block_attention_fp4(const BlockAttnFp4Args &b, const AttnPlan &p, const AttnForms &f, hipStream_t st) {
   TimedLaunch tl(K_BLOCK_ATTN_FP4, st);
-  if (b.a.dim == 64) launch_d<64>(b, p, f, st);
-  else if (b.a.dim == 128) launch_d<128>(b, p, f, st);
-  else launch_d<256>(b, p, f, st);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = b.a.dim == 64 ? launch_d<64>(b, p, f, st) : b.a.dim == 128 ? launch_d<128>(b, p, f, st) : launch_d<256>(b, p, f, st);
   return e != hipSuccess ? e : launch_attn_join(b.a, p, st);
 }
 
