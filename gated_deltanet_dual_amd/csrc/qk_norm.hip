@@ -301,7 +301,7 @@ __device__ __forceinline__ void weights_to_lds(float *lds, const QkNormArgs &a) 
 // The coefficients of n tokens from t0 on, [n][half], and behind each token's zeros where a
 // short vector's last channels would be.
 constexpr int kCoefMore = 4;
-template <typename C2> __device__ __forceinline__ void form_coefficients(C2 *coef, const RotaryArgs &r, const FastDiv &half, int64_t t0, int n) {
+template <typename IO, typename C2> __device__ __forceinline__ void form_coefficients(C2 *coef, const RotaryArgs &r, const FastDiv &half, int64_t t0, int n) {
   const int each = r.half + kCoefMore;
   for (int i = threadIdx.x; i < n * r.half; i += 256) {
     const int t = fast_div(i, half), j = i - t * r.half;
@@ -310,6 +310,8 @@ template <typename C2> __device__ __forceinline__ void form_coefficients(C2 *coe
       double s, c;
       sincospi(2.0 * turn_fraction(r.positions[t0 + t], r.freqs[j]), &s, &c);
       to = make_double2((double)r.mscale * c, (double)r.mscale * s);
+    } else if constexpr (sizeof(IO) == 4) {
+      to = turn_fp32(r.positions[t0 + t], r.freqs[j], r.mscale, r.sign);
     } else {
       to = turn(r.positions[t0 + t], r.freqs[j], r.mscale, r.sign);
     }
@@ -400,7 +402,7 @@ __device__ __forceinline__ void forward_rows(const QkNormArgs &a, const QkNormPl
   Row w0 = row_at(team < rows ? team : 0), w1;
   load(w0, x0);
   weights_to_lds(weights, a);
-  form_coefficients(coef, r, p.half, t0, n);
+  form_coefficients<IO>(coef, r, p.half, t0, n);
   if (OUT != PACKED && (int)threadIdx.x < n) place[threadIdx.x] = place_of(r, t0 + threadIdx.x);
   __syncthreads();
   if (rows <= teams) {  // nothing to have under way
@@ -502,7 +504,7 @@ __device__ __forceinline__ void keys_to_fp4(const QkNormArgs &a, const QkNormPla
   int row0 = (threadIdx.x >> 6) * wave_teams;
   load(row0 + wave_team, x0);
   weights_to_lds(weights, a);
-  form_coefficients(coef, r, p.half, t0, n);
+  form_coefficients<IO>(coef, r, p.half, t0, n);
   if ((int)threadIdx.x < n) place[threadIdx.x] = place_of(r, t0 + threadIdx.x);
   __syncthreads();
   for (; row0 < rows; row0 += 2 * teams) {
@@ -642,13 +644,13 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
   };
   int buf = 0;
   weights_to_lds(weights, a);
-  form_coefficients(coefs, r, p.half, (int64_t)blockIdx.x * step, count((int64_t)blockIdx.x * step));
+  form_coefficients<IO>(coefs, r, p.half, (int64_t)blockIdx.x * step, count((int64_t)blockIdx.x * step));
   __syncthreads();
   for (int64_t t0 = (int64_t)blockIdx.x * step; t0 < r.tokens; t0 += (int64_t)gridDim.x * step, buf ^= 1) {
     const float2 *const coef = coefs + buf * each;
     const int64_t next = t0 + (int64_t)gridDim.x * step;
     pass(std::integral_constant<int, 0>(), t0, count(t0), coef,
-         [&] { form_coefficients(coefs + (buf ^ 1) * each, r, p.half, next, count(next)); });
+         [&] { form_coefficients<IO>(coefs + (buf ^ 1) * each, r, p.half, next, count(next)); });
     pass(std::integral_constant<int, 1>(), t0, count(t0), coef, [] {});
     __syncthreads();
   }

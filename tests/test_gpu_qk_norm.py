@@ -506,3 +506,27 @@ def test_interleaved_heads_of_an_item_more_than_lanes(g, half):
     vectors of 8: 65 items for 64 lanes."""
     test_forms(g, 6, 2, 1, 1024, 2 * half, True, "bf16", "qk")
     test_cache_fp4(g, 9, 3, 2, 1024, 2 * half, True, "bf16", "qk", 16)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_coefficients_of_fp32_rows(g, inter):
+    """Rows whose pairs are (1, 0) come out as the cosine and sine themselves, in reverse as the
+    cosine and the negative sine: off by 4 half steps (two units of the functions) and one of the
+    last sum, relative to the value also where it is near 0; what 64 bits leave of 4096 radians
+    is 4e-12."""
+    import torch
+    T, d = 4096, 64
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    freqs = 10000.0 ** (-torch.arange(d // 2, dtype=torch.float64, device="cuda") / (d // 2))
+    re = torch.arange(d // 2, device="cuda") * (2 if inter else 1)
+    im = re + (1 if inter else d // 2)
+    x = torch.zeros(T, 1, d, device="cuda")
+    x[..., re] = 1.0
+    angle = pos.cpu().double()[:, None] * freqs.cpu()
+    c, s = torch.cos(angle), torch.sin(angle)
+    y, z = g.qk_norm_rotary(pos, freqs, x, x, interleaved=inter)
+    back = g.qk_norm_rotary_bwd(pos, freqs, x, x, x, x, interleaved=inter)
+    for got, sign in ((y, 1), (z, 1), (back["dq"], -1), (back["dk"], -1)):
+        for at, want in ((re, c), (im, sign * s)):
+            off = (got[:, 0, at].cpu().double() - want).abs()
+            assert (off <= 5 * STEP * want.abs() + 4e-12).all(), float((off / want.abs().clamp(min=1e-9)).max() / STEP)
