@@ -530,3 +530,21 @@ def test_coefficients_of_fp32_rows(g, inter):
         for at, want in ((re, c), (im, sign * s)):
             off = (got[:, 0, at].cpu().double() - want).abs()
             assert (off <= 5 * STEP * want.abs() + 4e-12).all(), float((off / want.abs().clamp(min=1e-9)).max() / STEP)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_weights_sums_of_many_teams(g, io):
+    """256 heads of 8 channels of one token, a team of a workgroup each: gradients whose sum in
+    32 bits would lose the small ones beside two large ones of either sign.  Rows of ones have a
+    norm of 1, so that every term is a gradient itself."""
+    import torch
+    io = types(io)
+    H, d = 256, 8
+    x = torch.ones(1, H, d, device="cuda").to(io)
+    dy = torch.ones(1, H, d, device="cuda").to(io)
+    dy[0, 0], dy[0, H - 1] = 2.0 ** 25, -2.0 ** 25
+    dy[0, 1] = torch.arange(d).to(io)
+    pos, freqs = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.float64, device="cuda")
+    w = torch.ones(d, device="cuda")
+    out = g.qk_norm_rotary_bwd(pos, freqs, x, None, dy, None, w, eps=0.0)
+    assert out["dq_weight"].tolist() == [H - 3.0 + i for i in range(d)]
