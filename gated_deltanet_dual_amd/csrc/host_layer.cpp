@@ -94,8 +94,9 @@ namespace {
 // CU's instructions that several keep busy, and its share of memory's time where no other
 // row group reads it.  Measured: the shared form of two row tiles at d = 128, 4096 keys 106 us
 // alone, 4 x 2048 keys 80 us two a CU; d = 256, one: 2 x 2048 111 us; d = 64, two: 4 x 1024 60
-// us four a CU.  The other form, one row tile at d = 128, 4096 keys 29 us where every CU has
-// one, 2 x 2048 24 us.
+// us four a CU.  The other form, one row tile at d = 128, 4096 keys a workgroup 43 us with one a
+// CU (2048 keys 28) and 63 with four (40); two tiles 45 (29) and 116 (70); d = 64 36 (24) and 54
+// (36), two 37 (26) and 83 (49); d = 256 2048 keys 33 and 85.
 struct KeyCost {
   int alone, busy, memory;
 };
@@ -106,9 +107,9 @@ KeyCost key_cost(bool shared, int tiles, int dim) {
     if (dim == 64) return tiles == 2 ? KeyCost{180, 146, memory} : KeyCost{120, 90, memory};
     return tiles == 2 ? KeyCost{260, 195, memory} : KeyCost{176, 120, memory};
   }
-  if (dim == 256) return {140, 70, memory};
-  if (dim == 64) return tiles == 2 ? KeyCost{65, 40, memory} : KeyCost{50, 25, memory};
-  return tiles == 2 ? KeyCost{98, 55, memory} : KeyCost{70, 35, memory};
+  if (dim == 256) return {145, 72, memory};
+  if (dim == 64) return tiles == 2 ? KeyCost{75, 50, memory} : KeyCost{57, 31, memory};
+  return tiles == 2 ? KeyCost{112, 69, memory} : KeyCost{78, 43, memory};
 }
 constexpr int64_t kCus = 256, kStart = 45000;  // a launch's start and end
 }  // namespace
@@ -119,8 +120,9 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   const int64_t rows = (int64_t)a.block * (a.q_heads / a.kv_heads);
   const int64_t all_rows = rows * a.num_req;
   const int two = a.dim == 256 ? 1 : 2;
-  // Many rows share their tiles.  256 requests x 1024 own keys, 4 heads of 128: 32 rows 38 us
-  // apart and 53 shared, 48 rows 59 and 54; 128 requests, 64 rows of 64: 24 and 21.
+  // Many rows share their tiles.  256 requests x 1024 own keys, 4 heads of 128: 32 rows 42 us
+  // apart and 50 shared, 48 rows 68 and 54; of 64, 32 rows 28 and 33, 128 requests x 64 rows 28
+  // and 21.
   f.own_shared = rows > 16 * two;
   // as over bf16: two row tiles a wave where that leaves a workgroup for every CU
   p.own_tiles = f.own_shared ? (rows > 64 && ceil_div(rows, 128) * a.kv_heads * a.num_req >= 256 ? two : 1) : rows > 16 ? 2 : 1;
@@ -143,9 +145,10 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   const int64_t together = a.prefix_len > 0 && all_tiles <= part_tiles ? passes(units, a.prefix_len + a.max_seq_len, own.alone, own_each) : INT64_MAX;
 
   // The prefix's too, where the rows of all kv heads are many; 4 of them over 32000 keys: at d =
-  // 128 512 rows 56 us apart and 59 shared, 1024 97 and 95, 2048 176 and 156; at d = 64 256 rows 28
-  // and 29, 512 43 and 41, 1024 72 and 63; at d = 256 128 rows 53 and 45, one head 256 rows 33 and 35.
-  const int64_t many = a.dim == 128 ? 4096 : a.dim == 64 ? 1536 : 384;
+  // 128 128 rows 30 us apart and 30 shared, 256 45 and 39, 1024 116 and 94; at d = 64 128 rows 23
+  // and 23, 256 32 and 28; at d = 256 128 rows 55 and 43; one head of 128 256 rows 24 and 27, 512
+  // 30 and 30, of 256 256 rows 34 and 34, 512 49 and 43.
+  const int64_t many = a.dim == 256 ? 256 : 512;
   f.prefix_shared = f.own_shared || (a.prefix_len > 0 && all_rows * a.kv_heads > many);
   p.prefix_tiles = a.prefix_len == 0 ? p.own_tiles : f.prefix_shared ? two : all_rows > 16 ? two : 1;
   if (!f.prefix_shared && p.prefix_tiles < p.own_tiles) p.prefix_tiles = p.own_tiles;
