@@ -108,7 +108,7 @@ KeyCost key_cost(bool shared, int tiles, int dim) {
     return tiles == 2 ? KeyCost{260, 195, memory} : KeyCost{176, 120, memory};
   }
   if (dim == 256) return {145, 72, memory};
-  if (dim == 64) return tiles == 2 ? KeyCost{75, 50, memory} : KeyCost{57, 31, memory};
+  if (dim == 64) return tiles == 2 ? KeyCost{75, 50, memory} : KeyCost{57, 27, memory};
   return tiles == 2 ? KeyCost{112, 69, memory} : KeyCost{78, 43, memory};
 }
 constexpr int64_t kCus = 256, kStart = 45000;  // a launch's start and end
