@@ -18,6 +18,7 @@ __device__ __forceinline__ void meet() {
 }
 
 template <bool V> struct Const { static constexpr bool value = V; };
+template <int A, int B> struct Range { static constexpr int from = A, to = B; };
 
 // Where the 16-byte piece c of row `row` of a V tile [rows][D] bf16 sits: the
 // pairs of pieces that a transpose read takes from 16 rows fall on all banks.
@@ -45,7 +46,9 @@ __device__ __forceinline__ const BlockAttnArgs &attn_args(const BlockAttnFp4Args
 // with rows on from workgroup to workgroup, so that all SIMDs of a CU get some.
 // from.load(page, head, row in it, buffer) begins to fetch this wave's 16 rows of a tile.
 // Where From::kLands they come to registers, a tile earlier, and from.land(buffer) writes
-// them to LDS.
+// them to LDS.  Where From::kHalves the weights go into the second product in two halves
+// (two_halves), which leaves fewer registers: half of the values' operands are read late, and
+// places in a tile are formed where they are used.
 template <int D, int NQ, int TK, typename From, typename Args>
 __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, const Part &w, int turn,
                                           u16 (&kt_lds)[2][TK * D], u16 (&vt_lds)[2][TK * D]) {
@@ -147,12 +150,16 @@ __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, c
     const int r = 4 * grp + (col >> 2);
     va[d] = r * D + v_piece<D>(r, 2 * d + ((col & 3) >> 1)) * 8 + (col & 1) * 4;
   }
-  // V's operands of 32 keys
-  auto read_v = [&](u16 *vb, int h, bf16x8 (&vf)[DT]) {
+  // places differ from the first by bits of e or d alone
+  int k_first = ka[0], v_first = va[0];
+  auto k_at = [&](int e) { return From::kHalves ? k_first ^ (32 * e) : ka[e]; };
+  auto v_at = [&](int d) { return From::kHalves ? v_first ^ (16 * d) : va[d]; };
+  // V's operands of 32 keys, of some of the channel tiles
+  auto read_v = [&](u16 *vb, int h, bf16x8 (&vf)[DT], auto tiles) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d % VA] + d / VA * 128 + 32 * h * D));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + va[d % VA] + d / VA * 128 + (32 * h + 16) * D));
+    for (int d = tiles.from; d < tiles.to; ++d) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_at(d % VA) + d / VA * 128 + 32 * h * D));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_at(d % VA) + d / VA * 128 + (32 * h + 16) * D));
       vf[d] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   };
@@ -181,6 +188,7 @@ __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, c
     if (!live) return;
 #pragma unroll
     for (int h = 0; h < TK / 32; ++h) {
+      if constexpr (From::kHalves) asm volatile("" : "+v"(k_first), "+v"(v_first));
       floatx4 s[NQ][2];
       // two subtiles in turn: 2 NQ accumulators, each product a step behind its last
 #pragma unroll
@@ -188,7 +196,7 @@ __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, c
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
           const bf16x8 kf =
-              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4v *>(kb + ka[e % KA] + e / KA * 128 + (32 * h + 16 * sb) * D));
+              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4v *>(kb + k_at(e % KA) + e / KA * 128 + (32 * h + 16 * sb) * D));
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
             if (e == 0) s[n][sb] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -197,7 +205,8 @@ __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, c
         }
       // V's operands while the scores become weights
       bf16x8 vf[DT];
-      read_v(vb, h, vf);
+      constexpr int kEarly = From::kHalves ? DT / 2 : DT;
+      read_v(vb, h, vf, Range<0, kEarly>());
       float top[NQ];
       bool over = false;
 #pragma unroll
@@ -222,21 +231,34 @@ __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, c
           for (int d = 0; d < DT; ++d) o[n][d] *= al;
         }
       }
-      bf16x8 pb[NQ];
+      bf16x8 pb[NQ], rest[From::kHalves ? NQ : 1];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const float base = m[n] == -INFINITY ? 0.0f : m[n] * sc;  // a row that sees nothing yet
         float x[8], sum = 0.0f;
-        uint32_t v[4];
+        uint32_t v[4], r[4];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e >> 2][e & 3], sc, -base));
           sum += x[e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (From::kHalves) {
+            const uint2 w = two_halves(x[2 * e], x[2 * e + 1]);
+            v[e] = w.x;
+            r[e] = w.y;
+          } else {
+            v[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+          }
+        }
+        if constexpr (From::kHalves) rest[n] = __builtin_bit_cast(bf16x8, make_uint4(r[0], r[1], r[2], r[3]));
         pb[n] = __builtin_bit_cast(bf16x8, make_uint4(v[0], v[1], v[2], v[3]));
         l[n] += sum;
+      }
+      if constexpr (From::kHalves) {
+        asm volatile("" ::: "memory");  // not before the weights
+        read_v(vb, h, vf, Range<kEarly, DT>());
       }
       if constexpr (ragged.value) {
         if (odd) {
@@ -270,9 +292,18 @@ __device__ __forceinline__ void attn_part(const Args &args, const AttnPlan &p, c
         }
       }
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int c = 0; c < DT; c += kEarly) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf[d], pb[n]);
+        for (int d = c; d < c + kEarly; ++d)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf[d], pb[n]);
+        if constexpr (From::kHalves) {
+#pragma unroll
+          for (int d = c; d < c + kEarly; ++d)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) mma_bf16(o[n][d], vf[d], rest[n]);
+        }
+      }
     }
   };
   if constexpr (From::kLands) {

@@ -127,7 +127,7 @@ template <int D, int TK, bool NT> struct MemoryToLds {
       for (int i = 0; i < LOADS; i += 4) load_lds16<NT>({v_load(i), v_load(i + 1), v_load(i + 2), v_load(i + 3)});
     }
   }
-  static constexpr bool kLands = false;
+  static constexpr bool kLands = false, kHalves = false;
 };
 
 // NQP, NQO: row tiles of a wave for the prefix (rows of all requests) and for a

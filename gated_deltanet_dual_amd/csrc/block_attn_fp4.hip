@@ -13,13 +13,12 @@
 // their products to 2^-14 of the largest only: scores off by 5e-6 of themselves where bf16
 // products are off by 1e-8.)
 //
-// Beside bf16 values the second product takes its weights in bf16.  Few rows give them in two
-// halves (two_halves) and a product for each: outputs are off by their own rounding, 1.66e-3 of
-// themselves in the mean, where weights rounded once make 2.29e-3, for a little time: 256
-// requests over their own keys 28.6 and 29.8 us, one token over 131072 keys 21.3 and 22.0, 5
-// rows of narrow heads 24.1 and 26.5.  Many rows give them rounded once, half a step or 2^-8 of
-// a weight at most, as over bf16: two halves took 138 us for 103 over a shared prefix, 45 for 42
-// at d = 256.  The sum l takes the weights as they are in both forms.
+// Beside bf16 values the second product takes its weights in bf16: in two halves (two_halves), a
+// product for each, so that outputs are off by their own rounding, 1.66e-3 of themselves in the
+// mean, where weights rounded once make 2.29e-3.  It costs 256 requests over their own keys 28.6
+// and 29.9 us, one token over 131072 keys 21.2 and 22.0, 5 rows of narrow heads 24.3 and 26.5, a
+// shared prefix, whose 32 more matrix instructions a tile and 160 of the vector units find little
+// to run beside, 104 and 122, and 56 rows at d = 256 41 and 43.6.
 //
 // Few rows (part_fp4): 4 bits make the operands small enough to need no LDS.  A lane loads
 // 32 codes of one key as 16 bytes, which are its share of the first product's operand (each
@@ -413,7 +412,7 @@ __device__ __forceinline__ void part_fp4(const BlockAttnFp4Args &b, const AttnPl
 // has one subtile of K and of V; TK = 32: waves 0, 1 K, 2, 3 V.
 template <int D, int TK> struct CodesToLds {
   static constexpr int SUBS = TK / 16, W = D / 32;  // words of codes of a lane's row, pieces in LDS
-  static constexpr bool kLands = true;
+  static constexpr bool kLands = true, kHalves = true;
   const BlockAttnFp4Args &b;
   u16 *kt, *vt;
   int shift, lane, wave, sub;
@@ -458,13 +457,14 @@ template <int D, int TK> struct CodesToLds {
   }
   __device__ __forceinline__ void put(const Codes &x, u16 *tile, bool value) const {
     const int row = row_of(lane), q = quarter_of(lane);
-    u16 *to = tile + (sub * 16 + row) * D;
     const bool turn = D == 64 ? row & 1 : value && (q & 1);
     const int piece = (value ? v_piece<D>(row, W * q) : k_piece<D>(row, W * q)) ^ (D == 256 ? 4 * (q & 1) : 0) ^ (turn ? 1 : 0);
+    int to = (sub * 16 + row) * D + piece * 8;
+    asm volatile("" : "+v"(to));  // formed here: the four places kept in registers throughout cost spills
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const uint32_t mine = x.c[i], other = x.c[i ^ 1], c = turn ? other : mine, s = x.s[i / 4] << 23;
-      *reinterpret_cast<uint4 *>(to + (piece ^ i) * 8) =
+      *reinterpret_cast<uint4 *>(tile + (to ^ (8 * i))) =
           make_uint4(fp4_pair<0>(c, s), fp4_pair<1>(c, s), fp4_pair<2>(c, s), fp4_pair<3>(c, s));
     }
   }

@@ -472,20 +472,24 @@ def test_refusals(g):
         ok(v_cache=(odd, vc[1]))
 
 
-FEW_ROWS = [(1, 1, 4, 4, 128, 64, [700], 0), (3, 4, 2, 4, 128, 16, [1, 33, 130], 77), (4, 1, 1, 8, 256, 32, [15, 16, 31, 32], 1),
-            (2, 16, 1, 2, 64, 32, [16, 47], 40), (5, 3, 1, 5, 64, 128, [3, 64, 127, 128, 129], 129), (1, 1, 1, 2, 64, 16, [4500], 0),
-            (1, 1, 1, 4, 128, 16, [70], 4200), (3, 2, 2, 2, 128, 16, [0, 33, 70], 4100), (2, 8, 1, 4, 128, 16, [8, 90], 20)]
+FEW_AND_MANY_ROWS = [
+    (1, 1, 4, 4, 128, 64, [700], 0), (3, 4, 2, 4, 128, 16, [1, 33, 130], 77), (4, 1, 1, 8, 256, 32, [15, 16, 31, 32], 1),
+    (2, 16, 1, 2, 64, 32, [16, 47], 40), (5, 3, 1, 5, 64, 128, [3, 64, 127, 128, 129], 129), (1, 1, 1, 2, 64, 16, [4500], 0),
+    (1, 1, 1, 4, 128, 16, [70], 4200), (3, 2, 2, 2, 128, 16, [0, 33, 70], 4100), (2, 8, 1, 4, 128, 16, [8, 90], 20),
+    # tiles that four waves share: of own keys, with a prefix before them, of a prefix alone
+    (2, 16, 1, 8, 64, 32, [16, 47], 40), (2, 20, 1, 8, 128, 32, [20, 131], 70), (2, 9, 1, 8, 256, 16, [9, 90], 31),
+    (2, 32, 2, 2, 128, 32, [32, 190], 0), (3, 9, 1, 5, 64, 32, [20, 0, 131], 4500), (140, 4, 2, 2, 128, 16, [(i * 29) % 70 for i in range(140)], 4300),
+    (50, 2, 1, 8, 256, 16, [(i * 29) % 70 for i in range(50)], 4200), (130, 20, 1, 4, 128, 16, [(i * 29) % 90 for i in range(130)], 77)]
 
 
 @pytest.mark.parametrize("causal", [False, True])
-@pytest.mark.parametrize("i", range(len(FEW_ROWS)))
-def test_weights_of_few_rows_keep_16_bits(g, i, causal):
-    """Up to 16 (d = 256) or 32 rows a kv head and request, and not thousands over a prefix: the weights
-    go into the second product in two bf16 halves.  The first is cut, so that up to 2^-7 of a weight
-    is left, the second rounds that by 2^-8 of itself, and 2^-20 are added: 2^-15 + 2^-20 of sum
-    p |v| / sum p in place of 2^-8.  Scores, exponentials and sums as above."""
+@pytest.mark.parametrize("i", range(len(FEW_AND_MANY_ROWS)))
+def test_weights_keep_16_bits(g, i, causal):
+    """The weights go into the second product in two bf16 halves.  The first is cut, so that up to
+    2^-7 of a weight is left, the second rounds that by 2^-8 of itself, and 2^-20 are added: 2^-15 +
+    2^-20 of sum p |v| / sum p in place of 2^-8.  Scores, exponentials and sums as above."""
     import torch
-    R, B, Hk, G, d, page, lens, prefix = FEW_ROWS[i]
+    R, B, Hk, G, d, page, lens, prefix = FEW_AND_MANY_ROWS[i]
     q, kc, vc, bt, sl, pt = make(50 + i, R, B, Hk, G, d, page, lens, prefix)
     o = g.block_attention_fp4(q, kc, vc, bt, sl, prefix_table=pt, prefix_len=prefix, causal=causal)
     ro, _, size = attention64(q, cache_values(*kc), cache_values(*vc), bt, sl, pt, prefix, causal)
