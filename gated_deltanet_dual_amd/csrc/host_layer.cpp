@@ -92,20 +92,20 @@ AttnPlan attn_plan(const BlockAttnArgs &a) {
 namespace {
 // What a key costs a workgroup, in tenths of a nanosecond: alone on its CU, its share of a
 // CU's instructions that several keep busy, and its share of memory's time where no other
-// row group reads it.  Measured: the shared form of two row tiles at d = 128, 4096 keys 106 us
-// alone, 4 x 2048 keys 80 us two a CU; d = 256, one: 2 x 2048 111 us; d = 64, two: 4 x 1024 60
-// us four a CU.  The other form, one row tile at d = 128, 4096 keys a workgroup 43 us with one a
-// CU (2048 keys 28) and 63 with four (40); two tiles 45 (29) and 116 (70); d = 64 36 (24) and 54
-// (36), two 37 (26) and 83 (49); d = 256 2048 keys 33 and 85.
+// row group reads it.  Measured with one workgroup a CU and with two (the shared form) or four
+// of so many keys each: the shared form of two row tiles at d = 128, 4096 keys 122 us and 195
+// (2048 keys 71 and 115), d = 64 88 and 160 (52 and 88), d = 256, one, 2048 keys 87 and 133.  The
+// other form, one row tile at d = 128, 4096 keys 43 us and 63 (2048 28 and 40), two 45 and 116
+// (29 and 70); d = 64 36 and 54 (24 and 36), two 37 and 83 (26 and 49); d = 256 2048 keys 33 and 85.
 struct KeyCost {
   int alone, busy, memory;
 };
 KeyCost key_cost(bool shared, int tiles, int dim) {
   const int memory = dim / 2 - dim / 64;  // 17 / 16 of a byte a channel, at 4.4 TB/s over 256 CUs
   if (shared) {
-    if (dim == 256) return {390, 275, memory};
-    if (dim == 64) return tiles == 2 ? KeyCost{180, 146, memory} : KeyCost{120, 90, memory};
-    return tiles == 2 ? KeyCost{260, 195, memory} : KeyCost{176, 120, memory};
+    if (dim == 256) return {435, 312, memory};
+    if (dim == 64) return tiles == 2 ? KeyCost{225, 190, memory} : KeyCost{150, 117, memory};
+    return tiles == 2 ? KeyCost{295, 234, memory} : KeyCost{200, 144, memory};
   }
   if (dim == 256) return {145, 72, memory};
   if (dim == 64) return tiles == 2 ? KeyCost{75, 50, memory} : KeyCost{57, 27, memory};
@@ -121,8 +121,8 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   const int64_t all_rows = rows * a.num_req;
   const int two = a.dim == 256 ? 1 : 2;
   // Many rows share their tiles.  256 requests x 1024 own keys, 4 heads of 128: 32 rows 42 us
-  // apart and 50 shared, 48 rows 68 and 54; of 64, 32 rows 28 and 33, 128 requests x 64 rows 28
-  // and 21.
+  // apart and 60 shared, 48 rows 68 and 62; of 64, 32 rows 28 and 40, 128 requests x 64 rows 28
+  // and 24.
   f.own_shared = rows > 16 * two;
   // as over bf16: two row tiles a wave where that leaves a workgroup for every CU
   p.own_tiles = f.own_shared ? (rows > 64 && ceil_div(rows, 128) * a.kv_heads * a.num_req >= 256 ? two : 1) : rows > 16 ? 2 : 1;
@@ -145,10 +145,10 @@ AttnPlan attn_fp4_plan(const BlockAttnArgs &a, AttnForms &f) {
   const int64_t together = a.prefix_len > 0 && all_tiles <= part_tiles ? passes(units, a.prefix_len + a.max_seq_len, own.alone, own_each) : INT64_MAX;
 
   // The prefix's too, where the rows of all kv heads are many; 4 of them over 32000 keys: at d =
-  // 128 128 rows 30 us apart and 30 shared, 256 45 and 39, 1024 116 and 94; at d = 64 128 rows 23
-  // and 23, 256 32 and 28; at d = 256 128 rows 55 and 43; one head of 128 256 rows 24 and 27, 512
-  // 30 and 30, of 256 256 rows 34 and 34, 512 49 and 43.
-  const int64_t many = a.dim == 256 ? 256 : 512;
+  // 128 128 rows 31 us apart and 33 shared, 256 45 and 44 (over 8000 keys and 1000 own 28.0 and
+  // 26.6), 512 66 and 67, 1024 117 and 110; at d = 64 256 rows 32 and 33, 512 51 and 47; at d = 256
+  // 128 rows 55 and 45; one head of 256 256 rows 34 and 36, 512 48 and 45.
+  const int64_t many = a.dim == 128 ? 768 : a.dim == 64 ? 1024 : 384;
   f.prefix_shared = f.own_shared || (a.prefix_len > 0 && all_rows * a.kv_heads > many);
   p.prefix_tiles = a.prefix_len == 0 ? p.own_tiles : f.prefix_shared ? two : all_rows > 16 ? two : 1;
   if (!f.prefix_shared && p.prefix_tiles < p.own_tiles) p.prefix_tiles = p.own_tiles;
