@@ -15,10 +15,9 @@
 //
 // Beside bf16 values the second product takes its weights in bf16: in two halves (two_halves), a
 // product for each, so that outputs are off by their own rounding, 1.66e-3 of themselves in the
-// mean, where weights rounded once make 2.29e-3.  It costs 256 requests over their own keys 28.6
-// and 29.9 us, one token over 131072 keys 21.2 and 22.0, 5 rows of narrow heads 24.3 and 26.5, a
-// shared prefix, whose 32 more matrix instructions a tile and 160 of the vector units find little
-// to run beside, 104 and 122, and 56 rows at d = 256 41 and 43.6.
+// mean, where weights rounded once make 2.29e-3.  It is not for nothing: 256 requests over their own
+// keys take 29.9 us for 28.6, one token over 131072 keys 22.0 for 21.3, 5 rows of narrow heads
+// 26.5 for 24.2, a shared prefix 125 for 104 and 56 rows at d = 256 43.7 for 41.3.
 //
 // Few rows (part_fp4): 4 bits make the operands small enough to need no LDS.  A lane loads
 // 32 codes of one key as 16 bytes, which are its share of the first product's operand (each
@@ -29,15 +28,18 @@
 // So the waves of a workgroup share nothing while they pass the keys: each takes every
 // fourth tile of 32 keys, one tile in registers while the next one is under way, and the
 // four join at the end.  Memory bounds it: 256 requests x 4 tokens, 4 heads of 128, up to
-// 1024 keys 28.3 us, 4.2 TB/s, of which the loads alone take 26.8; one token over 131072
-// keys 15.9 us, 4.6 TB/s, and 5.4 to join.
+// 1024 keys 30 us, 3.9 TB/s, of which the loads alone take 26.8; one token over 131072
+// keys 17 us, 4.3 TB/s, and 5.4 to join.
 //
 // Many rows (CodesToLds): what a wave converts there would be converted again by every other
 // wave with rows of the same keys; so four waves convert a tile once, into LDS, and each passes
 // it with 16 or 32 rows of its own, by the loop of attn_tiles.h.  256 requests x 4 over a
-// prefix of 8192: 103 us with the requests' own keys beside it, 740 TFLOP/s; LDS, vector and
-// matrix instructions each take some 2000 cycles of a tile of 64 keys and 128 rows.  As few
-// rows it took 142.
+// prefix of 8192: 125 us with the requests' own keys beside it, 600 TFLOP/s of the two products
+// that the formula names.  No unit is full: of 280 thousand cycles the vector units are active
+// in 53 %, the matrix units in 39 %, LDS in 19 %; but the two waves of a SIMD do not run the
+// one beside the other (53 and 39 are nearly all), and a wave waits a third of its time for its
+// turn and a quarter for loads and its fellows.  More than two do not fit: 254 registers at d =
+// 128 with two row tiles.  As few rows such a prefix takes longer (attn_fp4_plan).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -427,7 +429,7 @@ template <int D, int TK> struct CodesToLds {
   // them (d = 64, 128) or two; so the eight lanes are half quarters of four rows, every other
   // lane has its halves the other way round (d = 256) and of values, where only even places
   // change with the row, each two words.  37 requests x 7 x 16 heads of 256 over 2500 + 777
-  // keys: 43 us with those conflicts, half of the LDS' cycles, 37 without.
+  // keys, weights rounded once: 43 us with those conflicts, half of the LDS' cycles, 37 without.
   __device__ __forceinline__ static int row_of(int lane) { return D == 64 ? lane >> 2 : (lane >> 1 & 3) | (lane >> 4 << 2); }
   __device__ __forceinline__ static int quarter_of(int lane) { return D == 64 ? lane & 3 : (lane & 1) | (lane >> 2 & 2); }
   __device__ __forceinline__ void fetch(Codes &x, const void *codes, const uint8_t *scales, int64_t ph, int row) const {

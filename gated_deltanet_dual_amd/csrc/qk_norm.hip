@@ -14,10 +14,13 @@
 // them would wait for them) while a row is finished, so each half of the loop has its
 // own; weights and coefficients come from LDS, for a load from memory that is waited for
 // waits for all before it as well.  32768 tokens of 16 query and 4 key heads of 128 in
-// bf16: forward 62 us (5.4 TB/s; 92 with loads and weights in turn), reverse 119 us
-// (4.2 TB/s; 167), where its instructions, some 35 a channel, weigh as much.  Short
-// vectors cost: heads of 80, 50 channels turned as halves, 71 and 106 us.  Below some
-// 2000 tokens the chain of a workgroup's loads bounds it: 1024 tokens 7.1 and 15 us.
+// bf16, the kernels alone: forward 58 us (5.7 TB/s of x and y; 92 with loads and weights
+// in turn), reverse 106 us (4.8 TB/s of x, dy and dx; 167), where its instructions, some 35
+// a channel, weigh as much, and 4.2 us for the weights' partial rows.  fp32, 16384 tokens:
+// 56 and 106 us.  Short vectors cost: heads of 80 in bf16, 50 channels turned as halves, 70
+// and 105 us (3.0 TB/s).  Below some 2000 tokens the chain of a workgroup's loads bounds it:
+// 1024 tokens 5.3 and 9.5 us.  Into a cache of the rows' own type 16384 tokens take 44 us in
+// bf16 and 81 in fp32 (4.5 and 5.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "fast_div.h"
@@ -424,8 +427,9 @@ __device__ __forceinline__ void forward_rows(const QkNormArgs &a, const QkNormPl
 // value next to the border of two codes, half a step apart, goes to the right one, which 32
 // bits would miss once in some 10^5 values.  They pass through LDS, a wave's own part of it,
 // where groups of 32 channels lie together whatever pairs were turned.  16384 tokens of 16
-// query, 4 key and 4 value heads of 128: 50 to 53 us (2.9 TB/s), bound by instructions: the
-// queries and values alone are 38, the keys and values 25, and waves of both share the SIMDs.
+// query, 4 key and 4 value heads of 128: 50 us (3.7 TB/s), bound by instructions: the
+// queries and values alone are 38, the keys and values 25, and waves of both share the SIMDs;
+// in fp32, with twice the bytes a row, 72 us (5.0 TB/s).
 // (fp32 first, its errors bounded, and 64 bits for the waves that have a value near a border,
 // one in 50: 66 us, for most workgroups have such a wave and wait for it.)
 __device__ __forceinline__ void wave_lds_ready() {
@@ -680,8 +684,8 @@ __global__ __launch_bounds__(256) void qk_norm_rotary_bwd_kernel(QkNormArgs a, Q
 }
 
 // Rows of a cache in 4 bits as bf16 or fp32: 8 channels a thread.  16512 rows of 4 heads of
-// 128, keys and values: 12.4 us, 3.8 TB/s, of which a launch's start and end are a third; 1152
-// rows 3.3 us.
+// 128, keys and values: 12.5 us, 3.8 TB/s, of which a launch's start and end are a third; 1152
+// rows 3.3 us; in fp32 18.9 and 4.2 us.
 template <typename IO>
 __global__ __launch_bounds__(256) void cache_fp4_rows_kernel(Cache4Rows a, FastDiv chunks, FastDiv row_items) {
   const int per_row = a.heads * (a.dim / 8);
