@@ -21,7 +21,7 @@ __device__ __forceinline__ float xmax32(float x) {
 
 // Two weights of at least 0 in two bf16 halves each, the first ones in x: cut, so that up to
 // 2^-7 of a weight is left, and that rounded, off by 2^-15 of the weight at most.  2^-20 of it
-// are added, so that the second half of a weight that is not 0 is not 0 either: a value of
+// are added, so that the second half of a weight above 2^-113 is above 0 as well: a value of
 // infinity times both halves stays one.
 __device__ __forceinline__ uint2 two_halves(float x, float y) {
   const uint32_t first = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
